@@ -15,7 +15,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdgfp8.so")
-SOURCES = ["api.hip", "gemm.hip", "quantize.hip"]
+SOURCES = ["api.hip", "gemm.hip", "quantize.hip", "api_ops.hip", "router.hip", "moe.hip", "lora.hip"]
 ARCH = "gfx950"
 
 
@@ -36,7 +36,7 @@ def compile_flags() -> list[str]:
     ]
 
 
-def build(verbose: bool = False, jobs: int = 3) -> str:
+def build(verbose: bool = False, jobs: int = 6) -> str:
     """Compile every source to an object in parallel, then link the shared
     library; always recompiles."""
     objdir = os.path.join(HERE, "_build")

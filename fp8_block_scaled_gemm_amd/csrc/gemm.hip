@@ -136,28 +136,6 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-__device__ __forceinline__ v4f mfma_block(const v8i& b, const v8i& a) {
-    const v4f zero = {0.f, 0.f, 0.f, 0.f};
-    // format 0 = e4m3 for both operands; zero scale operands select the
-    // unscaled instruction
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, zero, 0, 0, 0, 0, 0, 0);
-}
-
-// acc + 2^(eb-127) * 2^(ea-127) * (B_blk A_blk^T) in one instruction.  Each
-// lane passes one E8M0 byte per operand in bits 0-7 (opsel 0): operand 0's
-// (eb) applies to B row (lane & 15) of the sub-tile, operand 1's (ea) to A
-// row (lane & 15), each for the 32-wide K group (lane >> 4); a block's four
-// groups share one scale, so every lane passes its row's block scale.
-__device__ __forceinline__ v4f mfma_block_e8(const v8i& b, const v8i& a, const v4f& c, int eb,
-                                              int ea) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, 0, 0, 0, eb, 0, ea);
-}
-
-__device__ __forceinline__ v8i join(const v4u& lo, const v4u& hi) {
-    return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-               (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-}
-
 // Logical tile of workgroup `b` among `tiles`: XCD x (= b % 8) receives the
 // contiguous range [x*per, (x+1)*per); -1 for the padding slots.
 __device__ __forceinline__ int xcd_tile(int b, int tiles) {
@@ -277,7 +255,7 @@ __device__ __forceinline__ bool decode_tile(int b, int m_blocks, int n_blocks, i
     const int in_span = tile % span;
     ti.m0 = (first_m + in_span % gm) * T::BM;
     ti.n0 = (in_span / gm) * T::BN;
-    if (kForm == Form::Dense || kForm == Form::DenseAcc) {
+    if (kForm == Form::Dense || kForm == Form::DenseAcc || kForm == Form::DenseLora) {
         ti.valid = (int)min<int64_t>(T::BM, rows - ti.m0);
         ti.arow0 = ti.m0;
     } else {
@@ -289,9 +267,81 @@ __device__ __forceinline__ bool decode_tile(int b, int m_blocks, int n_blocks, i
     return true;
 }
 
+// The adapter term of a tile (DenseLora): the wave walks the distinct adapters
+// of its rows; for each, a lane multiplies its row's rank-R vector by 16-row
+// tiles of that adapter's second matrix with bf16 MFMA and keeps the product
+// where the row is the adapter's own (a select, not a zeroed operand, so that
+// an infinity or NaN in one request's adapter stays in that request's rows).
+// The vector is fp32; it enters as the sum of two bf16 parts, which leaves an
+// error of 2^-17 of it, far below the final rounding to bf16.
+template <class T>
+__device__ __forceinline__ void add_lora(v4f (&acc)[T::TM][T::TN], const LoraTail& lora, int lane,
+                                         int wm, int wcol, const TileInfo& ti, int64_t rows,
+                                         int64_t N) {
+    typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+    const int lr = lane & 15, lg = lane >> 4;
+    int id[T::TM];
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) {
+        const int row = 16 * (T::WAVES_M * i + wm) + lr;
+        id[i] = row < ti.valid ? lora.ids[ti.arow0 + row] : -1;
+        if (id[i] < 0 || id[i] >= lora.L) id[i] = 0x7fffffff;
+    }
+    for (int after = -1;;) {
+        int cur = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i)
+            if (id[i] > after) cur = min(cur, id[i]);
+#pragma unroll
+        for (int d = 8; d >= 1; d >>= 1) cur = min(cur, __shfl_xor(cur, d, 64));
+        cur = __builtin_amdgcn_readfirstlane(cur);
+        if (cur == 0x7fffffff) return;
+        after = cur;
+        const uint16_t* const b = lora.lora_b + ((int64_t)cur * N + ti.n0 + wcol) * lora.R;
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i) {
+            if (__ballot(id[i] == cur) == 0) continue;
+            const int64_t row = ti.arow0 + min(16 * (T::WAVES_M * i + wm) + lr, ti.valid - 1);
+            v4f sum[T::TN];
+#pragma unroll
+            for (int j = 0; j < T::TN; ++j) sum[j] = v4f{0.f, 0.f, 0.f, 0.f};
+            for (int k0 = 0; k0 < lora.R; k0 += 32) {
+                const int k = k0 + 8 * lg;
+                float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (k < lora.R && id[i] == cur) {
+                    for (int p = 0; p < lora.parts; ++p) {
+                        const float* v = lora.low + ((int64_t)p * rows + row) * lora.R + k;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) f[q] += v[q];
+                    }
+                }
+                v8bf hi, lo;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    hi[q] = (__bf16)f[q];
+                    lo[q] = (__bf16)(f[q] - (float)hi[q]);
+                }
+#pragma unroll
+                for (int j = 0; j < T::TN; ++j) {
+                    v4u raw = {0u, 0u, 0u, 0u};
+                    if (k < lora.R && ti.n0 + wcol + 16 * j + lr < N)
+                        raw = *reinterpret_cast<const v4u*>(b + (int64_t)(16 * j + lr) * lora.R + k);
+                    const v8bf bf = __builtin_bit_cast(v8bf, raw);
+                    sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf, hi, sum[j], 0, 0, 0);
+                    sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf, lo, sum[j], 0, 0, 0);
+                }
+            }
+            if (id[i] == cur) {
+#pragma unroll
+                for (int j = 0; j < T::TN; ++j) acc[i][j] += sum[j];
+            }
+        }
+    }
+}
+
 // Epilogue of a tile: the lane holds tile row 16 (WAVES_M i + wm) + lr and
 // columns wcol + 16j + 4lg .. +3 of acc[i][j].  DenseAcc adds the fp32 addend
-// C first; then the tile is rounded to bf16, staged in LDS (which every wave
+// C first (DenseLora has added its term); then the tile is rounded to bf16, staged in LDS (which every wave
 // must be done with) and stored row-predicated.
 template <class T, Form kForm>
 __device__ __forceinline__ void store_tile(v4f (&acc)[T::TM][T::TN], uint8_t* smem, int tid, int wm,
@@ -384,12 +434,17 @@ __device__ __forceinline__ void store_tile(v4f (&acc)[T::TM][T::TN], uint8_t* sm
 // block's partial promoted as acc += (sa sb) P.  With kE8: E8M0 exponent
 // bytes, rows padded to a multiple of 4 bytes ([rows][SP], [groups][NB][SP]),
 // applied by the scaled MFMA itself, which accumulates straight into acc.
+// What only DenseLora passes.
+struct NoTail {};
+template <Form kForm>
+using TailOf = typename std::conditional<kForm == Form::DenseLora, LoraTail, NoTail>::type;
+
 template <class T, Form kForm, bool kE8, bool kMixed = false>
 __global__ __launch_bounds__(T::kThreads, 2) void gemm_kernel(
     const uint8_t* __restrict__ A, const void* __restrict__ sa_v, const uint8_t* __restrict__ B,
     const void* __restrict__ sb_v, uint16_t* __restrict__ D, const int32_t* __restrict__ aux,
     const float* __restrict__ C, int64_t rows, int64_t N, int64_t K, int64_t G, int m_blocks,
-    int n_blocks) {
+    int n_blocks, TailOf<kForm> tail) {
     using ScaleT = typename std::conditional<kE8, uint8_t, float>::type;
     const ScaleT* __restrict__ sa = static_cast<const ScaleT*>(sa_v);
     const ScaleT* __restrict__ sb = static_cast<const ScaleT*>(sb_v);
@@ -633,6 +688,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void gemm_kernel(
         // ---- epilogue
         wait_vmcnt<0>();  // the empty loads of the last steps have retired
         lds_barrier();
+        if constexpr (kForm == Form::DenseLora) add_lora<T>(acc, tail, lane, wm, wcol, ti, rows, N);
         store_tile<T, kForm>(acc, smem, tid, wm, wcol, lr, lg, ti, C, D, N);
         if constexpr (!kMixed) {
             break;
@@ -666,9 +722,11 @@ static dg_status launch_tiled(const GemmArgs& a, hipStream_t stream) {
     // and a tile's rows of fp32 C
     if (kForm == Form::DenseAcc && (int64_t)T::BM * a.N * 4 >= (int64_t(1) << 32))
         return DG_ERR_SHAPE;
+    TailOf<kForm> tail;
+    if constexpr (kForm == Form::DenseLora) tail = a.lora;
     hipLaunchKernelGGL((gemm_kernel<T, kForm, kE8>), dim3((unsigned)grid), dim3(T::kThreads), 0, stream,
                        a.A, a.sa, a.B, a.sb, a.D, a.aux, a.C, a.rows, a.N, a.K, a.G, (int)m_blocks,
-                       (int)n_blocks);
+                       (int)n_blocks, tail);
     if constexpr (kForm == Form::Contiguous) {
         // Blocks whose rows carry more than one valid id: one workgroup per
         // 128-row block, which exits at once unless its block is mixed.  The
@@ -676,7 +734,7 @@ static dg_status launch_tiled(const GemmArgs& a, hipStream_t stream) {
         if (launched() != DG_OK) return DG_ERR_HIP;
         hipLaunchKernelGGL((gemm_kernel<T, kForm, kE8, true>), dim3((unsigned)m_blocks), dim3(T::kThreads),
                            0, stream, a.A, a.sa, a.B, a.sb, a.D, a.aux, a.C, a.rows, a.N, a.K, a.G,
-                           (int)m_blocks, (int)n_blocks);
+                           (int)m_blocks, (int)n_blocks, tail);
     }
     return launched();
 }
@@ -798,6 +856,7 @@ dg_status launch_gemm(Form form, const GemmArgs& a, hipStream_t stream) {
             case Form::Dense: return launch_dense<Form::Dense, true>(a, stream);
             case Form::Contiguous: return launch_tiled<TileRows128, Form::Contiguous, true>(a, stream);
             case Form::Masked: return launch_tiled<TileLargeT, Form::Masked, true>(a, stream);
+            case Form::DenseLora: return launch_dense<Form::DenseLora, true>(a, stream);
             default: return DG_ERR_UNSUPPORTED;
         }
     }
@@ -806,6 +865,7 @@ dg_status launch_gemm(Form form, const GemmArgs& a, hipStream_t stream) {
         case Form::DenseAcc: return launch_dense<Form::DenseAcc, false>(a, stream);
         case Form::Contiguous: return launch_tiled<TileRows128, Form::Contiguous, false>(a, stream);
         case Form::Masked: return launch_tiled<TileMasked, Form::Masked, false>(a, stream);
+        case Form::DenseLora: return launch_dense<Form::DenseLora, false>(a, stream);
     }
     return DG_ERR_UNSUPPORTED;
 }

@@ -16,7 +16,16 @@ namespace dg {
 inline dg_status launched() { return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP; }
 
 // DenseAcc: dense routing, D = bf16(C + A B^T scaled) with C fp32 [rows][N]
-enum class Form : int { Dense = 0, Contiguous = 1, Masked = 2, DenseAcc = 3 };
+// DenseLora: dense routing, D = bf16(A B^T scaled + each row's adapter term)
+enum class Form : int { Dense = 0, Contiguous = 1, Masked = 2, DenseAcc = 3, DenseLora = 4 };
+
+// DenseLora: row m adds low[m] lora_b[ids[m]]^T when ids[m] is in [0, L)
+struct LoraTail {
+    const float* low;        // [parts][rows][R], summed over parts
+    const uint16_t* lora_b;  // bf16 [L][N][R]
+    const int32_t* ids;      // [rows]
+    int parts, L, R;         // R a multiple of 8
+};
 
 struct GemmArgs {
     const uint8_t* A;     // e4m3 codes, K-contiguous rows
@@ -29,6 +38,7 @@ struct GemmArgs {
     int64_t N, K, G;
     const float* C;       // DenseAcc: fp32 [rows][N] added before the bf16 rounding
     bool e8m0 = false;    // scales are E8M0 exponent bytes, SP = K/128 rounded up to 4
+    LoraTail lora = {};   // DenseLora
 };
 
 dg_status launch_gemm(Form form, const GemmArgs& args, hipStream_t stream);
