@@ -1,6 +1,6 @@
 // Device helpers shared by the gfx950 kernels of this library: vector types
-// for MFMA operands and 16-byte accesses, the FP8 matrix instruction and the
-// e4m3 conversion.
+// for MFMA operands and 16-byte accesses, direct loads to LDS with their
+// waits, the FP8 matrix instruction and the e4m3 conversion.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -29,6 +29,66 @@ __device__ __forceinline__ uint32_t e4m3x4_hw(float a, float b, float c, float d
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
     return (uint32_t)w;
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+    return static_cast<uint32_t>(reinterpret_cast<size_t>((lds_ptr_t)p));
+}
+
+// Raw buffer resource (gfx9 V#): `bytes` readable from `base`, stride 0.
+// Loads at offsets past `bytes` return zero and touch no memory.
+__device__ __forceinline__ v4u buffer_rsrc(const void* base, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    v4u r;
+    r[0] = (uint32_t)a;
+    r[1] = (uint32_t)(a >> 32) & 0xffffu;
+    r[2] = bytes;
+    r[3] = 0x00020000u;
+    return r;
+}
+
+// One wave-wide direct load: lane l's bytes at buffer offset `off` land at
+// dst + size*l in LDS (dst is wave-uniform, passed in M0).  Written as inline
+// assembly on purpose: the compiler then does not track these LDS writes and
+// cannot put a wait for the stage being filled in front of reads of the
+// other stage (its alias tracking for such loads depends on control flow).
+// The kernel orders them itself: every LDS read of a buffer is separated
+// from the loads that refill it by a barrier (a compiler memory barrier as
+// well), and a buffer is read only after the explicit vmcnt wait and barrier
+// that publish it.  So the statements carry no memory clobber, and the
+// compiler may still schedule unrelated LDS reads and arithmetic across them.
+__device__ __forceinline__ void load_lds_16(const v4u& rsrc, uint32_t off, void* dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(lds_addr(dst)), "v"(off), "s"(rsrc) : "m0");
+}
+__device__ __forceinline__ void load_lds_4(const v4u& rsrc, uint32_t off, void* dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :: "s"(lds_addr(dst)), "v"(off), "s"(rsrc) : "m0");
+}
+
+// s_waitcnt on the vector-memory counter only (gfx9 encoding: vmcnt bits
+// [3:0] and [15:14], expcnt and lgkmcnt left at their no-wait maxima).
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+// The same with lgkmcnt = 0: every LDS access this wave issued has completed.
+template <int N>
+__device__ __forceinline__ void wait_vmcnt_lgkm0() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+}
+
+// Workgroup barrier that is also a compiler barrier for memory accesses, but
+// (unlike __syncthreads) waits for nothing: the kernel has already waited for
+// exactly the loads the barrier publishes.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // The partial product of one 128-wide K block of a 16x16 sub-tile.

@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "fewrow.h"
+#include "quantize_common.h"
 
 namespace dg {
 
@@ -29,124 +30,240 @@ struct MoeJob {
 
 // Workspace layout, in bytes from its start.
 struct MoeLayout {
-    int64_t units, order, hidden, codes, scales, total;
+    int64_t units, order, codes, scales, total;
     MoeLayout(int64_t T, int64_t k, int64_t E, int64_t I) {
         const int64_t P = T * k, U = std::min(P, E);
         auto up = [](int64_t v) { return (v + 255) & ~int64_t(255); };
         units = 0;
         order = units + up(U * sizeof(MoeUnit));
-        hidden = order + up(P * 4);
-        codes = hidden + up(P * I * 4);
+        codes = order + up(P * 4);
         scales = codes + up(P * I);
         total = scales + up(P * ((I / 128 + 3) & ~int64_t(3)) * 4);
     }
 };
 
-// Rows of one unit, found by each wave for itself from the ids: the pairs of
-// the unit's expert in order, into `list` if given.  count is 0 when the unit
-// has no expert here, or (units numbered by pair) an earlier pair named it.
+// Rows of one unit, found by the whole workgroup from the ids: the pairs of
+// the unit's expert in order, into `list`.  count is 0 when the unit has no
+// expert here, or (units numbered by pair) an earlier pair named it.  Each
+// wave scans a share of the ids, copied to LDS first so that no step waits for
+// memory.  `ids_lds` holds P ids and may be reused once this returns.
+template <int W>
 __device__ __forceinline__ MoeUnit find_unit(const int32_t* __restrict__ ids, int P, int E, int unit,
-                                             bool by_pair, int lane, uint16_t* list) {
-    MoeUnit u;
-    u.e = by_pair ? ids[unit] : unit;
-    u.start = u.count = u.pad = 0;
+                                             bool by_pair, int* ids_lds, uint16_t* list) {
+    __shared__ int found[W][3];  // pairs of the expert, pairs of lower experts, first pair
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int i = threadIdx.x; i < P; i += 64 * W) ids_lds[i] = ids[i];
+    __syncthreads();
+    MoeUnit u = {by_pair ? ids_lds[unit] : unit, 0, 0, 0};
+    u.e = __builtin_amdgcn_readfirstlane(u.e);
     if (u.e < 0 || u.e >= E) return u;
-    for (int base = 0; base < P; base += 64) {
-        const int q = base + lane;
-        const int id = q < P ? ids[q] : -1;
+    const int per = (P + 64 * W - 1) / (64 * W) * 64, q0 = wave * per, q1 = min(q0 + per, P);
+    int count = 0, lower = 0, first = P;
+    for (int base = q0; base < q1; base += 64) {
+        const int id = base + lane < q1 ? ids_lds[base + lane] : -1;
         const uint64_t same = __ballot(id == u.e);
-        u.start += __popcll(__ballot(id >= 0 && id < u.e));
-        if (by_pair && u.count == 0 && same != 0 && base + __builtin_ctzll(same) < unit) return u;
-        if (list && id == u.e)
-            list[u.count + __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32),
-                                                     __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0))] =
-                (uint16_t)q;
-        u.count += __popcll(same);
+        if (count == 0 && same != 0) first = base + __builtin_ctzll(same);
+        count += __popcll(same);
+        lower += __popcll(__ballot(id >= 0 && id < u.e));
     }
+    if (lane == 0) {
+        found[wave][0] = count;
+        found[wave][1] = lower;
+        found[wave][2] = first;
+    }
+    __syncthreads();
+    int before = 0, whole = 0;
+    first = P;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w == wave) before = whole;
+        whole += found[w][0];
+        u.start += found[w][1];
+        first = min(first, found[w][2]);
+    }
+    if (by_pair && first != unit) return u;
+    u.count = __builtin_amdgcn_readfirstlane(whole);
+    u.start = __builtin_amdgcn_readfirstlane(u.start);
+    for (int base = q0; base < q1; base += 64) {
+        const int id = base + lane < q1 ? ids_lds[base + lane] : -1;
+        const uint64_t same = __ballot(id == u.e);
+        if (id == u.e)
+            list[before + __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32),
+                                                    __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0))] =
+                (uint16_t)(base + lane);
+        before += __popcll(same);
+    }
+    __syncthreads();
     return u;
 }
 
-// First product: hidden[row] = silu(gate) * up, fp32.  A workgroup's four
-// waves take 16 hidden columns each of one unit; a wave multiplies the gate
-// and the up rows of the weights by the same activations.
-template <int R, bool kE8>
-__global__ __launch_bounds__(256) void moe_gate_up_kernel(
+// First product: silu(gate) * up, quantized per 128 hidden columns.  A
+// workgroup's eight waves take 16 hidden columns each of one 128-column block
+// of one unit; a wave multiplies its gate and its up rows of the weights by
+// the unit's activations, up to 16 R rows at a time.
+//
+// A K block of everything the workgroup multiplies (256 weight rows, the
+// activation rows, their scales) is one stage of a ring in LDS, filled by
+// direct loads that take whole 128-byte lines, eight consecutive lanes a
+// line: fragment-shaped loads straight to registers touch 16 lines for 16
+// bytes each and are bound by the cache's tag rate (R = 4: 3.3 TB/s).  Each
+// stage costs one barrier.  The stages ahead, D - 1 of them, keep the weights
+// of D - 1 K blocks, 32 KB each, in flight per CU.
+//
+// The sums go through the bf16 matrix instruction (see multiply_exact): the
+// FP8 one would move about one code in 600 of the quantized result.
+constexpr int kGateWaves = 8;
+
+template <int R>
+struct GateStage {
+    uint8_t b[kGateWaves * 32 * 128];  // wave w: 16 gate rows, 16 up rows
+    uint8_t a[16 * R * 128];
+    float sa[64];
+    float sb[64];  // [0] gate, [1] up
+};
+
+template <int R, int D, bool kE8>
+__global__ __launch_bounds__(64 * kGateWaves) void moe_gate_up_kernel(
     const uint8_t* __restrict__ x, const void* __restrict__ sx_v, const int32_t* __restrict__ ids,
     const uint8_t* __restrict__ w13, const void* __restrict__ s13_v, MoeUnit* __restrict__ units,
-    int32_t* __restrict__ order, float* __restrict__ hidden, int P, int k, int E, int H, int I,
-    bool by_pair) {
+    int32_t* __restrict__ order, uint8_t* __restrict__ codes, void* __restrict__ scales, int P, int k,
+    int E, int H, int I, bool by_pair) {
+    constexpr int kLoads = 6;  // direct loads per wave and stage: 4 of B, A, scales
     using S = typename std::conditional<kE8, uint8_t, float>::type;
-    const S* sx = static_cast<const S*>(sx_v);
-    const S* s13 = static_cast<const S*>(s13_v);
-    extern __shared__ __align__(16) uint8_t smem[];
-    uint16_t* list = reinterpret_cast<uint16_t*>(smem);
+    using Stage = GateStage<R>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Stage* const ring = reinterpret_cast<Stage*>(smem);
+    uint8_t* const unused = smem + D * sizeof(Stage);  // 1 KB: where loads that carry nothing land
+    uint16_t* const list = reinterpret_cast<uint16_t*>(unused + 1024);
+    __shared__ uint32_t tops[16 * R][kGateWaves];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
-    const MoeUnit u = find_unit(ids, P, E, blockIdx.y, by_pair, lane, wave == 0 ? list : nullptr);
+    const MoeUnit u = find_unit<kGateWaves>(ids, P, E, blockIdx.y, by_pair, reinterpret_cast<int*>(smem), list);
     if (blockIdx.x == 0 && threadIdx.x == 0) units[blockIdx.y] = u;
     if (u.count == 0) return;
-    __syncthreads();
     if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < u.count; i += 256) order[u.start + i] = list[i];
+        for (int i = threadIdx.x; i < u.count; i += 64 * kGateWaves) order[u.start + i] = list[i];
 
-    const int KB = H >> 7, SP = scale_pitch<kE8>(KB), n0 = (blockIdx.x * 4 + wave) * 16;
-    const int NB = (2 * I + 127) >> 7;
-    const uint8_t* b[2];
-    const S* sb[2];
+    const int KB = H >> 7, SP = scale_pitch<kE8>(KB), NB = I >> 6;  // scale rows of w13: 2I / 128
+    const uint32_t none = kNoRow;
+    const int sub = lane >> 3, chunk = ((lane & 7) ^ sub) * 16;
+    const int col = blockIdx.x * 128 + wave * 16;
+    // every offset fits 31 bits: 2 I H <= 2^29, T H <= 2^22
+    const v4u bufB = buffer_rsrc(w13 + (int64_t)u.e * 2 * I * H, (uint32_t)(2 * I) * (uint32_t)H);
+    const v4u bufX = buffer_rsrc(x, (uint32_t)(P / k) * (uint32_t)H);
+    const v4u bufSX = buffer_rsrc(sx_v, (uint32_t)(P / k) * SP * sizeof(S));
+    const v4u bufSB = buffer_rsrc(static_cast<const S*>(s13_v) + (int64_t)u.e * NB * SP, (uint32_t)NB * SP * sizeof(S));
+    uint32_t offB[4];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        b[c] = w13 + ((int64_t)u.e * 2 * I + c * I + n0 + lr) * H + lg * 16;
-        sb[c] = s13 + ((int64_t)u.e * NB + ((c * I + n0) >> 7)) * SP;
-    }
+    for (int j = 0; j < 4; ++j)
+        offB[j] = (uint32_t)((j >> 1) * I + col + 8 * (j & 1) + sub) * (uint32_t)H + chunk;
+
     for (int m0 = 0; m0 < u.count; m0 += 16 * R) {
-        const int rows = u.count - m0;
-        const uint8_t* a[R];
-        const S* sa[R];
+        const int rows = min(u.count - m0, 16 * R);
+        // wave w < 2R loads activation rows 8w .. 8w+7; wave 0 the row scales,
+        // wave 1 the column scales (one word holds four K blocks' exponents)
+        const int arow = 8 * wave + sub;
+        const uint32_t offA = wave < 2 * R && arow < rows ? (uint32_t)(list[m0 + arow] / k) * (uint32_t)H + chunk : none;
+        const uint32_t offS =
+            wave == 0 && lane < rows ? (uint32_t)(list[m0 + lane] / k) * SP * (uint32_t)sizeof(S)
+            : wave == 1 && lane < 2  ? (uint32_t)((lane * I + blockIdx.x * 128) >> 7) * SP * (uint32_t)sizeof(S)
+                                     : none;
+        const v4u bufS = wave == 0 ? bufSX : bufSB;
+        auto issue = [&](int kb, Stage& s) __attribute__((always_inline)) {
+            const bool real = kb < KB;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int t = list[min(m0 + 16 * r + lr, u.count - 1)] / k;
-            a[r] = x + (int64_t)t * H + lg * 16;
-            sa[r] = sx + (int64_t)t * SP;
-        }
+            for (int j = 0; j < 4; ++j)
+                load_lds_16(bufB, real ? offB[j] + kb * 128 : none, s.b + wave * 4096 + j * 1024);
+            load_lds_16(bufX, real ? offA + kb * 128 : none, wave < 2 * R ? s.a + wave * 1024 : unused);
+            load_lds_4(bufS, real ? offS + (kE8 ? kb & ~3 : kb * 4) : none,
+                       wave == 0 ? (void*)s.sa : wave == 1 ? (void*)s.sb : (void*)unused);
+        };
         v4f acc[R][2];
         clear(acc);
-        constexpr int D = R == 1 ? 4 : 2;
-        Block<R, 2, kE8> ring[D];
-        auto load = [&](int kb, Block<R, 2, kE8>& s) __attribute__((always_inline)) {
-            kb = min(kb, KB - 1);
+        lds_barrier();  // the ids, or the last rows' stages, have been read
+#pragma unroll
+        for (int d = 0; d < D - 1; ++d) issue(d, ring[d]);
+        int at = 0;
+        for (int kb = 0; kb < KB; ++kb) {
+            // stage kb has landed for this wave, and with the barrier for all;
+            // all are also done with stage kb - 1, which the next loads refill
+            wait_vmcnt<kLoads * (D - 2)>();
+            lds_barrier();
+            issue(kb + D - 1, ring[at == 0 ? D - 1 : at - 1]);
+            const Stage& s = ring[at];
+            Block<R, 2, kE8> f;
+            const uint8_t* const pb = s.b + wave * 4096 + lr * 128;
+            const int lo = (lg ^ (lr & 7)) << 4, hi = lo ^ 64;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                load_chunks(b[c] + kb * 128, s.b[c]);
-                s.sb[c] = sb[c][kb];
+                f.b[c][0] = *reinterpret_cast<const v4u*>(pb + c * 2048 + lo);
+                f.b[c][1] = *reinterpret_cast<const v4u*>(pb + c * 2048 + hi);
+                if constexpr (kE8)
+                    f.sb[c] = reinterpret_cast<const uint8_t*>(s.sb + c)[kb & 3];
+                else
+                    f.sb[c] = s.sb[c];
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                load_chunks(a[r] + kb * 128, s.a[r]);
-                s.sa[r] = sa[r][kb];
+                f.a[r][0] = *reinterpret_cast<const v4u*>(s.a + r * 2048 + lr * 128 + lo);
+                f.a[r][1] = *reinterpret_cast<const v4u*>(s.a + r * 2048 + lr * 128 + hi);
+                if constexpr (kE8)
+                    f.sa[r] = reinterpret_cast<const uint8_t*>(s.sa + 16 * r + lr)[kb & 3];
+                else
+                    f.sa[r] = s.sa[16 * r + lr];
             }
-        };
-#pragma unroll
-        for (int d = 0; d < D; ++d) load(d, ring[d]);
-        for (int kb = 0; kb < KB; kb += D) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                if (kb + d < KB) multiply(ring[d], rows, acc);
-                load(kb + d + D, ring[d]);
-            }
+            multiply_exact(f, rows, acc);
+            at = at == D - 1 ? 0 : at + 1;
         }
+
+        // silu(gate) * up, then the block's largest magnitude per row across
+        // the waves, compared as bits so that a NaN wins
+        float h[R][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int row = m0 + 16 * r + lr;
-            if (row >= u.count) continue;
-            v4f h;
+            uint32_t top = 0;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float g = acc[r][0][q];
-                h[q] = g / (1.0f + expf(-g)) * acc[r][1][q];
+                h[r][q] = g / (1.0f + expf(-g)) * acc[r][1][q];
+                top = max(top, __float_as_uint(h[r][q]) & 0x7fffffffu);
             }
-            *reinterpret_cast<v4f*>(hidden + (int64_t)(u.start + row) * I + n0 + 4 * lg) = h;
+            top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+            if (lg == 0) tops[16 * r + lr][wave] = top;
         }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = 16 * r + lr;
+            uint32_t top = 0;
+#pragma unroll
+            for (int w = 0; w < kGateWaves; ++w) top = max(top, tops[row][w]);
+            if (row >= rows) continue;
+            const float a = __uint_as_float(top);
+            const bool finite = top < 0x7f800000u;
+            const float scale = a / 448.0f;
+            const int ex = kE8 ? e8m0_exponent(a) : 0;
+            const float y = kE8 ? exp2_neg(ex) : 1.0f / scale;
+            const bool fast = scale >= 1.17549435e-38f && y <= 3.40282347e38f;
+            float v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] = kE8 ? h[r][q] * y : fast ? quotient_rn(h[r][q], scale, y) : h[r][q] / scale;
+            const int64_t out = u.start + m0 + row;
+            *reinterpret_cast<uint32_t*>(codes + out * I + col + 4 * lg) =
+                (kE8 || top != 0) ? e4m3x4_hw(v[0], v[1], v[2], v[3]) : 0u;
+            if (wave == 0 && lg == 0) {
+                const int64_t to = out * scale_pitch<kE8>(I >> 7) + blockIdx.x;
+                if (kE8)
+                    static_cast<uint8_t*>(scales)[to] = finite ? (uint8_t)(ex + 127) : (uint8_t)255;
+                else
+                    static_cast<float*>(scales)[to] = finite ? scale : __builtin_nanf("");
+            }
+        }
+        wait_vmcnt<0>();  // the empty loads of the last stages have retired
+        __syncthreads();
     }
 }
 
@@ -219,7 +336,9 @@ __global__ __launch_bounds__(64 * W) void moe_down_kernel(
         // the loader runs D steps ahead of the multiplier, each with its own
         // place (job, K block) in the list
         int lj = first / KB, lk = first % KB;
-        const uint8_t *b, *a[R];
+        const auto hbuf = buffer_of(codes, (int64_t)P * I);
+        const uint8_t* b;
+        uint32_t a[R];
         const S *sb, *sa[R];
         auto aim = [&](int j) __attribute__((always_inline)) {
             const int e = __builtin_amdgcn_readfirstlane(jobs[j].e);
@@ -230,7 +349,7 @@ __global__ __launch_bounds__(64 * W) void moe_down_kernel(
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int row = start + min(16 * r + lr, count - 1);
-                a[r] = codes + (int64_t)row * I + lg * 16;
+                a[r] = 16 * r + lr < count ? (uint32_t)(row * I + lg * 16) : kNoRow;
                 sa[r] = sh + (int64_t)row * SP;
             }
         };
@@ -239,7 +358,7 @@ __global__ __launch_bounds__(64 * W) void moe_down_kernel(
             s.sb[0] = sb[lk];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                load_chunks(a[r] + lk * 128, s.a[r]);
+                load_chunks(hbuf, a[r] + lk * 128, s.a[r]);
                 s.sa[r] = sa[r][lk];
             }
             if (++lk == KB) {
@@ -303,17 +422,15 @@ static dg_status moe_r(const MoeArgs& a, hipStream_t stream) {
     uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
     MoeUnit* const units = reinterpret_cast<MoeUnit*>(ws + at.units);
     int32_t* const order = reinterpret_cast<int32_t*>(ws + at.order);
-    float* const hidden = reinterpret_cast<float*>(ws + at.hidden);
     uint8_t* const codes = ws + at.codes;
     void* const scales = ws + at.scales;
     const int P = a.T * a.k, U = std::min(P, a.E);
-    hipLaunchKernelGGL((moe_gate_up_kernel<R, kE8>), dim3(a.I / 64, U), dim3(256), (P * 2 + 15) & ~15,
-                       stream, a.x, a.sx, a.ids, a.w13, a.s13, units, order, hidden, P, a.k, a.E, a.H,
-                       a.I, P <= a.E);
-    dg_status s = launched();
-    if (s != DG_OK) return s;
-    s = kE8 ? launch_quantize_per_token_e8m0(hidden, P, a.I, codes, static_cast<uint8_t*>(scales), stream)
-            : launch_quantize_per_token(hidden, P, a.I, codes, static_cast<float*>(scales), stream);
+    constexpr int D = R == 4 ? 3 : 4;
+    const size_t ring = D * sizeof(GateStage<R>) + 1024;
+    hipLaunchKernelGGL((moe_gate_up_kernel<R, D, kE8>), dim3(a.I / 128, U), dim3(64 * kGateWaves),
+                       ring + P * 2, stream, a.x, a.sx, a.ids, a.w13, a.s13, units, order, codes, scales,
+                       P, a.k, a.E, a.H, a.I, P <= a.E);
+    const dg_status s = launched();
     if (s != DG_OK) return s;
     constexpr int W = 4;
     const size_t lds = W * a.T * 64 + ((P + 3) & ~3) * 4 + (U + P / (16 * R)) * sizeof(MoeJob) + P * 2;
