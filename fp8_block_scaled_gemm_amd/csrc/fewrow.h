@@ -119,6 +119,108 @@ __device__ __forceinline__ void clear(v4f (&acc)[R][C]) {
         for (int c = 0; c < C; ++c) acc[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
 }
 
+// ------------------------------------------------------------------- panels
+//
+// A workgroup of eight waves multiplies 16 R rows of A, shared, by 128 C rows
+// of B, 16 C a wave.  A K block of all of it is one stage of a ring in LDS,
+// filled by direct loads that take whole 128-byte lines, eight consecutive
+// lanes a line: fragment-shaped loads straight to registers touch 16 lines
+// for 16 bytes each and are bound by the cache's tag rate.  Each stage costs
+// one barrier.  The stages ahead keep the weights of D - 1 K blocks in flight.
+// In LDS 16-byte chunk c of row r sits at c ^ (r & 7), which the loading lanes
+// arrange by the chunk they ask for, so that fragment reads do not conflict.
+constexpr int kPanelWaves = 8;
+
+template <int R, int C>
+struct PanelStage {
+    uint8_t b[kPanelWaves * C * 2048];  // wave w: C tiles of 16 rows
+    uint8_t a[16 * R * 128];
+    float sa[64];  // per row of A
+    float sb[64];  // [c] of tile set c
+};
+
+// Bytes of LDS for a panel: the ring and the place where loads land that carry
+// nothing (every wave issues the same number of loads per stage).
+template <int R, int C, int D>
+constexpr size_t panel_lds() {
+    return D * sizeof(PanelStage<R, C>) + 1024;
+}
+
+// What the lanes of a wave load.  Offsets are bytes from the buffers' starts
+// at K block 0, or kNoRow.
+template <int C>
+struct PanelLoads {
+    v4u bufB, bufA, bufS;  // bufS: the scales this wave loads
+    uint32_t offB[2 * C];  // lane l: row 8 j + l / 8 of the wave's 16 C rows
+    uint32_t offA;         // lane l of wave w: row 8 w + l / 8 of A
+    uint32_t offS;         // lane l of wave 0: scale row l of A; of wave 1: column scales of tile set l
+};
+
+// The 16-byte chunk that lane l asks for, in bytes.
+__device__ __forceinline__ uint32_t panel_chunk(int lane) { return ((lane & 7) ^ (lane >> 3)) * 16; }
+
+// acc = the scaled product over KB K blocks; `rows` (uniform) rows of A count.
+// kExact: through bf16 (multiply_exact).  The ring must be free on entry and
+// is free again on return (the call ends with a barrier).
+template <int R, int C, int D, bool kE8, bool kExact>
+__device__ __forceinline__ void panel_product(uint8_t* smem, const PanelLoads<C>& p, int KB, int rows,
+                                              int wave, int lane, v4f (&acc)[R][C]) {
+    using Stage = PanelStage<R, C>;
+    Stage* const ring = reinterpret_cast<Stage*>(smem);
+    uint8_t* const unused = smem + D * sizeof(Stage);
+    constexpr int kLoads = 2 * C + 2;
+    const int lr = lane & 15, lg = lane >> 4;
+    auto issue = [&](int kb, Stage& s) __attribute__((always_inline)) {
+        const bool real = kb < KB;  // stages past the last one load nothing
+#pragma unroll
+        for (int j = 0; j < 2 * C; ++j)
+            load_lds_16(p.bufB, real ? p.offB[j] + kb * 128 : kNoRow, s.b + wave * C * 2048 + j * 1024);
+        load_lds_16(p.bufA, real ? p.offA + kb * 128 : kNoRow, wave < 2 * R ? s.a + wave * 1024 : unused);
+        load_lds_4(p.bufS, real ? p.offS + (kE8 ? kb & ~3 : kb * 4) : kNoRow,
+                   wave == 0 ? (void*)s.sa : wave == 1 ? (void*)s.sb : (void*)unused);
+    };
+    clear(acc);
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) issue(d, ring[d]);
+    const int lo = (lg ^ (lr & 7)) << 4, hi = lo ^ 64;
+    int at = 0;
+    for (int kb = 0; kb < KB; ++kb) {
+        // stage kb has landed for this wave, and with the barrier for all; all
+        // are also done with stage kb - 1, which the next loads refill
+        wait_vmcnt_lgkm0<kLoads * (D - 2)>();
+        lds_barrier();
+        issue(kb + D - 1, ring[at == 0 ? D - 1 : at - 1]);
+        const Stage& s = ring[at];
+        Block<R, C, kE8> f;
+        const uint8_t* const pb = s.b + wave * C * 2048 + lr * 128;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            f.b[c][0] = *reinterpret_cast<const v4u*>(pb + c * 2048 + lo);
+            f.b[c][1] = *reinterpret_cast<const v4u*>(pb + c * 2048 + hi);
+            if constexpr (kE8)  // one word holds four K blocks' exponents
+                f.sb[c] = reinterpret_cast<const uint8_t*>(s.sb + c)[kb & 3];
+            else
+                f.sb[c] = s.sb[c];
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            f.a[r][0] = *reinterpret_cast<const v4u*>(s.a + r * 2048 + lr * 128 + lo);
+            f.a[r][1] = *reinterpret_cast<const v4u*>(s.a + r * 2048 + lr * 128 + hi);
+            if constexpr (kE8)
+                f.sa[r] = reinterpret_cast<const uint8_t*>(s.sa + 16 * r + lr)[kb & 3];
+            else
+                f.sa[r] = s.sa[16 * r + lr];
+        }
+        if constexpr (kExact)
+            multiply_exact(f, rows, acc);
+        else
+            multiply(f, rows, acc);
+        at = at == D - 1 ? 0 : at + 1;
+    }
+    wait_vmcnt_lgkm0<0>();  // the empty loads of the last stages have retired
+    lds_barrier();
+}
+
 // Scales per row of `kb` K blocks: fp32 as they are, E8M0 bytes padded to four.
 template <bool kE8>
 __host__ __device__ __forceinline__ int scale_pitch(int kb) {

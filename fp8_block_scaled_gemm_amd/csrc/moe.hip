@@ -28,17 +28,23 @@ struct MoeJob {
     uint16_t start, count;
 };
 
+// Up to this many tokens the second product adds up each token's experts
+// itself; larger batches write every pair's product and add them up after.
+constexpr int kFusedTokens = 16;
+
 // Workspace layout, in bytes from its start.
 struct MoeLayout {
-    int64_t units, order, codes, scales, total;
-    MoeLayout(int64_t T, int64_t k, int64_t E, int64_t I) {
+    int64_t units, order, place, codes, scales, out, total;
+    MoeLayout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
         const int64_t P = T * k, U = std::min(P, E);
         auto up = [](int64_t v) { return (v + 255) & ~int64_t(255); };
         units = 0;
         order = units + up(U * sizeof(MoeUnit));
-        codes = order + up(P * 4);
+        place = order + up(P * 4);
+        codes = place + up(P * 4);
         scales = codes + up(P * I);
-        total = scales + up(P * ((I / 128 + 3) & ~int64_t(3)) * 4);
+        out = scales + up(P * ((I / 128 + 3) & ~int64_t(3)) * 4);
+        total = out + (T > kFusedTokens ? up(P * H * 4) : 0);
     }
 };
 
@@ -98,124 +104,55 @@ __device__ __forceinline__ MoeUnit find_unit(const int32_t* __restrict__ ids, in
 }
 
 // First product: silu(gate) * up, quantized per 128 hidden columns.  A
-// workgroup's eight waves take 16 hidden columns each of one 128-column block
-// of one unit; a wave multiplies its gate and its up rows of the weights by
-// the unit's activations, up to 16 R rows at a time.
-//
-// A K block of everything the workgroup multiplies (256 weight rows, the
-// activation rows, their scales) is one stage of a ring in LDS, filled by
-// direct loads that take whole 128-byte lines, eight consecutive lanes a
-// line: fragment-shaped loads straight to registers touch 16 lines for 16
-// bytes each and are bound by the cache's tag rate (R = 4: 3.3 TB/s).  Each
-// stage costs one barrier.  The stages ahead, D - 1 of them, keep the weights
-// of D - 1 K blocks, 32 KB each, in flight per CU.
+// workgroup takes one 128-column block of one unit, up to 16 R rows at a time;
+// a wave multiplies its 16 gate and its 16 up rows of the weights by the same
+// activations.
 //
 // The sums go through the bf16 matrix instruction (see multiply_exact): the
 // FP8 one would move about one code in 600 of the quantized result.
-constexpr int kGateWaves = 8;
-
-template <int R>
-struct GateStage {
-    uint8_t b[kGateWaves * 32 * 128];  // wave w: 16 gate rows, 16 up rows
-    uint8_t a[16 * R * 128];
-    float sa[64];
-    float sb[64];  // [0] gate, [1] up
-};
-
 template <int R, int D, bool kE8>
-__global__ __launch_bounds__(64 * kGateWaves) void moe_gate_up_kernel(
+__global__ __launch_bounds__(64 * kPanelWaves) void moe_gate_up_kernel(
     const uint8_t* __restrict__ x, const void* __restrict__ sx_v, const int32_t* __restrict__ ids,
     const uint8_t* __restrict__ w13, const void* __restrict__ s13_v, MoeUnit* __restrict__ units,
-    int32_t* __restrict__ order, uint8_t* __restrict__ codes, void* __restrict__ scales, int P, int k,
-    int E, int H, int I, bool by_pair) {
-    constexpr int kLoads = 6;  // direct loads per wave and stage: 4 of B, A, scales
+    int32_t* __restrict__ order, int32_t* __restrict__ place, uint8_t* __restrict__ codes,
+    void* __restrict__ scales, int P, int k, int E, int H, int I, bool by_pair) {
     using S = typename std::conditional<kE8, uint8_t, float>::type;
-    using Stage = GateStage<R>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    Stage* const ring = reinterpret_cast<Stage*>(smem);
-    uint8_t* const unused = smem + D * sizeof(Stage);  // 1 KB: where loads that carry nothing land
-    uint16_t* const list = reinterpret_cast<uint16_t*>(unused + 1024);
-    __shared__ uint32_t tops[16 * R][kGateWaves];
+    uint16_t* const list = reinterpret_cast<uint16_t*>(smem + panel_lds<R, 2, D>());
+    __shared__ uint32_t tops[16 * R][kPanelWaves];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
-    const MoeUnit u = find_unit<kGateWaves>(ids, P, E, blockIdx.y, by_pair, reinterpret_cast<int*>(smem), list);
+    const MoeUnit u = find_unit<kPanelWaves>(ids, P, E, blockIdx.y, by_pair, reinterpret_cast<int*>(smem), list);
     if (blockIdx.x == 0 && threadIdx.x == 0) units[blockIdx.y] = u;
     if (u.count == 0) return;
     if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < u.count; i += 64 * kGateWaves) order[u.start + i] = list[i];
+        for (int i = threadIdx.x; i < u.count; i += 64 * kPanelWaves) {
+            order[u.start + i] = list[i];
+            place[list[i]] = u.start + i;
+        }
 
     const int KB = H >> 7, SP = scale_pitch<kE8>(KB), NB = I >> 6;  // scale rows of w13: 2I / 128
-    const uint32_t none = kNoRow;
-    const int sub = lane >> 3, chunk = ((lane & 7) ^ sub) * 16;
-    const int col = blockIdx.x * 128 + wave * 16;
+    const int sub = lane >> 3, col = blockIdx.x * 128 + wave * 16;
+    const uint32_t chunk = panel_chunk(lane), kSz = sizeof(S);
     // every offset fits 31 bits: 2 I H <= 2^29, T H <= 2^22
-    const v4u bufB = buffer_rsrc(w13 + (int64_t)u.e * 2 * I * H, (uint32_t)(2 * I) * (uint32_t)H);
-    const v4u bufX = buffer_rsrc(x, (uint32_t)(P / k) * (uint32_t)H);
-    const v4u bufSX = buffer_rsrc(sx_v, (uint32_t)(P / k) * SP * sizeof(S));
-    const v4u bufSB = buffer_rsrc(static_cast<const S*>(s13_v) + (int64_t)u.e * NB * SP, (uint32_t)NB * SP * sizeof(S));
-    uint32_t offB[4];
+    PanelLoads<2> p;
+    p.bufB = buffer_rsrc(w13 + (int64_t)u.e * 2 * I * H, (uint32_t)(2 * I) * (uint32_t)H);
+    p.bufA = buffer_rsrc(x, (uint32_t)(P / k) * (uint32_t)H);
+    p.bufS = wave == 0 ? buffer_rsrc(sx_v, (uint32_t)(P / k) * SP * kSz)
+                       : buffer_rsrc(static_cast<const S*>(s13_v) + (int64_t)u.e * NB * SP, (uint32_t)NB * SP * kSz);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        offB[j] = (uint32_t)((j >> 1) * I + col + 8 * (j & 1) + sub) * (uint32_t)H + chunk;
+        p.offB[j] = (uint32_t)((j >> 1) * I + col + 8 * (j & 1) + sub) * (uint32_t)H + chunk;
 
     for (int m0 = 0; m0 < u.count; m0 += 16 * R) {
-        const int rows = min(u.count - m0, 16 * R);
-        // wave w < 2R loads activation rows 8w .. 8w+7; wave 0 the row scales,
-        // wave 1 the column scales (one word holds four K blocks' exponents)
-        const int arow = 8 * wave + sub;
-        const uint32_t offA = wave < 2 * R && arow < rows ? (uint32_t)(list[m0 + arow] / k) * (uint32_t)H + chunk : none;
-        const uint32_t offS =
-            wave == 0 && lane < rows ? (uint32_t)(list[m0 + lane] / k) * SP * (uint32_t)sizeof(S)
-            : wave == 1 && lane < 2  ? (uint32_t)((lane * I + blockIdx.x * 128) >> 7) * SP * (uint32_t)sizeof(S)
-                                     : none;
-        const v4u bufS = wave == 0 ? bufSX : bufSB;
-        auto issue = [&](int kb, Stage& s) __attribute__((always_inline)) {
-            const bool real = kb < KB;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                load_lds_16(bufB, real ? offB[j] + kb * 128 : none, s.b + wave * 4096 + j * 1024);
-            load_lds_16(bufX, real ? offA + kb * 128 : none, wave < 2 * R ? s.a + wave * 1024 : unused);
-            load_lds_4(bufS, real ? offS + (kE8 ? kb & ~3 : kb * 4) : none,
-                       wave == 0 ? (void*)s.sa : wave == 1 ? (void*)s.sb : (void*)unused);
-        };
+        const int rows = min(u.count - m0, 16 * R), arow = 8 * wave + sub;
+        p.offA = arow < rows ? (uint32_t)(list[m0 + arow] / k) * (uint32_t)H + chunk : kNoRow;
+        p.offS = wave == 0 && lane < rows ? (uint32_t)(list[m0 + lane] / k) * SP * kSz
+                 : wave == 1 && lane < 2  ? (uint32_t)((lane * I + blockIdx.x * 128) >> 7) * SP * kSz
+                                          : kNoRow;
         v4f acc[R][2];
-        clear(acc);
-        lds_barrier();  // the ids, or the last rows' stages, have been read
-#pragma unroll
-        for (int d = 0; d < D - 1; ++d) issue(d, ring[d]);
-        int at = 0;
-        for (int kb = 0; kb < KB; ++kb) {
-            // stage kb has landed for this wave, and with the barrier for all;
-            // all are also done with stage kb - 1, which the next loads refill
-            wait_vmcnt<kLoads * (D - 2)>();
-            lds_barrier();
-            issue(kb + D - 1, ring[at == 0 ? D - 1 : at - 1]);
-            const Stage& s = ring[at];
-            Block<R, 2, kE8> f;
-            const uint8_t* const pb = s.b + wave * 4096 + lr * 128;
-            const int lo = (lg ^ (lr & 7)) << 4, hi = lo ^ 64;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                f.b[c][0] = *reinterpret_cast<const v4u*>(pb + c * 2048 + lo);
-                f.b[c][1] = *reinterpret_cast<const v4u*>(pb + c * 2048 + hi);
-                if constexpr (kE8)
-                    f.sb[c] = reinterpret_cast<const uint8_t*>(s.sb + c)[kb & 3];
-                else
-                    f.sb[c] = s.sb[c];
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                f.a[r][0] = *reinterpret_cast<const v4u*>(s.a + r * 2048 + lr * 128 + lo);
-                f.a[r][1] = *reinterpret_cast<const v4u*>(s.a + r * 2048 + lr * 128 + hi);
-                if constexpr (kE8)
-                    f.sa[r] = reinterpret_cast<const uint8_t*>(s.sa + 16 * r + lr)[kb & 3];
-                else
-                    f.sa[r] = s.sa[16 * r + lr];
-            }
-            multiply_exact(f, rows, acc);
-            at = at == D - 1 ? 0 : at + 1;
-        }
+        panel_product<R, 2, D, kE8, true>(smem, p, KB, rows, wave, lane, acc);
 
         // silu(gate) * up, then the block's largest magnitude per row across
         // the waves, compared as bits so that a NaN wins
@@ -239,7 +176,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void moe_gate_up_kernel(
             const int row = 16 * r + lr;
             uint32_t top = 0;
 #pragma unroll
-            for (int w = 0; w < kGateWaves; ++w) top = max(top, tops[row][w]);
+            for (int w = 0; w < kPanelWaves; ++w) top = max(top, tops[row][w]);
             if (row >= rows) continue;
             const float a = __uint_as_float(top);
             const bool finite = top < 0x7f800000u;
@@ -262,9 +199,71 @@ __global__ __launch_bounds__(64 * kGateWaves) void moe_gate_up_kernel(
                     static_cast<float*>(scales)[to] = finite ? scale : __builtin_nanf("");
             }
         }
-        wait_vmcnt<0>();  // the empty loads of the last stages have retired
-        __syncthreads();
+        __syncthreads();  // tops have been read
     }
+}
+
+// Second product of a batch, unweighted: out[row] = h w2^T in fp32, one 128
+// column block of one unit per workgroup.
+template <int R, int D, bool kE8>
+__global__ __launch_bounds__(64 * kPanelWaves) void moe_down_rows_kernel(
+    const uint8_t* __restrict__ codes, const void* __restrict__ sh_v, const uint8_t* __restrict__ w2,
+    const void* __restrict__ s2_v, const MoeUnit* __restrict__ units, float* __restrict__ out, int P,
+    int H, int I) {
+    using S = typename std::conditional<kE8, uint8_t, float>::type;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lr = lane & 15, lg = lane >> 4;
+    const int e = __builtin_amdgcn_readfirstlane(units[blockIdx.y].e);
+    const int start = __builtin_amdgcn_readfirstlane(units[blockIdx.y].start);
+    const int count = __builtin_amdgcn_readfirstlane(units[blockIdx.y].count);
+    const int KB = I >> 7, SP = scale_pitch<kE8>(KB), NB = H >> 7;
+    const int sub = lane >> 3, col = blockIdx.x * 128 + wave * 16;
+    const uint32_t chunk = panel_chunk(lane), kSz = sizeof(S);
+    for (int m0 = 0; m0 < count; m0 += 16 * R) {
+        const int rows = min(count - m0, 16 * R), arow = 8 * wave + sub, row0 = start + m0;
+        PanelLoads<1> p;
+        // offsets fit 31 bits: H I <= 2^28, 16 R rows of I
+        p.bufB = buffer_rsrc(w2 + (int64_t)e * H * I, (uint32_t)H * (uint32_t)I);
+        p.bufA = buffer_rsrc(codes + (int64_t)row0 * I, (uint32_t)rows * (uint32_t)I);
+        p.bufS = wave == 0
+                     ? buffer_rsrc(static_cast<const S*>(sh_v) + (int64_t)row0 * SP, (uint32_t)rows * SP * kSz)
+                     : buffer_rsrc(static_cast<const S*>(s2_v) + (int64_t)e * NB * SP, (uint32_t)NB * SP * kSz);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) p.offB[j] = (uint32_t)(col + 8 * j + sub) * (uint32_t)I + chunk;
+        p.offA = arow < rows ? (uint32_t)arow * (uint32_t)I + chunk : kNoRow;
+        p.offS = wave == 0 && lane < rows ? (uint32_t)lane * SP * kSz
+                 : wave == 1 && lane == 0 ? (uint32_t)blockIdx.x * SP * kSz
+                                          : kNoRow;
+        v4f acc[R][1];
+        panel_product<R, 1, D, kE8, false>(smem, p, KB, rows, wave, lane, acc);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (16 * r + lr < rows)
+                *reinterpret_cast<v4f*>(out + (int64_t)(row0 + 16 * r + lr) * H + col + 4 * lg) = acc[r][0];
+    }
+}
+
+// y_t = bf16(sum over j of weight * out[place of (t, j)]), four columns a thread.
+__global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restrict__ out,
+                                                          const int32_t* __restrict__ ids,
+                                                          const int32_t* __restrict__ place,
+                                                          const float* __restrict__ weights,
+                                                          uint16_t* __restrict__ y, int k, int E, int H) {
+    const int64_t t = blockIdx.y;
+    const int c = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (c >= H) return;
+    v4f sum = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < k; ++j) {
+        const int id = ids[t * k + j];
+        if (id < 0 || id >= E) continue;
+        sum += weights[t * k + j] * *reinterpret_cast<const v4f*>(out + (int64_t)place[t * k + j] * H + c);
+    }
+    const v2f lo = {sum[0], sum[1]}, hi = {sum[2], sum[3]};
+    v2u packed;
+    packed[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector(lo, v2bf));
+    packed[1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, v2bf));
+    *reinterpret_cast<v2u*>(y + t * H + c) = packed;
 }
 
 // Second product and the weighted sum: a workgroup owns 16 columns of y for
@@ -413,25 +412,36 @@ __global__ __launch_bounds__(64 * W) void moe_down_kernel(
 }
 
 int64_t moe_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
-    return MoeLayout(T, k, E, I).total;
+    return MoeLayout(T, k, E, H, I).total;
 }
 
 template <int R, bool kE8>
 static dg_status moe_r(const MoeArgs& a, hipStream_t stream) {
-    const MoeLayout at(a.T, a.k, a.E, a.I);
+    const MoeLayout at(a.T, a.k, a.E, a.H, a.I);
     uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
     MoeUnit* const units = reinterpret_cast<MoeUnit*>(ws + at.units);
     int32_t* const order = reinterpret_cast<int32_t*>(ws + at.order);
+    int32_t* const place = reinterpret_cast<int32_t*>(ws + at.place);
     uint8_t* const codes = ws + at.codes;
     void* const scales = ws + at.scales;
     const int P = a.T * a.k, U = std::min(P, a.E);
     constexpr int D = R == 4 ? 3 : 4;
-    const size_t ring = D * sizeof(GateStage<R>) + 1024;
-    hipLaunchKernelGGL((moe_gate_up_kernel<R, D, kE8>), dim3(a.I / 128, U), dim3(64 * kGateWaves),
-                       ring + P * 2, stream, a.x, a.sx, a.ids, a.w13, a.s13, units, order, codes, scales,
+    hipLaunchKernelGGL((moe_gate_up_kernel<R, D, kE8>), dim3(a.I / 128, U), dim3(64 * kPanelWaves),
+                       (panel_lds<R, 2, D>()) + P * 2, stream, a.x, a.sx, a.ids, a.w13, a.s13, units, order,
+                       place, codes, scales,
                        P, a.k, a.E, a.H, a.I, P <= a.E);
     const dg_status s = launched();
     if (s != DG_OK) return s;
+    if (a.T > kFusedTokens) {
+        float* const out = reinterpret_cast<float*>(ws + at.out);
+        constexpr int D2 = 3;
+        hipLaunchKernelGGL((moe_down_rows_kernel<R, D2, kE8>), dim3(a.H / 128, U), dim3(64 * kPanelWaves),
+                           (panel_lds<R, 1, D2>()), stream, codes, scales, a.w2, a.s2, units, out, P, a.H, a.I);
+        if (launched() != DG_OK) return DG_ERR_HIP;
+        hipLaunchKernelGGL(moe_combine_kernel, dim3((a.H + 1023) / 1024, a.T), dim3(256), 0, stream, out, a.ids,
+                           place, a.weights, a.y, a.k, a.E, a.H);
+        return launched();
+    }
     constexpr int W = 4;
     const size_t lds = W * a.T * 64 + ((P + 3) & ~3) * 4 + (U + P / (16 * R)) * sizeof(MoeJob) + P * 2;
     hipLaunchKernelGGL((moe_down_kernel<R, kE8, W>), dim3(a.H / 16), dim3(64 * W), lds, stream, codes,
