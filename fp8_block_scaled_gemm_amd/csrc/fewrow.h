@@ -152,7 +152,7 @@ template <int C>
 struct PanelLoads {
     v4u bufB, bufA, bufS;  // bufS: the scales this wave loads
     uint32_t offB[2 * C];  // lane l: row 8 j + l / 8 of the wave's 16 C rows
-    uint32_t offA;         // lane l of wave w: row 8 w + l / 8 of A
+    uint32_t offA[2];      // lane l of wave w: row 8 w + l / 8 of A ([0]; free panels: see panel_a_loads)
     uint32_t offS;         // lane l of wave 0: scale row l of A; of wave 1: column scales of tile set l
 };
 
@@ -175,7 +175,7 @@ __device__ __forceinline__ void panel_product(uint8_t* smem, const PanelLoads<C>
 #pragma unroll
         for (int j = 0; j < 2 * C; ++j)
             load_lds_16(p.bufB, real ? p.offB[j] + kb * 128 : kNoRow, s.b + wave * C * 2048 + j * 1024);
-        load_lds_16(p.bufA, real ? p.offA + kb * 128 : kNoRow, wave < 2 * R ? s.a + wave * 1024 : unused);
+        load_lds_16(p.bufA, real ? p.offA[0] + kb * 128 : kNoRow, wave < 2 * R ? s.a + wave * 1024 : unused);
         load_lds_4(p.bufS, real ? p.offS + (kE8 ? kb & ~3 : kb * 4) : kNoRow,
                    wave == 0 ? (void*)s.sa : wave == 1 ? (void*)s.sb : (void*)unused);
     };
@@ -218,6 +218,104 @@ __device__ __forceinline__ void panel_product(uint8_t* smem, const PanelLoads<C>
         at = at == D - 1 ? 0 : at + 1;
     }
     wait_vmcnt_lgkm0<0>();  // the empty loads of the last stages have retired
+    lds_barrier();
+}
+
+// For few rows of A the same panel without a barrier per K block: A and the
+// scales come in chunks of four K blocks, double-buffered, one barrier per
+// chunk; in between every wave runs on its own through its private ring of B.
+// (A lone workgroup on a CU streams 35 GB/s with the barrier per K block.)
+constexpr int kChunk = 4;
+
+// Direct loads of each of W waves for a chunk of A; load i = wave * this + j
+// takes rows 8 (i % 2R) .. + 7.
+constexpr int panel_a_loads(int R, int W) { return kChunk * 2 * R / W; }
+
+template <int R, int C, int D, int W>
+struct FreePanel {
+    uint8_t b[D][W * C * 2048];
+    uint8_t a[2][kChunk][16 * R * 128];
+    float sa[2][256];  // [row][kChunk]; E8M0: one word per row
+    float sb[2][256];  // [c][kChunk]
+    uint8_t unused[1024];
+};
+
+template <int R, int C, int D, int W, bool kE8, bool kExact>
+__device__ __forceinline__ void free_panel_product(uint8_t* smem, const PanelLoads<C>& p, int KB, int rows,
+                                                   int wave, int lane, v4f (&acc)[R][C]) {
+    static_assert(R <= 2, "A chunks of more rows do not fit beside the ring");
+    constexpr int kA = panel_a_loads(R, W);
+    FreePanel<R, C, D, W>& s = *reinterpret_cast<FreePanel<R, C, D, W>*>(smem);
+    const int lr = lane & 15, lg = lane >> 4;
+    auto issue_b = [&](int kb, int st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 2 * C; ++j)
+            load_lds_16(p.bufB, kb < KB ? p.offB[j] + kb * 128 : kNoRow, s.b[st] + wave * C * 2048 + j * 1024);
+    };
+    // a wave's loads of an A chunk: K block i / 2R, rows 8 (i % 2R) .. + 7
+    auto issue_chunk = [&](int kb0, int buf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < kA; ++j) {
+            const int i = wave * kA + j, kb = kb0 + i / (2 * R);
+            load_lds_16(p.bufA, kb < KB ? p.offA[j] + kb * 128 : kNoRow, s.a[buf][0] + i * 1024);
+        }
+        void* const to = wave == 0 ? (void*)s.sa[buf] : wave == 1 ? (void*)s.sb[buf] : (void*)s.unused;
+        const uint32_t off = kb0 < KB ? p.offS + kb0 * (kE8 ? 1 : 4) : kNoRow;
+        if (kE8)
+            load_lds_4(p.bufS, off, to);
+        else
+            load_lds_16(p.bufS, off, to);
+    };
+    clear(acc);
+    issue_chunk(0, 0);
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) issue_b(d, d);
+    wait_vmcnt_lgkm0<2 * C * (D - 1)>();
+    lds_barrier();
+    const int lo = (lg ^ (lr & 7)) << 4, hi = lo ^ 64;
+    int at = 0;
+    for (int kb0 = 0; kb0 < KB; kb0 += kChunk) {
+        const int buf = (kb0 / kChunk) & 1;
+        issue_chunk(kb0 + kChunk, buf ^ 1);  // its last reader passed the barrier below
+#pragma unroll
+        for (int kk = 0; kk < kChunk; ++kk) {
+            const int kb = kb0 + kk;
+            if (kb < KB) {
+                wait_vmcnt_lgkm0<2 * C * (D - 2)>();  // this wave's B of kb
+                asm volatile("" ::: "memory");
+                issue_b(kb + D - 1, at == 0 ? D - 1 : at - 1);
+                Block<R, C, kE8> f;
+                const uint8_t* const pb = s.b[at] + wave * C * 2048 + lr * 128;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    f.b[c][0] = *reinterpret_cast<const v4u*>(pb + c * 2048 + lo);
+                    f.b[c][1] = *reinterpret_cast<const v4u*>(pb + c * 2048 + hi);
+                    if constexpr (kE8)
+                        f.sb[c] = reinterpret_cast<const uint8_t*>(s.sb[buf] + c)[kk];
+                    else
+                        f.sb[c] = s.sb[buf][c * kChunk + kk];
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const uint8_t* const pa = s.a[buf][kk] + (16 * r + lr) * 128;
+                    f.a[r][0] = *reinterpret_cast<const v4u*>(pa + lo);
+                    f.a[r][1] = *reinterpret_cast<const v4u*>(pa + hi);
+                    if constexpr (kE8)
+                        f.sa[r] = reinterpret_cast<const uint8_t*>(s.sa[buf] + 16 * r + lr)[kk];
+                    else
+                        f.sa[r] = s.sa[buf][(16 * r + lr) * kChunk + kk];
+                }
+                if constexpr (kExact)
+                    multiply_exact(f, rows, acc);
+                else
+                    multiply(f, rows, acc);
+                at = at == D - 1 ? 0 : at + 1;
+            }
+        }
+        wait_vmcnt_lgkm0<2 * C * kChunk>();  // the next chunk, loaded before these K blocks' B
+        lds_barrier();
+    }
+    wait_vmcnt_lgkm0<0>();
     lds_barrier();
 }
 

@@ -28,13 +28,16 @@ struct MoeJob {
     uint16_t start, count;
 };
 
-// Up to this many tokens the second product adds up each token's experts
-// itself; larger batches write every pair's product and add them up after.
-constexpr int kFusedTokens = 16;
+// A few pairs: the hidden rows fit the second product's LDS, and there are at
+// most 256 blocks of 128 hidden columns, so the first product takes 64 columns
+// a workgroup.  Then the second product adds up each token's experts itself.
+// More pairs: 128 columns quantized by the first product, the second writes
+// every pair's product, a third launch adds them up.
+inline bool few_pairs(int64_t T, int64_t k, int64_t I) { return T <= 16 && T * k * I <= 32768; }
 
 // Workspace layout, in bytes from its start.
 struct MoeLayout {
-    int64_t units, order, place, codes, scales, out, total;
+    int64_t units, order, place, codes, scales, hidden, out, total;
     MoeLayout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
         const int64_t P = T * k, U = std::min(P, E);
         auto up = [](int64_t v) { return (v + 255) & ~int64_t(255); };
@@ -42,9 +45,11 @@ struct MoeLayout {
         order = units + up(U * sizeof(MoeUnit));
         place = order + up(P * 4);
         codes = place + up(P * 4);
-        scales = codes + up(P * I);
-        out = scales + up(P * ((I / 128 + 3) & ~int64_t(3)) * 4);
-        total = out + (T > kFusedTokens ? up(P * H * 4) : 0);
+        const bool few = few_pairs(T, k, I);
+        scales = codes + (few ? 0 : up(P * I));
+        hidden = scales + (few ? 0 : up(P * ((I / 128 + 3) & ~int64_t(3)) * 4));
+        out = hidden + (few ? up(P * I * 4) : 0);
+        total = out + (few ? 0 : up(P * H * 4));
     }
 };
 
@@ -103,6 +108,32 @@ __device__ __forceinline__ MoeUnit find_unit(const int32_t* __restrict__ ids, in
     return u;
 }
 
+// Codes of four hidden values in a block whose largest magnitude has the bits
+// `top` (a NaN's are the largest), and the block's scale or exponent byte: the
+// per-token quantizer's recipe, with a NaN scale for a block that is not finite.
+template <bool kE8>
+__device__ __forceinline__ typename std::conditional<kE8, int, float>::type quantize_hidden(
+    uint32_t top, const v4f& v, uint32_t& codes) {
+    const float a = __uint_as_float(top);
+    const bool finite = top < 0x7f800000u;
+    float d[4];
+    if constexpr (kE8) {
+        const int ex = e8m0_exponent(a);
+        const float y = exp2_neg(finite ? ex : 0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) d[q] = v[q] * y;
+        codes = e4m3x4_hw(d[0], d[1], d[2], d[3]);
+        return finite ? ex + 127 : 255;
+    } else {
+        const float scale = a / 448.0f, y = 1.0f / scale;
+        const bool fast = scale >= 1.17549435e-38f && y <= 3.40282347e38f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) d[q] = fast ? quotient_rn(v[q], scale, y) : v[q] / scale;
+        codes = top != 0 ? e4m3x4_hw(d[0], d[1], d[2], d[3]) : 0u;
+        return finite ? scale : __builtin_nanf("");
+    }
+}
+
 // First product: silu(gate) * up, quantized per 128 hidden columns.  A
 // workgroup takes one 128-column block of one unit, up to 16 R rows at a time;
 // a wave multiplies its 16 gate and its 16 up rows of the weights by the same
@@ -110,30 +141,46 @@ __device__ __forceinline__ MoeUnit find_unit(const int32_t* __restrict__ ids, in
 //
 // The sums go through the bf16 matrix instruction (see multiply_exact): the
 // FP8 one would move about one code in 600 of the quantized result.
-template <int R, int D, bool kE8>
-__global__ __launch_bounds__(64 * kPanelWaves) void moe_gate_up_kernel(
+//
+// With four waves a workgroup takes 64 columns and leaves them in fp32, for
+// the second product to quantize: for a few pairs there are too few 128
+// column blocks to give every CU one, and a CU alone streams only 36 GB/s
+// (8 pairs of 7168 x 2048: 51 us with 128 workgroups of 128 columns).
+template <int R, int D, int W>
+constexpr size_t gate_lds() {
+    if constexpr (R <= 2)
+        return sizeof(FreePanel<R, 2, D, W>);
+    else
+        return panel_lds<R, 2, D>();
+}
+
+template <int R, int D, int W, bool kE8>
+__global__ __launch_bounds__(64 * W) void moe_gate_up_kernel(
     const uint8_t* __restrict__ x, const void* __restrict__ sx_v, const int32_t* __restrict__ ids,
     const uint8_t* __restrict__ w13, const void* __restrict__ s13_v, MoeUnit* __restrict__ units,
     int32_t* __restrict__ order, int32_t* __restrict__ place, uint8_t* __restrict__ codes,
-    void* __restrict__ scales, int P, int k, int E, int H, int I, bool by_pair) {
+    void* __restrict__ scales, float* __restrict__ hidden, int P, int k, int E, int H, int I,
+    bool by_pair) {
     using S = typename std::conditional<kE8, uint8_t, float>::type;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint16_t* const list = reinterpret_cast<uint16_t*>(smem + panel_lds<R, 2, D>());
+    constexpr bool kFree = R <= 2;
+    static_assert(W == kPanelWaves || (W == 4 && kFree), "whole 128-column blocks, or halves in fp32");
+    uint16_t* const list = reinterpret_cast<uint16_t*>(smem + gate_lds<R, D, W>());
     __shared__ uint32_t tops[16 * R][kPanelWaves];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
-    const MoeUnit u = find_unit<kPanelWaves>(ids, P, E, blockIdx.y, by_pair, reinterpret_cast<int*>(smem), list);
+    const MoeUnit u = find_unit<W>(ids, P, E, blockIdx.y, by_pair, reinterpret_cast<int*>(smem), list);
     if (blockIdx.x == 0 && threadIdx.x == 0) units[blockIdx.y] = u;
     if (u.count == 0) return;
     if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < u.count; i += 64 * kPanelWaves) {
+        for (int i = threadIdx.x; i < u.count; i += 64 * W) {
             order[u.start + i] = list[i];
             place[list[i]] = u.start + i;
         }
 
     const int KB = H >> 7, SP = scale_pitch<kE8>(KB), NB = I >> 6;  // scale rows of w13: 2I / 128
-    const int sub = lane >> 3, col = blockIdx.x * 128 + wave * 16;
+    const int sub = lane >> 3, col = blockIdx.x * 16 * W + wave * 16;
     const uint32_t chunk = panel_chunk(lane), kSz = sizeof(S);
     // every offset fits 31 bits: 2 I H <= 2^29, T H <= 2^22
     PanelLoads<2> p;
@@ -146,17 +193,24 @@ __global__ __launch_bounds__(64 * kPanelWaves) void moe_gate_up_kernel(
         p.offB[j] = (uint32_t)((j >> 1) * I + col + 8 * (j & 1) + sub) * (uint32_t)H + chunk;
 
     for (int m0 = 0; m0 < u.count; m0 += 16 * R) {
-        const int rows = min(u.count - m0, 16 * R), arow = 8 * wave + sub;
-        p.offA = arow < rows ? (uint32_t)(list[m0 + arow] / k) * (uint32_t)H + chunk : kNoRow;
+        const int rows = min(u.count - m0, 16 * R);
+#pragma unroll
+        for (int j = 0; j < (kFree ? panel_a_loads(R, W) : 1); ++j) {
+            const int arow = 8 * (kFree ? (wave * panel_a_loads(R, W) + j) % (2 * R) : wave) + sub;
+            p.offA[j] = arow < rows ? (uint32_t)(list[m0 + arow] / k) * (uint32_t)H + chunk : kNoRow;
+        }
         p.offS = wave == 0 && lane < rows ? (uint32_t)(list[m0 + lane] / k) * SP * kSz
-                 : wave == 1 && lane < 2  ? (uint32_t)((lane * I + blockIdx.x * 128) >> 7) * SP * kSz
+                 : wave == 1 && lane < 2  ? (uint32_t)((lane * I + (int)blockIdx.x * 16 * W) >> 7) * SP * kSz
                                           : kNoRow;
         v4f acc[R][2];
-        panel_product<R, 2, D, kE8, true>(smem, p, KB, rows, wave, lane, acc);
+        if constexpr (kFree)
+            free_panel_product<R, 2, D, W, kE8, true>(smem, p, KB, rows, wave, lane, acc);
+        else
+            panel_product<R, 2, D, kE8, true>(smem, p, KB, rows, wave, lane, acc);
 
         // silu(gate) * up, then the block's largest magnitude per row across
         // the waves, compared as bits so that a NaN wins
-        float h[R][4];
+        v4f h[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             uint32_t top = 0;
@@ -170,6 +224,14 @@ __global__ __launch_bounds__(64 * kPanelWaves) void moe_gate_up_kernel(
             top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
             if (lg == 0) tops[16 * r + lr][wave] = top;
         }
+        if constexpr (W != kPanelWaves) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (16 * r + lr < rows)
+                    *reinterpret_cast<v4f*>(hidden + (int64_t)(u.start + m0 + 16 * r + lr) * I + col + 4 * lg) =
+                        h[r];
+            continue;
+        }
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -178,26 +240,12 @@ __global__ __launch_bounds__(64 * kPanelWaves) void moe_gate_up_kernel(
 #pragma unroll
             for (int w = 0; w < kPanelWaves; ++w) top = max(top, tops[row][w]);
             if (row >= rows) continue;
-            const float a = __uint_as_float(top);
-            const bool finite = top < 0x7f800000u;
-            const float scale = a / 448.0f;
-            const int ex = kE8 ? e8m0_exponent(a) : 0;
-            const float y = kE8 ? exp2_neg(ex) : 1.0f / scale;
-            const bool fast = scale >= 1.17549435e-38f && y <= 3.40282347e38f;
-            float v[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                v[q] = kE8 ? h[r][q] * y : fast ? quotient_rn(h[r][q], scale, y) : h[r][q] / scale;
+            uint32_t packed;
+            const auto scale = quantize_hidden<kE8>(top, h[r], packed);
             const int64_t out = u.start + m0 + row;
-            *reinterpret_cast<uint32_t*>(codes + out * I + col + 4 * lg) =
-                (kE8 || top != 0) ? e4m3x4_hw(v[0], v[1], v[2], v[3]) : 0u;
-            if (wave == 0 && lg == 0) {
-                const int64_t to = out * scale_pitch<kE8>(I >> 7) + blockIdx.x;
-                if (kE8)
-                    static_cast<uint8_t*>(scales)[to] = finite ? (uint8_t)(ex + 127) : (uint8_t)255;
-                else
-                    static_cast<float*>(scales)[to] = finite ? scale : __builtin_nanf("");
-            }
+            *reinterpret_cast<uint32_t*>(codes + out * I + col + 4 * lg) = packed;
+            if (wave == 0 && lg == 0)
+                static_cast<S*>(scales)[out * scale_pitch<kE8>(I >> 7) + blockIdx.x] = (S)scale;
         }
         __syncthreads();  // tops have been read
     }
@@ -231,7 +279,7 @@ __global__ __launch_bounds__(64 * kPanelWaves) void moe_down_rows_kernel(
                      : buffer_rsrc(static_cast<const S*>(s2_v) + (int64_t)e * NB * SP, (uint32_t)NB * SP * kSz);
 #pragma unroll
         for (int j = 0; j < 2; ++j) p.offB[j] = (uint32_t)(col + 8 * j + sub) * (uint32_t)I + chunk;
-        p.offA = arow < rows ? (uint32_t)arow * (uint32_t)I + chunk : kNoRow;
+        p.offA[0] = arow < rows ? (uint32_t)arow * (uint32_t)I + chunk : kNoRow;
         p.offS = wave == 0 && lane < rows ? (uint32_t)lane * SP * kSz
                  : wave == 1 && lane == 0 ? (uint32_t)blockIdx.x * SP * kSz
                                           : kNoRow;
@@ -266,140 +314,192 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
     *reinterpret_cast<v2u*>(y + t * H + c) = packed;
 }
 
-// Second product and the weighted sum: a workgroup owns 16 columns of y for
-// every token.  Its waves split the list of (16 R rows of an expert, K block)
-// steps evenly and add their weighted products to an LDS slice of their own
+// Second product of a few pairs with the weighted sum: a workgroup owns 16
+// columns of y for every token.  It quantizes the hidden rows into LDS for
+// itself (at most 32 K values, from L2, behind the first weights), then its
+// waves split the list of (up to 16 rows of an expert, K block) steps evenly,
+// each streaming its share of the weights through a ring of its own in LDS,
+// with no barrier.  A wave adds its weighted products to a slice of its own
 // ([token][16] fp32); the slices are summed in wave order at the end.
-template <int R, bool kE8, int W>
-__global__ __launch_bounds__(64 * W) void moe_down_kernel(
-    const uint8_t* __restrict__ codes, const void* __restrict__ sh_v, const float* __restrict__ weights,
-    const uint8_t* __restrict__ w2, const void* __restrict__ s2_v, const MoeUnit* __restrict__ units,
-    const int32_t* __restrict__ order, uint16_t* __restrict__ y, int T, int U, int k, int H, int I) {
+constexpr int kDownWaves = 8, kDownRing = 3;
+
+struct MoeDownLds {
+    int ring, codes, scales, cols, slices, row_w, jobs, row_t, total;
+    __host__ __device__ MoeDownLds(int T, int P, int U, int I) {
+        ring = 0;
+        codes = kDownWaves * kDownRing * 2048;        // [P][I], chunk c of row r at c ^ (r & 7)
+        scales = codes + P * I;                       // [P][I / 128]
+        cols = scales + P * (I >> 7) * 4;             // [jobs][I / 128]
+        slices = cols + (U + P / 16) * (I >> 7) * 4;  // [wave][T][16]
+        slices = (slices + 15) & ~15;
+        row_w = slices + kDownWaves * T * 64;
+        jobs = row_w + ((P + 1) & ~1) * 4;
+        row_t = jobs + (U + P / 16) * (int)sizeof(MoeJob);
+        total = row_t + P * 2;
+    }
+};
+
+template <bool kE8>
+__global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(
+    const float* __restrict__ hidden, const float* __restrict__ weights, const uint8_t* __restrict__ w2,
+    const void* __restrict__ s2_v, const MoeUnit* __restrict__ units, const int32_t* __restrict__ order,
+    uint16_t* __restrict__ y, int T, int U, int k, int H, int I) {
+    constexpr int W = kDownWaves, D = kDownRing;
     using S = typename std::conditional<kE8, uint8_t, float>::type;
-    const S* sh = static_cast<const S*>(sh_v);
+    using V = typename std::conditional<kE8, int, float>::type;
     const S* s2 = static_cast<const S*>(s2_v);
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int P = T * k;
-    float* const slices = reinterpret_cast<float*>(smem);                      // [W][T][16]
-    float* const row_w = slices + W * T * 16;                                  // [P]
-    MoeJob* const jobs = reinterpret_cast<MoeJob*>(row_w + ((P + 3) & ~3));  // [U + P / (16 R)]
-    uint16_t* const row_t = reinterpret_cast<uint16_t*>(jobs + U + P / (16 * R));  // [P]
+    const MoeDownLds at(T, P, U, I);
+    uint8_t* const codes = smem + at.codes;
+    V* const scales = reinterpret_cast<V*>(smem + at.scales);
+    V* const cols = reinterpret_cast<V*>(smem + at.cols);
+    float* const slices = reinterpret_cast<float*>(smem + at.slices);
+    float* const row_w = reinterpret_cast<float*>(smem + at.row_w);
+    MoeJob* const jobs = reinterpret_cast<MoeJob*>(smem + at.jobs);
+    uint16_t* const row_t = reinterpret_cast<uint16_t*>(smem + at.row_t);
     __shared__ int totals[2];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
-    for (int i = threadIdx.x; i < W * T * 16; i += 64 * W) slices[i] = 0.0f;
     if (wave == 0) {
         int n = 0, rows = 0;
         for (int base = 0; base < U; base += 64) {
             MoeUnit u = {0, 0, 0, 0};
             if (base + lane < U) u = units[base + lane];
-            const int c = (u.count + 16 * R - 1) / (16 * R);
-            int at = c, sum = u.count;
+            const int c = (u.count + 15) / 16;
+            int sum_c = c, sum_r = u.count;  // inclusive sums over the lanes
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(at, d, 64), s = __shfl_up(sum, d, 64);
+                const int oc = __shfl_up(sum_c, d, 64), orow = __shfl_up(sum_r, d, 64);
                 if (lane >= d) {
-                    at += o;
-                    sum += s;
+                    sum_c += oc;
+                    sum_r += orow;
                 }
             }
             for (int i = 0; i < c; ++i)
-                jobs[n + at - c + i] = MoeJob{u.e, (uint16_t)(u.start + 16 * R * i),
-                                              (uint16_t)min(16 * R, u.count - 16 * R * i)};
-            n += __shfl(at, 63, 64);
-            rows += __shfl(sum, 63, 64);
+                jobs[n + sum_c - c + i] = MoeJob{u.e, (uint16_t)(u.start + 16 * i), (uint16_t)min(16, u.count - 16 * i)};
+            n += __shfl(sum_c, 63, 64);
+            rows += __shfl(sum_r, 63, 64);
         }
         if (lane == 0) {
             totals[0] = n;
             totals[1] = rows;
         }
     }
+    for (int i = threadIdx.x; i < W * T * 16; i += 64 * W) slices[i] = 0.0f;
     __syncthreads();
     const int n_jobs = __builtin_amdgcn_readfirstlane(totals[0]);
     const int n_rows = __builtin_amdgcn_readfirstlane(totals[1]);
+    const int KB = I >> 7, SP = scale_pitch<kE8>(KB), n0 = blockIdx.x * 16, NB = H >> 7;
+    const int first = wave * n_jobs * KB / W, last = (wave + 1) * n_jobs * KB / W;
+
+    // the loader runs D - 1 steps ahead of the multiplier, each with its own
+    // place (job, K block) in the list; past the wave's share it loads nothing
+    uint8_t* const ring = smem + at.ring + wave * D * 2048;
+    const uint32_t off0 = (uint32_t)(n0 + (lane >> 3)) * (uint32_t)I + panel_chunk(lane);
+    int lj = KB > 0 && n_jobs > 0 ? first / KB : 0, lk = first - lj * KB, ls = first;
+    v4u buf = buffer_rsrc(w2, 0);
+    if (ls < last)
+        buf = buffer_rsrc(w2 + (int64_t)__builtin_amdgcn_readfirstlane(jobs[lj].e) * H * I, (uint32_t)H * (uint32_t)I);
+    auto issue = [&](int slot) __attribute__((always_inline)) {
+        const bool real = ls < last;
+        load_lds_16(buf, real ? off0 + lk * 128 : kNoRow, ring + slot * 2048);
+        load_lds_16(buf, real ? off0 + 8 * I + lk * 128 : kNoRow, ring + slot * 2048 + 1024);
+        ++ls;
+        if (++lk == KB) {
+            lk = 0;
+            ++lj;
+            if (ls < last)
+                buf = buffer_rsrc(w2 + (int64_t)__builtin_amdgcn_readfirstlane(jobs[lj].e) * H * I,
+                                  (uint32_t)H * (uint32_t)I);
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) issue(d);
+
+    // 16 lanes quantize one 128-column block of one row, 8 columns each; a
+    // thread's first loads are all in flight before anything waits
+    constexpr int kBatch = 4;
+    const int per_row = I >> 3, items = n_rows * per_row;
+    v4f v[kBatch][2];
+    auto fetch = [&](int base) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n) {
+            const int i = base + n * 64 * W + threadIdx.x;
+            const float* const from = hidden + (i < items ? (int64_t)i * 8 : 0);
+            v[n][0] = *reinterpret_cast<const v4f*>(from);
+            v[n][1] = *reinterpret_cast<const v4f*>(from + 4);
+        }
+    };
+    fetch(0);
     for (int i = threadIdx.x; i < n_rows; i += 64 * W) {
         const int q = order[i];
         row_w[i] = weights[q];
         row_t[i] = (uint16_t)(q / k);
     }
-    __syncthreads();
-
-    const int KB = I >> 7, SP = scale_pitch<kE8>(KB), n0 = blockIdx.x * 16, NB = H >> 7;
-    const int first = (int)((int64_t)wave * n_jobs * KB / W);
-    const int last = (int)((int64_t)(wave + 1) * n_jobs * KB / W);
-    float* const mine = slices + wave * T * 16;
-    if (first < last) {
-        constexpr int D = R == 1 ? 4 : 2;
-        Block<R, 1, kE8> ring[D];
-        // the loader runs D steps ahead of the multiplier, each with its own
-        // place (job, K block) in the list
-        int lj = first / KB, lk = first % KB;
-        const auto hbuf = buffer_of(codes, (int64_t)P * I);
-        const uint8_t* b;
-        uint32_t a[R];
-        const S *sb, *sa[R];
-        auto aim = [&](int j) __attribute__((always_inline)) {
-            const int e = __builtin_amdgcn_readfirstlane(jobs[j].e);
-            const int start = __builtin_amdgcn_readfirstlane(jobs[j].start);
-            const int count = __builtin_amdgcn_readfirstlane(jobs[j].count);
-            b = w2 + ((int64_t)e * H + n0 + lr) * I + lg * 16;
-            sb = s2 + ((int64_t)e * NB + (n0 >> 7)) * SP;
+    for (int i = threadIdx.x; i < n_jobs * KB; i += 64 * W)
+        cols[i] = s2[((int64_t)jobs[i / KB].e * NB + (n0 >> 7)) * SP + i % KB];
+    for (int base = 0; base < items; base += kBatch * 64 * W) {
+        if (base > 0) fetch(base);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int row = start + min(16 * r + lr, count - 1);
-                a[r] = 16 * r + lr < count ? (uint32_t)(row * I + lg * 16) : kNoRow;
-                sa[r] = sh + (int64_t)row * SP;
-            }
-        };
-        auto load = [&](Block<R, 1, kE8>& s) __attribute__((always_inline)) {
-            load_chunks(b + lk * 128, s.b[0]);
-            s.sb[0] = sb[lk];
+        for (int n = 0; n < kBatch; ++n) {
+            const int i = base + n * 64 * W + threadIdx.x;
+            if (i >= items) break;  // uniform over each 16 lanes
+            const int row = i / per_row, c = i - row * per_row;
+            uint32_t top = 0;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                load_chunks(hbuf, a[r] + lk * 128, s.a[r]);
-                s.sa[r] = sa[r][lk];
-            }
-            if (++lk == KB) {
-                lk = 0;
-                lj = min(lj + 1, n_jobs - 1);
-                aim(lj);
-            }
-        };
-        aim(lj);
+            for (int q = 0; q < 8; ++q) top = max(top, __float_as_uint(v[n][q >> 2][q & 3]) & 0x7fffffffu);
 #pragma unroll
-        for (int d = 0; d < D; ++d) load(ring[d]);
-        int j = first / KB, kb = first % KB;
-        v4f acc[R][1];
-        clear(acc);
-        for (int s = first; s < last; s += D) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                if (s + d < last) {
-                    const int rows = __builtin_amdgcn_readfirstlane(jobs[j].count);
-                    multiply(ring[d], rows, acc);
-                    if (++kb == KB || s + d + 1 == last) {
-                        const int start = __builtin_amdgcn_readfirstlane(jobs[j].start);
-#pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            const int i = 16 * r + lr;
-                            if (i < rows) {
-                                // two rows may be one token: LDS adds, in lane order
-                                const float w = row_w[start + i];
-                                float* const to = mine + row_t[start + i] * 16 + 4 * lg;
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) atomicAdd(to + q, w * acc[r][0][q]);
-                            }
-                        }
-                        clear(acc);
-                        kb = 0;
-                        ++j;
-                    }
-                }
-                load(ring[d]);
-            }
+            for (int d = 8; d >= 1; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 16));
+            uint32_t w[2];
+            const V s = quantize_hidden<kE8>(top, v[n][0], w[0]);
+            quantize_hidden<kE8>(top, v[n][1], w[1]);
+            const int in = (c & 15) * 8;  // byte in the 128-byte block
+            uint8_t* const to = codes + row * I + (c >> 4) * 128 + ((((in >> 4) ^ row) & 7) << 4) + (in & 15);
+            *reinterpret_cast<v2u*>(to) = v2u{w[0], w[1]};
+            if ((c & 15) == 0) scales[row * KB + (c >> 4)] = s;
         }
     }
+    __syncthreads();
+
+    float* const mine = slices + wave * T * 16;
+    const int lo = (lg ^ (lr & 7)) << 4, hi = lo ^ 64;
+    int j = first < last ? first / KB : 0, kb = first - j * KB, slot = 0;
+    v4f acc[1][1];
+    clear(acc);
+    for (int s = first; s < last; ++s) {
+        wait_vmcnt_lgkm0<2 * (D - 2)>();
+        asm volatile("" ::: "memory");
+        issue(slot == 0 ? D - 1 : slot - 1);
+        const int count = __builtin_amdgcn_readfirstlane(jobs[j].count);
+        const int start = __builtin_amdgcn_readfirstlane(jobs[j].start);
+        const int row = start + min(lr, count - 1);
+        const uint8_t* const pb = ring + slot * 2048 + lr * 128;
+        const uint8_t* const pa = codes + row * I + kb * 128;
+        Block<1, 1, kE8> f;
+        f.b[0][0] = *reinterpret_cast<const v4u*>(pb + lo);
+        f.b[0][1] = *reinterpret_cast<const v4u*>(pb + hi);
+        f.a[0][0] = *reinterpret_cast<const v4u*>(pa + ((lg ^ (row & 7)) << 4));
+        f.a[0][1] = *reinterpret_cast<const v4u*>(pa + (((lg + 4) ^ (row & 7)) << 4));
+        f.sa[0] = scales[row * KB + kb];
+        f.sb[0] = cols[j * KB + kb];
+        multiply(f, 16, acc);
+        slot = slot == D - 1 ? 0 : slot + 1;
+        if (++kb == KB || s + 1 == last) {
+            if (lr < count) {
+                // two rows may be one token: LDS adds, in lane order
+                const float w = row_w[start + lr];
+                float* const to = mine + row_t[start + lr] * 16 + 4 * lg;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) atomicAdd(to + q, w * acc[0][0][q]);
+            }
+            clear(acc);
+            kb = 0;
+            ++j;
+        }
+    }
+    wait_vmcnt_lgkm0<0>();  // the empty loads of the last steps have retired
     __syncthreads();
     for (int i = threadIdx.x; i < T * 8; i += 64 * W) {
         const int t = i >> 3, c = (i & 7) * 2;
@@ -415,45 +515,55 @@ int64_t moe_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     return MoeLayout(T, k, E, H, I).total;
 }
 
-template <int R, bool kE8>
-static dg_status moe_r(const MoeArgs& a, hipStream_t stream) {
+template <bool kE8>
+static dg_status moe_few(const MoeArgs& a, hipStream_t stream) {
     const MoeLayout at(a.T, a.k, a.E, a.H, a.I);
     uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
     MoeUnit* const units = reinterpret_cast<MoeUnit*>(ws + at.units);
     int32_t* const order = reinterpret_cast<int32_t*>(ws + at.order);
-    int32_t* const place = reinterpret_cast<int32_t*>(ws + at.place);
-    uint8_t* const codes = ws + at.codes;
-    void* const scales = ws + at.scales;
+    float* const hidden = reinterpret_cast<float*>(ws + at.hidden);
     const int P = a.T * a.k, U = std::min(P, a.E);
-    constexpr int D = R == 4 ? 3 : 4;
-    hipLaunchKernelGGL((moe_gate_up_kernel<R, D, kE8>), dim3(a.I / 128, U), dim3(64 * kPanelWaves),
-                       (panel_lds<R, 2, D>()) + P * 2, stream, a.x, a.sx, a.ids, a.w13, a.s13, units, order,
-                       place, codes, scales,
+    constexpr int D = 4, W = 4;
+    hipLaunchKernelGGL((moe_gate_up_kernel<1, D, W, kE8>), dim3(a.I / 64, U), dim3(64 * W),
+                       (gate_lds<1, D, W>()) + P * 2, stream, a.x, a.sx, a.ids, a.w13, a.s13, units, order,
+                       reinterpret_cast<int32_t*>(ws + at.place), nullptr, nullptr, hidden, P, a.k, a.E, a.H,
+                       a.I, P <= a.E);
+    if (launched() != DG_OK) return DG_ERR_HIP;
+    hipLaunchKernelGGL((moe_down_kernel<kE8>), dim3(a.H / 16), dim3(64 * kDownWaves),
+                       MoeDownLds(a.T, P, U, a.I).total, stream, hidden, a.weights, a.w2, a.s2, units, order,
+                       a.y, a.T, U, a.k, a.H, a.I);
+    return launched();
+}
+
+template <int R, bool kE8>
+static dg_status moe_many(const MoeArgs& a, hipStream_t stream) {
+    const MoeLayout at(a.T, a.k, a.E, a.H, a.I);
+    uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
+    MoeUnit* const units = reinterpret_cast<MoeUnit*>(ws + at.units);
+    int32_t* const place = reinterpret_cast<int32_t*>(ws + at.place);
+    float* const out = reinterpret_cast<float*>(ws + at.out);
+    const int P = a.T * a.k, U = std::min(P, a.E);
+    constexpr int D = R == 1 ? 4 : 3, D2 = 3;
+    hipLaunchKernelGGL((moe_gate_up_kernel<R, D, kPanelWaves, kE8>), dim3(a.I / 128, U), dim3(64 * kPanelWaves),
+                       (gate_lds<R, D, kPanelWaves>()) + P * 2, stream, a.x, a.sx, a.ids, a.w13, a.s13, units,
+                       reinterpret_cast<int32_t*>(ws + at.order), place, ws + at.codes, ws + at.scales, nullptr,
                        P, a.k, a.E, a.H, a.I, P <= a.E);
-    const dg_status s = launched();
-    if (s != DG_OK) return s;
-    if (a.T > kFusedTokens) {
-        float* const out = reinterpret_cast<float*>(ws + at.out);
-        constexpr int D2 = 3;
-        hipLaunchKernelGGL((moe_down_rows_kernel<R, D2, kE8>), dim3(a.H / 128, U), dim3(64 * kPanelWaves),
-                           (panel_lds<R, 1, D2>()), stream, codes, scales, a.w2, a.s2, units, out, P, a.H, a.I);
-        if (launched() != DG_OK) return DG_ERR_HIP;
-        hipLaunchKernelGGL(moe_combine_kernel, dim3((a.H + 1023) / 1024, a.T), dim3(256), 0, stream, out, a.ids,
-                           place, a.weights, a.y, a.k, a.E, a.H);
-        return launched();
-    }
-    constexpr int W = 4;
-    const size_t lds = W * a.T * 64 + ((P + 3) & ~3) * 4 + (U + P / (16 * R)) * sizeof(MoeJob) + P * 2;
-    hipLaunchKernelGGL((moe_down_kernel<R, kE8, W>), dim3(a.H / 16), dim3(64 * W), lds, stream, codes,
-                       scales, a.weights, a.w2, a.s2, units, order, a.y, a.T, U, a.k, a.H, a.I);
+    if (launched() != DG_OK) return DG_ERR_HIP;
+    hipLaunchKernelGGL((moe_down_rows_kernel<R, D2, kE8>), dim3(a.H / 128, U), dim3(64 * kPanelWaves),
+                       (panel_lds<R, 1, D2>()), stream, ws + at.codes, ws + at.scales, a.w2, a.s2, units, out, P,
+                       a.H, a.I);
+    if (launched() != DG_OK) return DG_ERR_HIP;
+    hipLaunchKernelGGL(moe_combine_kernel, dim3((a.H + 1023) / 1024, a.T), dim3(256), 0, stream, out, a.ids, place,
+                       a.weights, a.y, a.k, a.E, a.H);
     return launched();
 }
 
 template <bool kE8>
 static dg_status moe_scales(const MoeArgs& a, hipStream_t stream) {
-    if (a.T <= 16) return moe_r<1, kE8>(a, stream);
-    if (a.T <= 32) return moe_r<2, kE8>(a, stream);
-    return moe_r<4, kE8>(a, stream);
+    if (few_pairs(a.T, a.k, a.I)) return moe_few<kE8>(a, stream);
+    if (a.T <= 16) return moe_many<1, kE8>(a, stream);
+    if (a.T <= 32) return moe_many<2, kE8>(a, stream);
+    return moe_many<4, kE8>(a, stream);
 }
 
 dg_status launch_moe(const MoeArgs& a, bool e8m0, hipStream_t stream) {

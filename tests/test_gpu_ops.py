@@ -382,3 +382,29 @@ def test_binding_refusals():
     m["sx"] = m["sx"].astype(np.float64)
     with pytest.raises(TypeError):
         run_moe(m, "fp32")
+
+
+@pytest.mark.parametrize("kind", ["fp32", "e8m0"])
+@pytest.mark.parametrize("T", [2, 12, 40])
+def test_moe_infinities_and_nans_stay_in_their_tokens(T, kind):
+    """A NaN code, or an activation that overflows, makes its token's row NaN and no other."""
+    c = moe_case(13, T, 2, 3, 256, 512, kind)
+    want, tol = ref.moe(*[c[n] for n in MOE_ORDER], kind)
+    c["x"][1, 77] = 0x7F                   # NaN
+    if T > 2:
+        c["sx"][5, :] = 254 if kind == "e8m0" else 3e38   # gate * up is past the largest fp32
+    got = host(run_moe(c, kind))
+    hit = np.zeros(T, bool)
+    hit[1] = True
+    hit[5:6] = T > 2
+    assert np.isnan(got[hit]).all()
+    assert (np.abs(got - want)[~hit] <= (tol + ref.BF16 * (np.abs(want) + tol))[~hit]).all()
+
+
+def test_moe_zero_rows_give_zeros():
+    for T in (3, 30):
+        c = moe_case(14, T, 2, 3, 128, 256, "fp32")
+        c["x"][0] = 0
+        c["sx"][0] = 0
+        assert (host(run_moe(c, "fp32"))[0] == 0).all()
+        check_moe(c, "fp32")
