@@ -76,7 +76,8 @@ dg_status moe(const uint8_t* x, const void* sx, const int32_t* ids, const float*
 
 dg_status check_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     if (N <= 0 || N % 8 != 0 || N >= (int64_t(1) << 22)) return DG_ERR_SHAPE;
-    if (K <= 0 || K % 128 != 0 || K >= (int64_t(1) << 24)) return DG_ERR_SHAPE;
+    // an adapter's R <= 128 rows of K bf16 are addressed with 31-bit offsets
+    if (K <= 0 || K % 128 != 0 || K >= (int64_t(1) << 23)) return DG_ERR_SHAPE;
     if (M < 0 || M > 0x7fffffffLL || L < 1 || L > 65536) return DG_ERR_SHAPE;
     if (R < 8 || R > 128 || R % 8 != 0) return DG_ERR_SHAPE;
     return DG_OK;
@@ -89,7 +90,7 @@ dg_status lora(const uint8_t* A, const void* sa, const uint8_t* B, const void* s
     dg_status s = check_lora(M, N, K, L, R);
     if (s != DG_OK) return s;
     if (M == 0) return DG_OK;
-    if (workspace_bytes < dg::lora_workspace(M, N, K, R)) return DG_ERR_SHAPE;
+    if (workspace_bytes < dg::lora_workspace(M, N, K, L, R)) return DG_ERR_SHAPE;
     s = check_ptrs({A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling, workspace});
     if (s != DG_OK) return s;
     const dg::LoraArgs a{A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling, M, N, K, (int)L, (int)R,
@@ -180,7 +181,7 @@ dg_status dg_fp8_gemm_nt_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t
     const dg_status s = check_lora(M, N, K, L, R);
     if (s != DG_OK) return s;
     if (bytes == nullptr) return DG_ERR_NULL;
-    *bytes = dg::lora_workspace(M, N, K, R);
+    *bytes = dg::lora_workspace(M, N, K, L, R);
     return DG_OK;
 }
 

@@ -207,75 +207,123 @@ __device__ __forceinline__ bool decode_tile(int b, int m_blocks, int n_blocks, i
     return true;
 }
 
-// The adapter term of a tile (DenseLora): the wave walks the distinct adapters
-// of its rows; for each, a lane multiplies its row's rank-R vector by 16-row
-// tiles of that adapter's second matrix with bf16 MFMA and keeps the product
-// where the row is the adapter's own (a select, not a zeroed operand, so that
-// an infinity or NaN in one request's adapter stays in that request's rows).
-// The vector is fp32; it enters as the sum of two bf16 parts, which leaves an
-// error of 2^-17 of it, far below the final rounding to bf16.
+// The adapter term of a tile (DenseLora), once the K loop has left LDS free.
+// The workgroup walks the distinct adapters of its rows, 64 of the rank at a
+// time: the rows' vectors are staged once as two bf16 slabs in the A stages
+// (64 bf16 are 128 bytes: a slab's layout is the FP8 one's), each adapter's
+// second matrix through the two B stages by direct loads, the next one behind
+// the current one's products.  A lane keeps a product where its row is the
+// adapter's own (a select, not a zeroed operand, so that an infinity or NaN in
+// one request's adapter stays in that request's rows).  The vector is fp32; as
+// a sum of two bf16 parts it is off by at most 2^-17, far below the final
+// rounding to bf16.  Each adapter of a tile costs about one load latency.
 template <class T>
-__device__ __forceinline__ void add_lora(v4f (&acc)[T::TM][T::TN], const LoraTail& lora, int lane,
-                                         int wm, int wcol, const TileInfo& ti, int64_t rows,
-                                         int64_t N) {
+__device__ __forceinline__ void add_lora(v4f (&acc)[T::TM][T::TN], uint8_t* smem, int* ids, const LoraTail& lora,
+                                         int tid, int wave, int lane, int wm, int wcol, const TileInfo& ti,
+                                         int64_t rows, int64_t N) {
     typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-    const int lr = lane & 15, lg = lane >> 4;
-    int id[T::TM];
-#pragma unroll
-    for (int i = 0; i < T::TM; ++i) {
-        const int row = 16 * (T::WAVES_M * i + wm) + lr;
-        id[i] = row < ti.valid ? lora.ids[ti.arow0 + row] : -1;
-        if (id[i] < 0 || id[i] >= lora.L) id[i] = 0x7fffffff;
+    constexpr int kNone = 0x7fffffff;
+    const int lr = lane & 15, lg = lane >> 4, R = lora.R;
+    for (int r = tid; r < T::BM; r += T::kThreads) {
+        const int id = r < ti.valid ? lora.ids[ti.arow0 + r] : -1;
+        ids[r] = id >= 0 && id < lora.L ? id : kNone;
     }
-    for (int after = -1;;) {
-        int cur = 0x7fffffff;
+    __syncthreads();
+    // the lowest adapter above `after` among the tile's rows, the same for every wave
+    auto next_id = [&](int after) __attribute__((always_inline)) {
+        int low = kNone;
+        for (int r = lane; r < T::BM; r += 64)
+            if (ids[r] > after) low = min(low, ids[r]);
 #pragma unroll
-        for (int i = 0; i < T::TM; ++i)
-            if (id[i] > after) cur = min(cur, id[i]);
+        for (int d = 32; d >= 1; d >>= 1) low = min(low, __shfl_xor(low, d, 64));
+        return __builtin_amdgcn_readfirstlane(low);
+    };
+    const int first = next_id(-1);
+    if (first == kNone) return;
+    const int sub = lane >> 3, lchunk = (lane & 7) ^ sub;
+    const int vn = (int)min<int64_t>(T::BN, N - ti.n0);
+    const int chunk_lo = (lg ^ (lr & 7)) << 4, chunk_hi = chunk_lo ^ 64;
+    for (int k0 = 0; k0 < R; k0 += 64) {
+        auto issue = [&](int id, int buf) __attribute__((always_inline)) {
+            const v4u rs = buffer_rsrc(lora.lora_b + ((int64_t)id * N + ti.n0) * R, (uint32_t)(vn * R * 2));
+            const bool in = 8 * lchunk + k0 < R;  // chunks past the rank read as zero
 #pragma unroll
-        for (int d = 8; d >= 1; d >>= 1) cur = min(cur, __shfl_xor(cur, d, 64));
-        cur = __builtin_amdgcn_readfirstlane(cur);
-        if (cur == 0x7fffffff) return;
-        after = cur;
-        const uint16_t* const b = lora.lora_b + ((int64_t)cur * N + ti.n0 + wcol) * lora.R;
-#pragma unroll
-        for (int i = 0; i < T::TM; ++i) {
-            if (__ballot(id[i] == cur) == 0) continue;
-            const int64_t row = ti.arow0 + min(16 * (T::WAVES_M * i + wm) + lr, ti.valid - 1);
-            v4f sum[T::TN];
-#pragma unroll
-            for (int j = 0; j < T::TN; ++j) sum[j] = v4f{0.f, 0.f, 0.f, 0.f};
-            for (int k0 = 0; k0 < lora.R; k0 += 32) {
-                const int k = k0 + 8 * lg;
-                float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (k < lora.R && id[i] == cur) {
-                    for (int p = 0; p < lora.parts; ++p) {
-                        const float* v = lora.low + ((int64_t)p * rows + row) * lora.R + k;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) f[q] += v[q];
-                    }
-                }
-                v8bf hi, lo;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    hi[q] = (__bf16)f[q];
-                    lo[q] = (__bf16)(f[q] - (float)hi[q]);
-                }
-#pragma unroll
-                for (int j = 0; j < T::TN; ++j) {
-                    v4u raw = {0u, 0u, 0u, 0u};
-                    if (k < lora.R && ti.n0 + wcol + 16 * j + lr < N)
-                        raw = *reinterpret_cast<const v4u*>(b + (int64_t)(16 * j + lr) * lora.R + k);
-                    const v8bf bf = __builtin_bit_cast(v8bf, raw);
-                    sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf, hi, sum[j], 0, 0, 0);
-                    sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf, lo, sum[j], 0, 0, 0);
-                }
+            for (int i = 0; i < T::kLoadsB; ++i) {
+                if ((T::BN / 8) % T::kWaves != 0 && wave + i * T::kWaves >= T::BN / 8) break;
+                const int row = (wave + i * T::kWaves) * 8;
+                load_lds_16(rs, in ? (uint32_t)((row + sub) * R + 8 * lchunk + k0) * 2 : 0x80000000u,
+                            smem + 2 * T::kStageA + buf * T::kStageB + row * 128);
             }
-            if (id[i] == cur) {
+        };
+        issue(first, 0);
+        for (int i = tid; i < T::BM * 8; i += T::kThreads) {
+            const int r = i >> 3, c = i & 7;
+            v4f f[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            if (ids[r] != kNone && 8 * c + k0 < R)
+                for (int p = 0; p < lora.parts; ++p) {
+                    const float* v = lora.low + ((int64_t)p * rows + ti.arow0 + r) * R + k0 + 8 * c;
+                    f[0] += *reinterpret_cast<const v4f*>(v);
+                    f[1] += *reinterpret_cast<const v4f*>(v + 4);
+                }
+            v8bf hi, lo;
 #pragma unroll
-                for (int j = 0; j < T::TN; ++j) acc[i][j] += sum[j];
+            for (int q = 0; q < 8; ++q) {
+                hi[q] = (__bf16)f[q >> 2][q & 3];
+                lo[q] = (__bf16)(f[q >> 2][q & 3] - (float)hi[q]);
             }
+            uint8_t* const to = smem + r * 128 + ((c ^ (r & 7)) << 4);
+            *reinterpret_cast<v8bf*>(to) = hi;
+            *reinterpret_cast<v8bf*>(to + T::kStageA) = lo;
         }
+        int buf = 0;
+        for (int cur = first; cur != kNone; buf ^= 1) {
+            const int after = next_id(cur);
+            // the current adapter's slab has landed for every wave, and every
+            // wave is done with the one that the next loads replace
+            wait_vmcnt_lgkm0<0>();
+            lds_barrier();
+            if (after != kNone) issue(after, buf ^ 1);
+            const uint8_t* const pb = smem + 2 * T::kStageA + buf * T::kStageB + (wcol + lr) * 128;
+            // two column tiles at a time, one row tile after the other: the
+            // accumulators leave few registers (hoisted reads spill them)
+            constexpr int kCols = T::TN % 2 == 0 ? 2 : 1;
+#pragma unroll
+            for (int j0 = 0; j0 < T::TN; j0 += kCols) {
+                v8bf b[kCols][2];
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) {
+                    b[j][0] = *reinterpret_cast<const v8bf*>(pb + (j0 + j) * 2048 + chunk_lo);
+                    b[j][1] = *reinterpret_cast<const v8bf*>(pb + (j0 + j) * 2048 + chunk_hi);
+                }
+#pragma unroll
+                for (int i = 0; i < T::TM; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    const int row = 16 * (T::WAVES_M * i + wm) + lr;
+                    const bool own = ids[row] == cur;
+                    if (__ballot(own) == 0) continue;
+                    const uint8_t* const pv = smem + row * 128;
+                    v4f sum[kCols];
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) sum[j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const v8bf v0 = *reinterpret_cast<const v8bf*>(pv + h * T::kStageA + chunk_lo);
+                        const v8bf v1 = *reinterpret_cast<const v8bf*>(pv + h * T::kStageA + chunk_hi);
+#pragma unroll
+                        for (int j = 0; j < kCols; ++j) {
+                            sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][0], v0, sum[j], 0, 0, 0);
+                            sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][1], v1, sum[j], 0, 0, 0);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j)
+                        if (own) acc[i][j0 + j] += sum[j];
+                }
+            }
+            cur = after;
+        }
+        wait_vmcnt_lgkm0<0>();
+        lds_barrier();  // the slabs have been read
     }
 }
 
@@ -628,7 +676,8 @@ __global__ __launch_bounds__(T::kThreads, 2) void gemm_kernel(
         // ---- epilogue
         wait_vmcnt<0>();  // the empty loads of the last steps have retired
         lds_barrier();
-        if constexpr (kForm == Form::DenseLora) add_lora<T>(acc, tail, lane, wm, wcol, ti, rows, N);
+        if constexpr (kForm == Form::DenseLora)
+            add_lora<T>(acc, smem, reinterpret_cast<int*>(smSA), tail, tid, wave, lane, wm, wcol, ti, rows, N);
         store_tile<T, kForm>(acc, smem, tid, wm, wcol, lr, lg, ti, C, D, N);
         if constexpr (!kMixed) {
             break;

@@ -1,118 +1,359 @@
-// A shared projection with each row's own low-rank adapter: the first small
-// product here, the second in the epilogue of the dense GEMM (gemm.hip).
-// include/dg_ops.h has the definition.
+// A shared projection with each row's own low-rank adapter.  include/dg_ops.h
+// has the definition.
+//
+// Many rows: the adapters' first product (the shrink) here, the second in the
+// epilogue of the dense GEMM (gemm.hip).  A few rows: one launch streams the
+// shared weights, K split over workgroups, beside the shrink's workgroups; a
+// second adds the parts and the adapters' second product.
 #include "ops_launch.h"
 
 #include <algorithm>
+#include <type_traits>
 
-#include "device_common.h"
+#include "fewrow.h"
 
 namespace dg {
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+constexpr int kMaxParts = 8;  // of the shrink's K
 
-constexpr int kShrinkWaves = 4;
+// Shape of the shrink for RT tiles of 16 ranks: RX tiles of 16 rows, W waves
+// with a ring of D stages each, a stage being 2 KB per tile of x and of the
+// adapter.  Beside the few-row product two workgroups share a CU's LDS; alone,
+// a workgroup takes it for itself and reads each adapter for twice the rows.
+template <int RT, bool kMany>
+struct ShrinkShape {
+    static constexpr int RX = kMany && RT <= 4 ? 2 : 1;
+    static constexpr int W = kMany ? (RT == 1 ? 8 : 4) : (RT == 8 ? 2 : 4);
+    static constexpr int D = kMany ? (RT == 2 ? 4 : RT == 8 ? 2 : 3) : (RT == 1 ? 4 : RT == 2 ? 3 : 2);
+    static constexpr int kStage = (RX + RT) * 2048;
+    static constexpr int kLds = W * D * kStage;
+    static constexpr int kPitch = 16 * RT + 4;
+    static_assert(W * 16 * RX * kPitch * 4 <= kLds, "the waves' sums fit the ring");
+};
+
+struct ShrinkArgs {
+    const uint16_t *x, *lora_a;
+    const int32_t* ids;
+    const float* scaling;
+    float* low;  // [parts][M][R]
+    int64_t M, K;
+    int L, R;
+    int blocks, slots, parts;
+};
 
 // low[part][m][0..R) = scaling[a] * x_m lora_a[a]^T over the part's share of K,
-// for the rows m that have an adapter.  A workgroup takes 16 rows, the distinct
-// adapters number blockIdx.y, + gridDim.y, .. among them, and one part of K,
-// which its waves split; the waves' sums meet in LDS.  Every lane holds row
-// (lane & 15) of x; a product row belongs to one x row only, so rows of other
-// adapters are computed beside it and dropped.
-template <int RT>
-__global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(
-    const uint16_t* __restrict__ x, const uint16_t* __restrict__ lora_a,
-    const int32_t* __restrict__ ids, const float* __restrict__ scaling, float* __restrict__ low,
-    int64_t M, int64_t K, int L, int R) {
-    __shared__ float part[kShrinkWaves][16][16 * RT + 4];
+// for the rows m that have an adapter.  A workgroup takes 16 RX rows, the
+// distinct adapters number `slot`, + slots, .. among them, and one part of K,
+// which its waves split; the waves' sums meet in LDS.  A product row belongs to one x row only, so rows of other adapters are
+// computed beside it and dropped.
+//
+// 64 columns of bf16 are 128 bytes, so a step of a wave looks like a K block of
+// the FP8 products and streams the same way: whole lines straight to a ring of
+// the wave's own in LDS (fragment-shaped loads to registers are bound by the
+// cache's tag rate, 16 bytes per clock).
+template <int RT, bool kMany>
+__device__ __forceinline__ void shrink_block(uint8_t* smem, const ShrinkArgs& g, int block, int slot0, int z) {
+    using Shape = ShrinkShape<RT, kMany>;
+    constexpr int RX = Shape::RX, W = Shape::W, D = Shape::D, kStage = Shape::kStage, kPitch = Shape::kPitch;
+    float* const part = reinterpret_cast<float*>(smem);  // [W][16 RX][kPitch], once the ring is done
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int lr = lane & 15, lg = lane >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * 16, row = std::min(m0 + lr, M - 1);
-    int id = m0 + lr < M ? ids[row] : -1;
-    if (id < 0 || id >= L) id = -1;
+    const int lr = lane & 15, lg = lane >> 4, R = g.R;
+    const int64_t m0 = (int64_t)block * 16 * RX, K = g.K;
+    const int rows = (int)std::min<int64_t>(16 * RX, g.M - m0);
+    int id = lane < rows ? g.ids[m0 + lane] : -1;  // lane l: row l
+    if (id < 0 || id >= g.L) id = -1;
     // the first row of each distinct adapter
     bool first = id >= 0;
-    for (int d = 0; d < 15; ++d) {
+    for (int d = 0; d < 16 * RX - 1; ++d) {
         const int o = __shfl(id, d, 64);
-        if (d < lr && o == id) first = false;
+        if (d < lane && o == id) first = false;
     }
-    uint32_t leaders = (uint32_t)__ballot(first) & 0xffffu;
-    const int steps = (int)(K >> 6), shares = gridDim.z * kShrinkWaves;
-    const int share = blockIdx.z * kShrinkWaves + wave;
+    uint32_t leaders = (uint32_t)__ballot(first);
+    const int steps = (int)(K >> 6), shares = g.parts * W, share = z * W + wave;
     const int s0 = (int)((int64_t)share * steps / shares), s1 = (int)((int64_t)(share + 1) * steps / shares);
-    const uint16_t* const px = x + row * K + 8 * lg;
+    // rows past the last one read as zero; K < 2^23, so R <= 128 rows of K bf16
+    // fit 31-bit offsets
+    const uint32_t pitch = (uint32_t)K * 2;
+    const v4u bufX = buffer_rsrc(g.x + m0 * K, (uint32_t)rows * pitch);
+    const uint32_t off = (uint32_t)(lane >> 3) * pitch + panel_chunk(lane);
+    uint8_t* const ring = smem + wave * D * kStage;
+    const int lo = (lg ^ (lr & 7)) << 4, hi = lo ^ 64;
     for (int n = 0; leaders != 0; ++n, leaders &= leaders - 1) {
-        if (n % gridDim.y != blockIdx.y) continue;
+        if (n % g.slots != slot0) continue;
         const int a = __builtin_amdgcn_readfirstlane(__shfl(id, __builtin_ctz(leaders), 64));
-        v4f acc[RT];
+        if (wave < W) {
+            const v4u bufA = buffer_rsrc(g.lora_a + (int64_t)a * R * K, (uint32_t)R * pitch);
+            auto issue = [&](int s, int slot) __attribute__((always_inline)) {
+                uint8_t* const to = ring + slot * kStage;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
-        const uint16_t* pa[RT];
+                for (int j = 0; j < 2 * RX; ++j)
+                    load_lds_16(bufX, s < s1 ? off + (uint32_t)(8 * j) * pitch + s * 128 : kNoRow, to + j * 1024);
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-            pa[r] = lora_a + ((int64_t)a * R + std::min(16 * r + lr, R - 1)) * K + 8 * lg;
-        for (int s = s0; s < s1; ++s) {
+                for (int j = 0; j < 2 * RT; ++j)
+                    load_lds_16(bufA, s < s1 ? off + (uint32_t)(8 * j) * pitch + s * 128 : kNoRow,
+                                to + RX * 2048 + j * 1024);
+            };
+            v4f acc[RX][RT];
+            clear(acc);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t at = (int64_t)s * 64 + 32 * h;
-                const v8bf xv = *reinterpret_cast<const v8bf*>(px + at);
+            for (int d = 0; d < D - 1; ++d) issue(s0 + d, d);
+            int slot = 0;
+            for (int s = s0; s < s1; ++s) {
+                wait_vmcnt_lgkm0<2 * (RX + RT) * (D - 2)>();
+                asm volatile("" ::: "memory");
+                issue(s + D - 1, slot == 0 ? D - 1 : slot - 1);
+                const uint8_t* const p = ring + slot * kStage + lr * 128;
+                v8bf xf[RX][2];
+#pragma unroll
+                for (int t = 0; t < RX; ++t) {
+                    xf[t][0] = *reinterpret_cast<const v8bf*>(p + t * 2048 + lo);
+                    xf[t][1] = *reinterpret_cast<const v8bf*>(p + t * 2048 + hi);
+                }
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const uint8_t* const q = p + 2048 * (RX + r);
+                    const v8bf a0 = *reinterpret_cast<const v8bf*>(q + lo), a1 = *reinterpret_cast<const v8bf*>(q + hi);
+#pragma unroll
+                    for (int t = 0; t < RX; ++t) {
+                        acc[t][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, xf[t][0], acc[t][r], 0, 0, 0);
+                        acc[t][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, xf[t][1], acc[t][r], 0, 0, 0);
+                    }
+                }
+                slot = slot == D - 1 ? 0 : slot + 1;
+            }
+            wait_vmcnt_lgkm0<0>();
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < RX; ++t)
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
-                    acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        *reinterpret_cast<const v8bf*>(pa[r] + at), xv, acc[r], 0, 0, 0);
-            }
+                    *reinterpret_cast<v4f*>(part + ((wave * RX + t) * 16 + lr) * kPitch + 16 * r + 4 * lg) = acc[t][r];
+        } else {
+            __syncthreads();
         }
-        __syncthreads();  // the last adapter's sums have been read
-#pragma unroll
-        for (int r = 0; r < RT; ++r) *reinterpret_cast<v4f*>(&part[wave][lr][16 * r + 4 * lg]) = acc[r];
         __syncthreads();
-        const float scale = scaling[a];
-        for (int i = threadIdx.x; i < 16 * R; i += 64 * kShrinkWaves) {
+        const float scale = g.scaling[a];
+        for (int i = threadIdx.x; i < 16 * RX * R; i += blockDim.x) {
             const int mi = i / R, r = i - mi * R;
             float sum = 0;
 #pragma unroll
-            for (int w = 0; w < kShrinkWaves; ++w) sum += part[w][mi][r];
-            if (__shfl(id, mi, 64) == a) low[((int64_t)blockIdx.z * M + m0 + mi) * R + r] = scale * sum;
+            for (int w = 0; w < W; ++w) sum += part[(w * 16 * RX + mi) * kPitch + r];
+            if (__shfl(id, mi, 64) == a) g.low[((int64_t)z * g.M + m0 + mi) * R + r] = scale * sum;
         }
+        __syncthreads();  // the sums have been read: the ring is free again
     }
 }
 
-// Parts of K: a few rows give few workgroups, so K is split over more of them.
-static int shrink_parts(int64_t M, int64_t K) {
-    const int64_t blocks = (M + 15) / 16, most = std::max<int64_t>(1, K / 512);
-    return (int)std::min(std::max<int64_t>(1, 64 / blocks), most);
+template <int RT>
+__global__ __launch_bounds__((64 * ShrinkShape<RT, true>::W)) void lora_shrink_kernel(ShrinkArgs g) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    shrink_block<RT, true>(smem, g, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
-int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int64_t R) {
-    return shrink_parts(M, K) * M * R * 4;
+// A few rows: the first workgroups multiply 16 T rows by 128 columns over one
+// share of K and leave fp32 parts; the others are the shrink's (in the other
+// order 64 rows of 64 adapters take 17.9 us instead of 15.0).  One burst of
+// loads has about 2 us of latency, so what counts is that all of B is asked
+// for at once: K is split until every CU has a workgroup.
+constexpr int kFewRing = 3;
+
+struct FewArgs {
+    const uint8_t* A;
+    const void* sa;
+    const uint8_t* B;
+    const void* sb;
+    float* sums;  // [shares][M][N]
+    int M, N, K;
+    int row_tiles, col_tiles, shares, per;  // per: K blocks of a share, a multiple of 4
+};
+
+template <int T, int RT, bool kE8>
+__global__ __launch_bounds__(64 * kPanelWaves) void lora_few_kernel(FewArgs f, ShrinkArgs g) {
+    using S = typename std::conditional<kE8, uint8_t, float>::type;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int base = f.row_tiles * f.col_tiles * f.shares;
+    int b = blockIdx.x;
+    if (b >= base) {
+        b -= base;
+        shrink_block<RT, false>(smem, g, b / (g.slots * g.parts), b / g.parts % g.slots, b % g.parts);
+        return;
+    }
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lr = lane & 15, lg = lane >> 4, sub = lane >> 3;
+    const int m0 = b % f.row_tiles * 16 * T, n0 = b / f.row_tiles % f.col_tiles * 128;
+    const int share = b / (f.row_tiles * f.col_tiles), kb0 = share * f.per;
+    const int KB = f.K >> 7, SP = scale_pitch<kE8>(KB), rows = min(16 * T, f.M - m0), cols = min(128, f.N - n0);
+    const uint32_t K = (uint32_t)f.K, chunk = panel_chunk(lane), kSz = sizeof(S);
+    PanelLoads<1> p;
+    // rows and columns past the last ones read as zero
+    p.bufA = buffer_rsrc(f.A + (int64_t)m0 * K + kb0 * 128, rows * K - kb0 * 128);
+    p.bufB = buffer_rsrc(f.B + (int64_t)n0 * K + kb0 * 128, cols * K - kb0 * 128);
+    p.bufS = wave == 0 ? buffer_rsrc(static_cast<const S*>(f.sa) + (int64_t)m0 * SP + kb0, (rows * SP - kb0) * kSz)
+                       : buffer_rsrc(static_cast<const S*>(f.sb) + (int64_t)(n0 >> 7) * SP + kb0, (SP - kb0) * kSz);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) p.offB[j] = (uint32_t)(16 * wave + 8 * j + sub) * K + chunk;
+    p.offA[0] = (uint32_t)(8 * wave + sub) * K + chunk;
+    p.offS = wave == 0 && lane < rows ? (uint32_t)lane * SP * kSz : wave == 1 && lane == 0 ? 0u : kNoRow;
+    v4f acc[T][1];
+    panel_product<T, 1, kFewRing, kE8, false>(smem, p, min(f.per, KB - kb0), rows, wave, lane, acc);
+    const int col = 16 * wave + 4 * lg;
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        if (16 * t + lr < rows && col < cols)  // N is a multiple of 8
+            *reinterpret_cast<v4f*>(f.sums + ((int64_t)share * f.M + m0 + 16 * t + lr) * f.N + n0 + col) = acc[t][0];
+}
+
+// D[m][n] = bf16(sum of the shares + low_m . lora_b[id][n]): one output a
+// thread, 256 columns of one row a workgroup.
+template <int RC>  // RC >= R / 8
+__global__ __launch_bounds__(256) void lora_combine_kernel(
+    const float* __restrict__ sums, const float* __restrict__ low, const uint16_t* __restrict__ lora_b,
+    const int32_t* __restrict__ ids, uint16_t* __restrict__ D, int M, int N, int L, int R, int parts, int shares) {
+    __shared__ float vec[8 * RC];
+    const int m = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x, at = min(n, N - 1);
+    const int id = ids[m];
+    const bool adapted = id >= 0 && id < L;  // uniform
+    float sum = 0;
+    v4u b[RC];
+    if (adapted) {
+        const uint16_t* const pb = lora_b + ((int64_t)id * N + at) * R;
+#pragma unroll
+        for (int c = 0; c < RC; ++c) b[c] = *reinterpret_cast<const v4u*>(pb + min(8 * c, R - 8));
+        if (threadIdx.x < 8 * RC) {
+            float v[kMaxParts], s = 0;
+#pragma unroll
+            for (int p = 0; p < kMaxParts; ++p)
+                v[p] = low[((int64_t)min(p, parts - 1) * M + m) * R + min((int)threadIdx.x, R - 1)];
+#pragma unroll
+            for (int p = 0; p < kMaxParts; ++p) s += p < parts ? v[p] : 0.0f;
+            vec[threadIdx.x] = s;
+        }
+    }
+    const float* const from = sums + (int64_t)m * N + at;
+    const int64_t next = (int64_t)M * N;
+    int s = 0;
+    for (; s + 4 <= shares; s += 4) {
+        const float v0 = from[s * next], v1 = from[(s + 1) * next], v2 = from[(s + 2) * next], v3 = from[(s + 3) * next];
+        sum += (v0 + v1) + (v2 + v3);
+    }
+    for (; s < shares; ++s) sum += from[s * next];
+    if (adapted) {
+        __syncthreads();
+        float term = 0;
+#pragma unroll
+        for (int c = 0; c < RC; ++c) {
+            if (8 * c >= R) break;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                term = fmaf(vec[8 * c + 2 * q], __uint_as_float(b[c][q] << 16), term);
+                term = fmaf(vec[8 * c + 2 * q + 1], __uint_as_float(b[c][q] & 0xffff0000u), term);
+            }
+        }
+        sum += term;
+    }
+    // N is a multiple of 8: the even lane of a pair stores both columns
+    const v2f pair = {sum, __shfl_xor(sum, 1, 64)};
+    if ((n & 1) == 0 && n < N)
+        *reinterpret_cast<uint32_t*>(D + (int64_t)m * N + n) =
+            __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, v2bf));
+}
+
+// What a call launches, from its sizes.
+struct LoraPlan {
+    bool few;
+    int T, row_tiles, col_tiles, shares, per;  // few rows
+    int blocks, slots, parts;                  // the shrink
+    int64_t low, sums, total;                  // workspace, in bytes from its start
+    LoraPlan(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+        // Up to 512 rows.  Where every row has its own adapter the dense tiles
+        // take a load latency per adapter, one after the other, and the few-row
+        // form spreads them over all CUs: 512 rows of 7168 x 2048, rank 32, 124
+        // against 55 us (200 rows 71 / 31); with 8 packed prompts it is 35
+        // against 46 us (256 rows of 2112 x 7168: 36 / 26).
+        few = M <= 512 && N <= 65536 && K <= 65536;
+        const int KB4 = (int)((K / 128 + 3) / 4);
+        T = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+        row_tiles = few ? (int)((M + 16 * T - 1) / (16 * T)) : 0;
+        col_tiles = few ? (int)((N + 127) / 128) : 0;
+        const int want = few ? std::max(1, std::min(16, 256 / (row_tiles * col_tiles))) : 1;
+        per = (KB4 + want - 1) / want * 4;
+        shares = (KB4 * 4 + per - 1) / per;
+        const int rows = 16 * (few ? 1 : R <= 64 ? 2 : 1);
+        blocks = (int)((M + rows - 1) / rows);
+        // alone a shrink's workgroup holds a CU's LDS, so none is launched that
+        // may find no adapter
+        slots = few ? (int)std::min<int64_t>(L, 16) : 1;
+        // few row blocks give few workgroups, so K is split over more of them
+        parts = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxParts, (few ? 64 : 256) / blocks, K / 256}));
+        auto up = [](int64_t v) { return (v + 255) & ~int64_t(255); };
+        low = 0;
+        sums = up(parts * M * R * 4);
+        total = sums + (few ? up((int64_t)shares * M * N * 4) : 0);
+    }
+};
+
+int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+    return LoraPlan(M, N, K, L, R).total;
 }
 
 template <int RT>
-static void shrink(const LoraArgs& a, float* low, int parts, hipStream_t stream) {
-    const int64_t blocks = (a.M + 15) / 16;
-    const int slots = (int)std::min<int64_t>(a.L, blocks >= 64 ? 4 : 16);
-    hipLaunchKernelGGL((lora_shrink_kernel<RT>), dim3((unsigned)blocks, slots, parts),
-                       dim3(64 * kShrinkWaves), 0, stream, a.x, a.lora_a, a.ids, a.scaling, low, a.M,
-                       a.K, a.L, a.R);
+static dg_status shrink(const ShrinkArgs& g, hipStream_t stream) {
+    using Shape = ShrinkShape<RT, true>;
+    hipLaunchKernelGGL((lora_shrink_kernel<RT>), dim3(g.blocks, g.slots, g.parts), dim3(64 * Shape::W),
+                       Shape::kLds, stream, g);
+    return launched();
+}
+
+template <int T, int RT, bool kE8>
+static dg_status few(const FewArgs& f, const ShrinkArgs& g, hipStream_t stream) {
+    constexpr size_t lds = std::max<size_t>(panel_lds<T, 1, kFewRing>(), ShrinkShape<RT, false>::kLds);
+    const int grid = f.row_tiles * f.col_tiles * f.shares + g.blocks * g.slots * g.parts;
+    hipLaunchKernelGGL((lora_few_kernel<T, RT, kE8>), dim3(grid), dim3(64 * kPanelWaves), lds, stream, f, g);
+    return launched();
+}
+
+template <int RT, bool kE8>
+static dg_status few_rows(const LoraPlan& at, const FewArgs& f, const ShrinkArgs& g, hipStream_t stream) {
+    return at.T == 1   ? few<1, RT, kE8>(f, g, stream)
+           : at.T == 2 ? few<2, RT, kE8>(f, g, stream)
+                       : few<4, RT, kE8>(f, g, stream);
+}
+
+template <int RT, bool kE8>
+static dg_status lora_rank(const LoraArgs& a, hipStream_t stream) {
+    const LoraPlan at(a.M, a.N, a.K, a.L, a.R);
+    uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
+    float* const low = reinterpret_cast<float*>(ws + at.low);
+    const ShrinkArgs g{a.x, a.lora_a, a.ids, a.scaling, low, a.M, a.K, a.L, a.R, at.blocks, at.slots, at.parts};
+    if (at.few) {
+        float* const sums = reinterpret_cast<float*>(ws + at.sums);
+        const FewArgs f{a.A, a.sa, a.B, a.sb, sums, (int)a.M, (int)a.N, (int)a.K, at.row_tiles, at.col_tiles,
+                        at.shares, at.per};
+        const dg_status s = few_rows<RT, kE8>(at, f, g, stream);
+        if (s != DG_OK) return s;
+        hipLaunchKernelGGL((lora_combine_kernel<2 * RT>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.M),
+                           dim3(256), 0, stream, sums, low, a.lora_b, a.ids, a.D, (int)a.M, (int)a.N, a.L, a.R,
+                           at.parts, at.shares);
+        return launched();
+    }
+    const dg_status s = shrink<RT>(g, stream);
+    if (s != DG_OK) return s;
+    GemmArgs d{a.A, a.sa, a.B, a.sb, a.D, nullptr, a.M, a.N, a.K, 1, nullptr};
+    d.e8m0 = kE8;
+    d.lora = LoraTail{low, a.lora_b, a.ids, at.parts, a.L, a.R};
+    return launch_gemm(Form::DenseLora, d, stream);
+}
+
+template <bool kE8>
+static dg_status lora_scales(const LoraArgs& a, hipStream_t stream) {
+    if (a.R <= 16) return lora_rank<1, kE8>(a, stream);
+    if (a.R <= 32) return lora_rank<2, kE8>(a, stream);
+    if (a.R <= 64) return lora_rank<4, kE8>(a, stream);
+    return lora_rank<8, kE8>(a, stream);
 }
 
 dg_status launch_lora(const LoraArgs& a, bool e8m0, hipStream_t stream) {
-    const int parts = shrink_parts(a.M, a.K);
-    float* const low = static_cast<float*>(a.workspace);
-    if (a.R <= 16)
-        shrink<1>(a, low, parts, stream);
-    else if (a.R <= 32)
-        shrink<2>(a, low, parts, stream);
-    else if (a.R <= 64)
-        shrink<4>(a, low, parts, stream);
-    else
-        shrink<8>(a, low, parts, stream);
-    const dg_status s = launched();
-    if (s != DG_OK) return s;
-    GemmArgs g{a.A, a.sa, a.B, a.sb, a.D, nullptr, a.M, a.N, a.K, 1, nullptr};
-    g.e8m0 = e8m0;
-    g.lora = LoraTail{low, a.lora_b, a.ids, parts, a.L, a.R};
-    return launch_gemm(Form::DenseLora, g, stream);
+    return e8m0 ? lora_scales<true>(a, stream) : lora_scales<false>(a, stream);
 }
 
 }  // namespace dg

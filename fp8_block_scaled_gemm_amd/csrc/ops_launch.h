@@ -61,7 +61,7 @@ struct LoraArgs {
     int L, R;
     void* workspace;
 };
-int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int64_t R);
+int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
 dg_status launch_lora(const LoraArgs& a, bool e8m0, hipStream_t stream);
 
 }  // namespace dg
