@@ -259,12 +259,16 @@ __device__ __forceinline__ void add_lora(v4f (&acc)[T::TM][T::TN], uint8_t* smem
         for (int i = tid; i < T::BM * 8; i += T::kThreads) {
             const int r = i >> 3, c = i & 7;
             v4f f[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            if (ids[r] != kNone && 8 * c + k0 < R)
+            if (ids[r] != kNone && 8 * c + k0 < R) {
                 for (int p = 0; p < lora.parts; ++p) {
                     const float* v = lora.low + ((int64_t)p * rows + ti.arow0 + r) * R + k0 + 8 * c;
                     f[0] += *reinterpret_cast<const v4f*>(v);
                     f[1] += *reinterpret_cast<const v4f*>(v + 4);
                 }
+                const float scale = lora.scaling[ids[r]];
+                f[0] *= scale;
+                f[1] *= scale;
+            }
             v8bf hi, lo;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {

@@ -19,10 +19,11 @@ inline dg_status launched() { return hipGetLastError() == hipSuccess ? DG_OK : D
 // DenseLora: dense routing, D = bf16(A B^T scaled + each row's adapter term)
 enum class Form : int { Dense = 0, Contiguous = 1, Masked = 2, DenseAcc = 3, DenseLora = 4 };
 
-// DenseLora: row m adds low[m] lora_b[ids[m]]^T when ids[m] is in [0, L)
+// DenseLora: row m adds scaling[a] * low[m] lora_b[a]^T, a = ids[m], when a is in [0, L)
 struct LoraTail {
     const float* low;        // [parts][rows][R], summed over parts
     const uint16_t* lora_b;  // bf16 [L][N][R]
+    const float* scaling;    // [L]
     const int32_t* ids;      // [rows]
     int parts, L, R;         // R a multiple of 8
 };
