@@ -207,6 +207,9 @@ __device__ __forceinline__ bool decode_tile(int b, int m_blocks, int n_blocks, i
     return true;
 }
 
+// Adapter ids of a tile's rows; kNoAdapter where a row has none.
+constexpr int kNoAdapter = 0x7fffffff;
+
 // The adapter term of a tile (DenseLora), once the K loop has left LDS free.
 // The workgroup walks the distinct adapters of its rows, 64 of the rank at a
 // time: the rows' vectors are staged once as two bf16 slabs in the A stages
@@ -218,17 +221,12 @@ __device__ __forceinline__ bool decode_tile(int b, int m_blocks, int n_blocks, i
 // a sum of two bf16 parts it is off by at most 2^-17, far below the final
 // rounding to bf16.  Each adapter of a tile costs about one load latency.
 template <class T>
-__device__ __forceinline__ void add_lora(v4f (&acc)[T::TM][T::TN], uint8_t* smem, int* ids, const LoraTail& lora,
+__device__ __forceinline__ void add_lora(v4f (&acc)[T::TM][T::TN], uint8_t* smem, const int* ids, const LoraTail& lora,
                                          int tid, int wave, int lane, int wm, int wcol, const TileInfo& ti,
                                          int64_t rows, int64_t N) {
     typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-    constexpr int kNone = 0x7fffffff;
+    constexpr int kNone = kNoAdapter;
     const int lr = lane & 15, lg = lane >> 4, R = lora.R;
-    for (int r = tid; r < T::BM; r += T::kThreads) {
-        const int id = r < ti.valid ? lora.ids[ti.arow0 + r] : -1;
-        ids[r] = id >= 0 && id < lora.L ? id : kNone;
-    }
-    __syncthreads();
     // the lowest adapter above `after` among the tile's rows, the same for every wave
     auto next_id = [&](int after) __attribute__((always_inline)) {
         int low = kNone;
@@ -256,24 +254,44 @@ __device__ __forceinline__ void add_lora(v4f (&acc)[T::TM][T::TN], uint8_t* smem
             }
         };
         issue(first, 0);
-        for (int i = tid; i < T::BM * 8; i += T::kThreads) {
-            const int r = i >> 3, c = i & 7;
-            v4f f[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            if (ids[r] != kNone && 8 * c + k0 < R) {
-                for (int p = 0; p < lora.parts; ++p) {
-                    const float* v = lora.low + ((int64_t)p * rows + ti.arow0 + r) * R + k0 + 8 * c;
-                    f[0] += *reinterpret_cast<const v4f*>(v);
-                    f[1] += *reinterpret_cast<const v4f*>(v + 4);
-                }
-                const float scale = lora.scaling[ids[r]];
-                f[0] *= scale;
-                f[1] *= scale;
+        // a thread's 8-rank pieces of the rows' vectors, all of a part's loads
+        // in flight at once
+        constexpr int kItems = T::BM * 8 / T::kThreads;
+        static_assert(T::BM * 8 % T::kThreads == 0, "whole passes over the vectors");
+        v4f f[kItems][2];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) f[i][0] = f[i][1] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < lora.parts; ++p) {
+            v4f v[kItems][2];
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int r = (i * T::kThreads + tid) >> 3, k = min(k0 + 8 * (tid & 7), R - 8);
+                const float* from = lora.low + ((int64_t)p * rows + ti.arow0 + min(r, ti.valid - 1)) * R + k;
+                v[i][0] = *reinterpret_cast<const v4f*>(from);
+                v[i][1] = *reinterpret_cast<const v4f*>(from + 4);
             }
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                f[i][0] += v[i][0];
+                f[i][1] += v[i][1];
+            }
+        }
+        float scale[kItems];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int id = ids[(i * T::kThreads + tid) >> 3];
+            scale[i] = lora.scaling[id == kNone ? 0 : id];
+        }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int r = (i * T::kThreads + tid) >> 3, c = tid & 7;
+            const bool in = ids[r] != kNone && k0 + 8 * c < R;
             v8bf hi, lo;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                hi[q] = (__bf16)f[q >> 2][q & 3];
-                lo[q] = (__bf16)(f[q >> 2][q & 3] - (float)hi[q]);
+                const float v = in ? scale[i] * f[i][q >> 2][q & 3] : 0.0f;
+                hi[q] = (__bf16)v;
+                lo[q] = (__bf16)(v - (float)hi[q]);
             }
             uint8_t* const to = smem + r * 128 + ((c ^ (r & 7)) << 4);
             *reinterpret_cast<v8bf*>(to) = hi;
@@ -446,6 +464,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void gemm_kernel(
     __shared__ __align__(1024) uint8_t smem[T::kSmem];
     __shared__ __align__(16) float smSA[2][T::BM * 4];
     __shared__ __align__(16) float smSB[2][64];
+    __shared__ int row_ids[kForm == Form::DenseLora ? T::BM : 1];
 
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -652,6 +671,13 @@ __global__ __launch_bounds__(T::kThreads, 2) void gemm_kernel(
         issue_b(0, 0);
         issue_a(1, 1, 0, T::kLoadsA / 2);
         issue_b(1, 1);
+        if constexpr (kForm == Form::DenseLora) {
+            for (int r = tid; r < T::BM; r += T::kThreads) {
+                const int id = r < ti.valid ? tail.ids[ti.arow0 + r] : -1;
+                row_ids[r] = id >= 0 && id < tail.L ? id : kNoAdapter;
+            }
+            wait_vmcnt_lgkm0<0>();
+        }
         wait_vmcnt<0>();
         lds_barrier();
         issue_a(1, 1, T::kLoadsA / 2, T::kLoadsA);
@@ -681,7 +707,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void gemm_kernel(
         wait_vmcnt<0>();  // the empty loads of the last steps have retired
         lds_barrier();
         if constexpr (kForm == Form::DenseLora)
-            add_lora<T>(acc, smem, reinterpret_cast<int*>(smSA), tail, tid, wave, lane, wm, wcol, ti, rows, N);
+            add_lora<T>(acc, smem, row_ids, tail, tid, wave, lane, wm, wcol, ti, rows, N);
         store_tile<T, kForm>(acc, smem, tid, wm, wcol, lr, lg, ti, C, D, N);
         if constexpr (!kMixed) {
             break;
