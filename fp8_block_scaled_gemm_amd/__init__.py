@@ -389,7 +389,7 @@ def _dims(t, what, n):
 def _enqueue(dev, name, *args):
     """Call a C entry point on the device's current stream (its last argument)."""
     fn = getattr(_lib or load_library(), name)
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)  # torch.cuda.current_stream without its object
     if torch.cuda.current_device() == dev.index:
         status = fn(*args, stream)
     else:

@@ -46,11 +46,50 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// One register move across lanes (DPP), `none` where no lane feeds this one.
+template <int kCtrl, int kRows, class T>
+__device__ __forceinline__ T dpp_move(T v, T none) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none),
+                                                               __builtin_bit_cast(int, v), kCtrl, kRows, 0xf, false));
+    } else {
+        const v2u n = __builtin_bit_cast(v2u, none), x = __builtin_bit_cast(v2u, v);
+        v2u r;
+        r[0] = (uint32_t)__builtin_amdgcn_update_dpp((int)n[0], (int)x[0], kCtrl, kRows, 0xf, false);
+        r[1] = (uint32_t)__builtin_amdgcn_update_dpp((int)n[1], (int)x[1], kCtrl, kRows, 0xf, false);
+        return __builtin_bit_cast(T, r);
+    }
+}
+
+// f over the wave's 64 values, in every lane (uniform); `none` is f's neutral
+// value.  Six register moves across lanes, where shuffles through LDS take
+// about ten times as long each: the k rounds below are one such chain each.
 template <class T, class F>
-__device__ __forceinline__ T wave_reduce(T v, F f) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v = f(v, __shfl_xor(v, d, 64));
-    return v;
+__device__ __forceinline__ T wave_reduce(T v, T none, F f) {
+    v = f(v, dpp_move<0x111, 0xf>(v, none));  // within rows of 16: from 1, 2, 4, 8 lanes below
+    v = f(v, dpp_move<0x112, 0xf>(v, none));
+    v = f(v, dpp_move<0x114, 0xf>(v, none));
+    v = f(v, dpp_move<0x118, 0xf>(v, none));
+    v = f(v, dpp_move<0x142, 0xa>(v, none));  // row sums 0 -> 1, 2 -> 3
+    v = f(v, dpp_move<0x143, 0xc>(v, none));  // rows 0-1 -> 2, 3
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+    } else {
+        const v2u x = __builtin_bit_cast(v2u, v);
+        return __builtin_bit_cast(T, v2u{(uint32_t)__builtin_amdgcn_readlane((int)x[0], 63),
+                                         (uint32_t)__builtin_amdgcn_readlane((int)x[1], 63)});
+    }
+}
+
+template <class T>
+__device__ __forceinline__ T wave_sum(T v) {
+    return wave_reduce(v, (T)0, [](T a, T b) { return a + b; });
+}
+__device__ __forceinline__ float wave_max(float v) {
+    return wave_reduce(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 
 // exp(x - top) with +infinity shared equally: the entries equal to an infinite
@@ -61,14 +100,31 @@ __device__ __forceinline__ F exp_below(F x, F top) {
     return exp(x - top);
 }
 
+// A lane's NV values of a row; one load where the rows keep it aligned.
 template <class In, int NV>
 __device__ __forceinline__ void load_row(const In* row, int E, int lane, float (&x)[NV]) {
+    constexpr int kVec = NV * sizeof(In) > 16 ? 16 / sizeof(In) : NV;
+    typedef In Vec __attribute__((ext_vector_type(kVec)));
+    const int e0 = lane * NV;
+    if (E % NV == 0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane * NV + i;
-        x[i] = e < E ? to_float(row[e]) : -INFINITY;
-        if (!(x[i] > -INFINITY)) x[i] = -INFINITY;  // NaN is masked like -infinity
+        for (int i = 0; i < NV; i += kVec) {
+            if (e0 < E) {
+                const Vec v = *reinterpret_cast<const Vec*>(row + e0 + i);
+#pragma unroll
+                for (int q = 0; q < kVec; ++q) x[i + q] = to_float((In)v[q]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < kVec; ++q) x[i + q] = -INFINITY;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i] = e0 + i < E ? to_float(row[e0 + i]) : -INFINITY;
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (!(x[i] > -INFINITY)) x[i] = -INFINITY;  // NaN is masked like -infinity
 }
 
 template <class In, int NV>
@@ -76,7 +132,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_kernel(
     const In* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ ids,
     float* __restrict__ weights, int64_t T, int E, int k, int n_group, int topk_group, bool sigmoid,
     bool renormalize, float scale) {
-    __shared__ uint64_t ranks[kRowsPerBlock][64 * NV];
+    __shared__ uint64_t ranks[kRowsPerBlock][64 * (NV < 2 ? 2 : NV)];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * kRowsPerBlock + w;
     if (t >= T) return;
@@ -85,7 +141,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_kernel(
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NV; ++i) top = fmaxf(top, x[i]);
-    top = wave_reduce(top, [](float a, float b) { return fmaxf(a, b); });
+    top = wave_max(top);
 
     // ranks; 0 is below every open expert's
     uint64_t key[NV];
@@ -103,7 +159,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_kernel(
             sum += p[i];
         }
         if (!sigmoid) {
-            sum = wave_reduce(sum, [](double a, double b) { return a + b; });
+            sum = wave_sum(sum);
 #pragma unroll
             for (int i = 0; i < NV; ++i) p[i] /= sum;
         }
@@ -114,22 +170,39 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_kernel(
             key[i] = x[i] > -INFINITY && p[i] > -(double)INFINITY ? order64(p[i]) : 0;
         }
         if (n_group > 1) {
+            const bool by_lane = NV >= 2 && (E / n_group) % NV == 0;
+            if (by_lane) {
+                uint64_t first = 0, second = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) ranks[w][lane * NV + i] = key[i];
+                for (int i = 0; i < NV; ++i) {
+                    second = max(second, min(first, key[i]));
+                    first = max(first, key[i]);
+                }
+                ranks[w][lane] = first;
+                if (NV >= 2) ranks[w][64 + lane] = second;
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) ranks[w][lane * NV + i] = key[i];
+            }
             wave_sync();
             const int size = E / n_group;
-            // lane g: the value of group g
+            // lane g: the value of group g, from its two best ranks.  Where a
+            // lane's experts are of one group, the lanes' two best are enough.
             uint64_t value = 0;
             if (lane < n_group) {
                 uint64_t first = 0, second = 0;
-                for (int i = 0; i < size; ++i) {
-                    const uint64_t r = ranks[w][lane * size + i];
-                    if (r > first) {
-                        second = first;
-                        first = r;
-                    } else if (r > second) {
-                        second = r;
+                auto take = [&](uint64_t r) __attribute__((always_inline)) {
+                    second = max(second, min(first, r));
+                    first = max(first, r);
+                };
+                if (by_lane) {
+#pragma unroll 4
+                    for (int i = lane * (size / NV); i < (lane + 1) * (size / NV); ++i) {
+                        take(ranks[w][i]);
+                        take(ranks[w][64 + i]);
                     }
+                } else {
+                    for (int i = 0; i < size; ++i) take(ranks[w][lane * size + i]);
                 }
                 auto number = [](uint64_t r) {
                     return __longlong_as_double((long long)((r >> 63) ? r & ~0x8000000000000000ull : ~r));
@@ -138,8 +211,10 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_kernel(
             }
             // how many groups come before this one
             int before = 0;
+            const uint32_t vlo = (uint32_t)value, vhi = (uint32_t)(value >> 32);
             for (int g = 0; g < n_group; ++g) {
-                const uint64_t o = __shfl(value, g, 64);
+                const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)vhi, g) << 32 |
+                                   (uint32_t)__builtin_amdgcn_readlane((int)vlo, g);
                 before += o > value || (o == value && g < lane);
             }
             const uint64_t open = __ballot(lane < n_group && before < topk_group);
@@ -151,27 +226,31 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_kernel(
         }
     }
 
-    // k rounds: the wave's largest rank, at its lowest index
+    // k rounds: the wave's largest rank, at its lowest index.  Ranks differ in
+    // their upper halves more often than not, and an open one's is never 0.
     int my_id = -1;
     float my_x = -INFINITY;
     for (int j = 0; j < k; ++j) {
         uint64_t best = key[0];
         int at = 0;
+        float at_x = x[0];
 #pragma unroll
         for (int i = 1; i < NV; ++i)
             if (key[i] > best) {
                 best = key[i];
                 at = i;
+                at_x = x[i];
             }
-        const uint64_t m = wave_reduce(best, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
-        if (m == 0) break;
-        const int owner = __builtin_ctzll(__ballot(best == m));
-        const int slot = __shfl(at, owner, 64);
-        float v = x[0];
-#pragma unroll
-        for (int i = 1; i < NV; ++i)
-            if (slot == i) v = x[i];
-        v = __shfl(v, owner, 64);
+        const uint32_t hi = (uint32_t)(best >> 32), top_hi = wave_max(hi);
+        if (top_hi == 0) break;
+        uint64_t owners = __ballot(hi == top_hi);
+        if (owners & (owners - 1)) {
+            const uint32_t low = hi == top_hi ? (uint32_t)best : 0u, top_low = wave_max(low);
+            owners = __ballot(hi == top_hi && low == top_low);
+        }
+        const int owner = __builtin_ctzll(owners);
+        const int slot = __builtin_amdgcn_readlane(at, owner);
+        const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(at_x), owner));
         if (lane == j) {
             my_id = owner * NV + slot;
             my_x = v;
@@ -183,25 +262,53 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_kernel(
         }
     }
 
-    auto add = [](auto a, auto b) { return a + b; };
     float weight = 0;
     if (sigmoid) {
         // one score per lane: 64 bits cost nothing and keep scores that fp32
         // would flush apart before they are divided by their sum
         double p = my_id >= 0 ? 1.0 / (1.0 + exp(-(double)my_x)) : 0.0;
-        if (renormalize) p /= wave_reduce(p, add) + kTopkEps;
+        if (renormalize) p /= wave_sum(p) + kTopkEps;
         weight = (float)p;
     } else {
         float sum = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) sum += x[i] > -INFINITY ? exp_below<float>(x[i], top) : 0.0f;
-        sum = wave_reduce(sum, add);
+        sum = wave_sum(sum);
         weight = my_id >= 0 ? exp_below<float>(my_x, top) / sum : 0.0f;
-        if (renormalize) weight /= wave_reduce(weight, add) + (float)kTopkEps;
+        if (renormalize) weight /= wave_sum(weight) + (float)kTopkEps;
     }
     if (lane < k) {
         ids[t * k + lane] = my_id;
         weights[t * k + lane] = weight * scale;
+    }
+}
+
+template <class In>
+__device__ __forceinline__ In from_float(float v) {
+    if constexpr (sizeof(In) == 2)
+        return __builtin_bit_cast(uint16_t, (__bf16)v);
+    else
+        return v;
+}
+
+template <class In, int NV>
+__device__ __forceinline__ void store_row(In* row, int E, int lane, const float (&v)[NV]) {
+    constexpr int kVec = NV * sizeof(In) > 16 ? 16 / sizeof(In) : NV;
+    typedef In Vec __attribute__((ext_vector_type(kVec)));
+    const int e0 = lane * NV;
+    if (E % NV == 0) {
+        if (e0 >= E) return;
+#pragma unroll
+        for (int i = 0; i < NV; i += kVec) {
+            Vec o;
+#pragma unroll
+            for (int q = 0; q < kVec; ++q) o[q] = from_float<In>(v[i + q]);
+            *reinterpret_cast<Vec*>(row + e0 + i) = o;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (e0 + i < E) row[e0 + i] = from_float<In>(v[i]);
     }
 }
 
@@ -221,14 +328,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_backward_kernel(
     float g = id >= 0 ? grad_w[t * k + lane] * scale : 0.0f;
     float xs = id >= 0 ? to_float(row[id]) : -INFINITY;
     if (!(xs > -INFINITY)) xs = -INFINITY;
-    auto store_grad = [&](int e, float d) {
-        if (e >= E) return;
-        if constexpr (sizeof(In) == 2)
-            grad[t * E + e] = __builtin_bit_cast(uint16_t, (__bf16)d);
-        else
-            grad[t * E + e] = d;
-    };
-    auto add = [](auto a, auto b) { return a + b; };
+    float out[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) dense[w][lane + 64 * i] = 0.0f;
     wave_sync();
@@ -238,40 +338,41 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_backward_kernel(
         double d = g;
         if (renormalize) {
             // w_j = p_j / S: dL/dp_j = (g_j - sum_i g_i p_i / S) / S
-            const double total = wave_reduce(p, add) + kTopkEps;
-            d = (d - wave_reduce(d * p, add) / total) / total;
+            const double total = wave_sum(p) + kTopkEps;
+            d = (d - wave_sum(d * p) / total) / total;
         }
         if (id >= 0) atomicAdd(&dense[w][id], (float)(d * p * (1.0 - p)));
         wave_sync();
 #pragma unroll
-        for (int i = 0; i < NV; ++i) store_grad(lane * NV + i, dense[w][lane * NV + i]);
+        for (int i = 0; i < NV; ++i) out[i] = dense[w][lane * NV + i];
+        store_row<In, NV>(grad + t * E, E, lane, out);
         return;
     }
 
     float top = -INFINITY, rsum = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) top = fmaxf(top, x[i]);
-    top = wave_reduce(top, [](float a, float b) { return fmaxf(a, b); });
+    top = wave_max(top);
     float e[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         e[i] = x[i] > -INFINITY ? exp_below<float>(x[i], top) : 0.0f;
         rsum += e[i];
     }
-    rsum = wave_reduce(rsum, add);
+    rsum = wave_sum(rsum);
     rsum = rsum > 0.0f ? 1.0f / rsum : 0.0f;  // 0: no expert is open
     const float p = id >= 0 && xs > -INFINITY ? exp_below<float>(xs, top) * rsum : 0.0f;
     if (renormalize) {
-        const float total = wave_reduce(p, add) + (float)kTopkEps;
-        const float mean = wave_reduce(g * p, add) / total;
+        const float total = wave_sum(p) + (float)kTopkEps;
+        const float mean = wave_sum(g * p) / total;
         g = id >= 0 ? (g - mean) / total : 0.0f;
     }
-    const float dot = wave_reduce(g * p, add);
+    const float dot = wave_sum(g * p);
     if (id >= 0) atomicAdd(&dense[w][id], g);
     wave_sync();
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        store_grad(lane * NV + i, e[i] * rsum * (dense[w][lane * NV + i] - dot));
+    for (int i = 0; i < NV; ++i) out[i] = e[i] * rsum * (dense[w][lane * NV + i] - dot);
+    store_row<In, NV>(grad + t * E, E, lane, out);
 }
 
 static int64_t row_blocks(int64_t T) { return (T + kRowsPerBlock - 1) / kRowsPerBlock; }
