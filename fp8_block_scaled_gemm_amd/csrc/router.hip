@@ -127,140 +127,191 @@ __device__ __forceinline__ void load_row(const In* row, int E, int lane, float (
         if (!(x[i] > -INFINITY)) x[i] = -INFINITY;  // NaN is masked like -infinity
 }
 
+// The two largest of two pairs, each with first >= second.
+struct Best2 {
+    double first, second;
+    __device__ __forceinline__ void take(double f, double s) {
+        second = fmax(fmin(first, f), fmax(second, s));
+        first = fmax(first, f);
+    }
+    template <int kCtrl>
+    __device__ __forceinline__ void merge_lanes() {
+        const double f = dpp_move<kCtrl, 0xf>(first, first), s = dpp_move<kCtrl, 0xf>(second, second);
+        take(f, s);
+    }
+    // a group with one open expert is ranked by that one
+    __device__ __forceinline__ double value() const {
+        return second > -(double)INFINITY ? first + second : first;
+    }
+};
+
+// Ranks of experts outside the topk_group best groups become -infinity (as
+// every closed expert's is).  `lds` holds 64 max(NV, 2) doubles of the wave.
+template <int NV>
+__device__ __forceinline__ void close_groups(double (&r)[NV], double* lds, int E, int n_group,
+                                             int topk_group, int lane) {
+    const double none = -(double)INFINITY;
+    const int size = E / n_group, lanes = size / NV;  // lanes of a group, where it is whole lanes
+    Best2 best = {none, none};
+    if (size % NV == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) best.take(r[i], none);
+    }
+    if (size % NV == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0) {
+        // groups of 1 .. 16 lanes: merged by moves within rows of 16 lanes
+        if (lanes >= 2) best.merge_lanes<0xb1>();   // swap neighbours
+        if (lanes >= 4) best.merge_lanes<0x4e>();   // swap pairs
+        if (lanes >= 8) best.merge_lanes<0x141>();  // mirror 8
+        if (lanes >= 16) best.merge_lanes<0x140>(); // mirror 16
+        const double mine = best.value();
+        const int group = lane / lanes;
+        const v2u bits = __builtin_bit_cast(v2u, mine);
+        int before = 0;  // groups ahead of this lane's
+        for (int g = 0; g < n_group; ++g) {
+            const double o = __builtin_bit_cast(
+                double, v2u{(uint32_t)__builtin_amdgcn_readlane((int)bits[0], g * lanes),
+                            (uint32_t)__builtin_amdgcn_readlane((int)bits[1], g * lanes)});
+            before += o > mine || (o == mine && g < group);
+        }
+        if (before >= topk_group) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) r[i] = none;
+        }
+        return;
+    }
+    // any other size: lane g gathers group g from LDS
+    const bool pairs = NV >= 2 && size % NV == 0;  // the lanes' two best are enough
+    if (pairs) {
+        lds[lane] = best.first;
+        lds[64 + lane] = best.second;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) lds[lane * NV + i] = r[i];
+    }
+    wave_sync();
+    best = {none, none};
+    if (lane < n_group) {
+        const int n = pairs ? lanes : size;
+        for (int i = lane * n; i < (lane + 1) * n; ++i) best.take(lds[i], pairs ? lds[64 + i] : none);
+    }
+    const double mine = best.value();
+    const v2u bits = __builtin_bit_cast(v2u, mine);
+    int before = 0;
+    for (int g = 0; g < n_group; ++g) {
+        const double o = __builtin_bit_cast(double, v2u{(uint32_t)__builtin_amdgcn_readlane((int)bits[0], g),
+                                                        (uint32_t)__builtin_amdgcn_readlane((int)bits[1], g)});
+        before += o > mine || (o == mine && g < lane);
+    }
+    const uint64_t open = __ballot(lane < n_group && before < topk_group);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane * NV + i;
+        if (e >= E || !((open >> (e / size)) & 1)) r[i] = none;
+    }
+}
+
 template <class In, int NV>
 __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_kernel(
     const In* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ ids,
     float* __restrict__ weights, int64_t T, int E, int k, int n_group, int topk_group, bool sigmoid,
     bool renormalize, float scale) {
-    __shared__ uint64_t ranks[kRowsPerBlock][64 * (NV < 2 ? 2 : NV)];
+    __shared__ double ranks[kRowsPerBlock][64 * (NV < 2 ? 2 : NV)];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * kRowsPerBlock + w;
     if (t >= T) return;
-    float x[NV];
+    float x[NV], b[NV];
     load_row<In, NV>(logits + t * E, E, lane, x);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) b[i] = bias && lane * NV + i < E ? bias[lane * NV + i] : 0.0f;
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NV; ++i) top = fmaxf(top, x[i]);
     top = wave_max(top);
 
-    // ranks; 0 is below every open expert's
+    // ranks as ordered integers; 0 is below every open expert's
     uint64_t key[NV];
     if (bias == nullptr && n_group == 1) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) key[i] = x[i] > -INFINITY ? (uint64_t)order32(x[i]) << 32 : 0;
     } else {
-        double p[NV];
+        double r[NV];
         double sum = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            p[i] = x[i] == -INFINITY ? 0.0
+            r[i] = x[i] == -INFINITY ? 0.0
                    : sigmoid         ? 1.0 / (1.0 + exp(-(double)x[i]))
                                      : exp_below<double>(x[i], top);
-            sum += p[i];
+            sum += r[i];
         }
         if (!sigmoid) {
             sum = wave_sum(sum);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) p[i] /= sum;
+            for (int i = 0; i < NV; ++i) r[i] /= sum;
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = lane * NV + i;
-            if (bias && e < E) p[i] += (double)bias[e];
-            key[i] = x[i] > -INFINITY && p[i] > -(double)INFINITY ? order64(p[i]) : 0;
+            r[i] += (double)b[i];
+            if (!(x[i] > -INFINITY && r[i] > -(double)INFINITY)) r[i] = -(double)INFINITY;
         }
-        if (n_group > 1) {
-            const bool by_lane = NV >= 2 && (E / n_group) % NV == 0;
-            if (by_lane) {
-                uint64_t first = 0, second = 0;
+        if (n_group > 1) close_groups<NV>(r, ranks[w], E, n_group, topk_group, lane);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    second = max(second, min(first, key[i]));
-                    first = max(first, key[i]);
-                }
-                ranks[w][lane] = first;
-                if (NV >= 2) ranks[w][64 + lane] = second;
-            } else {
-#pragma unroll
-                for (int i = 0; i < NV; ++i) ranks[w][lane * NV + i] = key[i];
-            }
-            wave_sync();
-            const int size = E / n_group;
-            // lane g: the value of group g, from its two best ranks.  Where a
-            // lane's experts are of one group, the lanes' two best are enough.
-            uint64_t value = 0;
-            if (lane < n_group) {
-                uint64_t first = 0, second = 0;
-                auto take = [&](uint64_t r) __attribute__((always_inline)) {
-                    second = max(second, min(first, r));
-                    first = max(first, r);
-                };
-                if (by_lane) {
-#pragma unroll 4
-                    for (int i = lane * (size / NV); i < (lane + 1) * (size / NV); ++i) {
-                        take(ranks[w][i]);
-                        take(ranks[w][64 + i]);
-                    }
-                } else {
-                    for (int i = 0; i < size; ++i) take(ranks[w][lane * size + i]);
-                }
-                auto number = [](uint64_t r) {
-                    return __longlong_as_double((long long)((r >> 63) ? r & ~0x8000000000000000ull : ~r));
-                };
-                if (first) value = order64(number(first) + (second ? number(second) : 0.0));
-            }
-            // how many groups come before this one
-            int before = 0;
-            const uint32_t vlo = (uint32_t)value, vhi = (uint32_t)(value >> 32);
-            for (int g = 0; g < n_group; ++g) {
-                const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)vhi, g) << 32 |
-                                   (uint32_t)__builtin_amdgcn_readlane((int)vlo, g);
-                before += o > value || (o == value && g < lane);
-            }
-            const uint64_t open = __ballot(lane < n_group && before < topk_group);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int e = lane * NV + i;
-                if (e >= E || !((open >> (e / size)) & 1)) key[i] = 0;
-            }
-        }
+        for (int i = 0; i < NV; ++i) key[i] = r[i] > -(double)INFINITY ? order64(r[i]) : 0;
     }
 
-    // k rounds: the wave's largest rank, at its lowest index.  Ranks differ in
-    // their upper halves more often than not, and an open one's is never 0.
-    int my_id = -1;
-    float my_x = -INFINITY;
-    for (int j = 0; j < k; ++j) {
-        uint64_t best = key[0];
-        int at = 0;
-        float at_x = x[0];
+    // k rounds: the wave's largest rank, at its lowest index.  Ranks are told
+    // apart by their upper halves (an open one's is never 0); only when those
+    // tie do the lower halves decide, then the index.  The comparisons' lane
+    // masks are scalars, so a round is about 20 vector instructions for 256
+    // experts; with 64-bit comparisons and selects per lane it was 55, and a
+    // batch of rows is bound by their issue.
+    uint32_t hi[NV], lo[NV];
 #pragma unroll
-        for (int i = 1; i < NV; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-                at_x = x[i];
-            }
-        const uint32_t hi = (uint32_t)(best >> 32), top_hi = wave_max(hi);
-        if (top_hi == 0) break;
-        uint64_t owners = __ballot(hi == top_hi);
-        if (owners & (owners - 1)) {
-            const uint32_t low = hi == top_hi ? (uint32_t)best : 0u, top_low = wave_max(low);
-            owners = __ballot(hi == top_hi && low == top_low);
-        }
-        const int owner = __builtin_ctzll(owners);
-        const int slot = __builtin_amdgcn_readlane(at, owner);
-        const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(at_x), owner));
-        if (lane == j) {
-            my_id = owner * NV + slot;
-            my_x = v;
-        }
-        if (lane == owner) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (slot == i) key[i] = 0;
-        }
+    for (int i = 0; i < NV; ++i) {
+        hi[i] = (uint32_t)(key[i] >> 32);
+        lo[i] = (uint32_t)key[i];
     }
+    int my_id = -1;
+    for (int j = 0; j < k; ++j) {
+        uint32_t most = hi[0];
+#pragma unroll
+        for (int i = 1; i < NV; ++i) most = max(most, hi[i]);
+        most = wave_max(most);
+        if (most == 0) break;
+        uint64_t mask[NV];
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            mask[i] = __ballot(hi[i] == most);
+            n += __popcll(mask[i]);
+        }
+        if (n > 1) {
+            uint32_t low = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) low = hi[i] == most ? max(low, lo[i]) : low;
+            low = wave_max(low);
+            uint64_t any = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                mask[i] = __ballot(hi[i] == most && lo[i] == low);
+                any |= mask[i];
+            }
+            // the lowest lane, there the lowest slot
+            uint64_t only = any & (0 - any);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                mask[i] &= only;
+                only ^= mask[i];
+            }
+        }
+        int id = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (mask[i]) id = __builtin_ctzll(mask[i]) * NV + i;
+            if ((mask[i] >> lane) & 1) hi[i] = 0;
+        }
+        if (lane == j) my_id = id;
+    }
+    float my_x = my_id >= 0 ? to_float(logits[t * E + my_id]) : -INFINITY;
 
     float weight = 0;
     if (sigmoid) {
