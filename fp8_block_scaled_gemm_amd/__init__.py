@@ -354,36 +354,39 @@ _SCORING = {"softmax": 0, "sigmoid": 1}
 
 
 def _ptr(t, what, dtype, shape, dev):
-    """The data pointer of a contiguous GPU tensor of this dtype and shape on
-    this device; raises like ``_check`` otherwise.  The common case is one
-    comparison each: these calls are a few microseconds long on the GPU."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous() and t.is_cuda and t.device == dev):
-        _check(t, what, dtype, shape)
-        raise ValueError(f"all tensors of a call must be on one device, got {dev} and {t.device}")
-    return t.data_ptr()
+    """The data pointer of a contiguous tensor of this dtype and shape on this
+    device, which is a GPU; raises like ``_check`` otherwise.  The common case
+    is one comparison each: these calls are a few microseconds long."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _check(t, what, dtype, shape)
+    raise ValueError(f"all tensors of a call must be on one device, got {dev} and {t.device}")
 
 
 def _codes_ptr(t, what, shape, dev):
-    if isinstance(t, torch.Tensor) and t.dtype is not torch.uint8:
-        t = _bytes(t, what)
+    if getattr(t, "dtype", None) is torch.float8_e4m3fn:
+        t = t.view(torch.uint8)
     return _ptr(t, what, torch.uint8, shape, dev)
 
 
 def _bf16_ptr(t, what, shape, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype not in _D_TYPES:
-        _check(t, what, _D_TYPES)
-    return _ptr(t, what, t.dtype, shape, dev)
+    dtype = getattr(t, "dtype", None)
+    return _ptr(t, what, dtype if dtype in _D_TYPES else _D_TYPES, shape, dev)
 
 
 def _dims(t, what, n):
+    """Shape of a GPU tensor of n dimensions."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
-    if t.dim() != n:
-        raise ValueError(f"{what} must have {n} dimensions, got shape {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{what} must have {n} dimensions, got shape {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{what} must be on the GPU")
-    return t.shape
+    return shape
 
 
 def _enqueue(dev, name, *args):
