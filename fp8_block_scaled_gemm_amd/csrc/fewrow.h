@@ -135,7 +135,7 @@ template <int R, int C>
 struct PanelStage {
     uint8_t b[kPanelWaves * C * 2048];  // wave w: C tiles of 16 rows
     uint8_t a[16 * R * 128];
-    float sa[64];  // per row of A
+    float sa[R > 4 ? 16 * R : 64];  // per row of A
     float sb[64];  // [c] of tile set c
 };
 
@@ -152,9 +152,15 @@ template <int C>
 struct PanelLoads {
     v4u bufB, bufA, bufS;  // bufS: the scales this wave loads
     uint32_t offB[2 * C];  // lane l: row 8 j + l / 8 of the wave's 16 C rows
-    uint32_t offA[2];      // lane l of wave w: row 8 w + l / 8 of A ([0]; free panels: see panel_a_loads)
-    uint32_t offS;         // lane l of wave 0: scale row l of A; of wave 1: column scales of tile set l
+    uint32_t offA[4];      // lane l of wave w: rows of A, see panel_a_loads
+    uint32_t offS;         // lane l of wave 0 (2): scale row l (64 + l) of A; of wave 1: column scales of tile set l
 };
+
+// Direct loads of a wave for the A rows of a panel's K block, or of a free
+// panel's chunk; load i = wave * this + j takes rows 8 (i % 2R) .. + 7, and
+// there may be more waves than loads.
+constexpr int kChunk = 4;  // K blocks of a free panel's chunk
+constexpr int panel_a_loads(int R, int W, int blocks) { return 2 * R * blocks > W ? 2 * R * blocks / W : 1; }
 
 // The 16-byte chunk that lane l asks for, in bytes.
 __device__ __forceinline__ uint32_t panel_chunk(int lane) { return ((lane & 7) ^ (lane >> 3)) * 16; }
@@ -168,16 +174,23 @@ __device__ __forceinline__ void panel_product(uint8_t* smem, const PanelLoads<C>
     using Stage = PanelStage<R, C>;
     Stage* const ring = reinterpret_cast<Stage*>(smem);
     uint8_t* const unused = smem + D * sizeof(Stage);
-    constexpr int kLoads = 2 * C + 2;
+    constexpr int kA = panel_a_loads(R, kPanelWaves, 1), kLoads = 2 * C + kA + 1;
     const int lr = lane & 15, lg = lane >> 4;
     auto issue = [&](int kb, Stage& s) __attribute__((always_inline)) {
         const bool real = kb < KB;  // stages past the last one load nothing
 #pragma unroll
         for (int j = 0; j < 2 * C; ++j)
             load_lds_16(p.bufB, real ? p.offB[j] + kb * 128 : kNoRow, s.b + wave * C * 2048 + j * 1024);
-        load_lds_16(p.bufA, real ? p.offA[0] + kb * 128 : kNoRow, wave < 2 * R ? s.a + wave * 1024 : unused);
+#pragma unroll
+        for (int j = 0; j < kA; ++j) {
+            const int i = wave * kA + j;
+            load_lds_16(p.bufA, real ? p.offA[j] + kb * 128 : kNoRow, i < 2 * R ? s.a + i * 1024 : unused);
+        }
         load_lds_4(p.bufS, real ? p.offS + (kE8 ? kb & ~3 : kb * 4) : kNoRow,
-                   wave == 0 ? (void*)s.sa : wave == 1 ? (void*)s.sb : (void*)unused);
+                   wave == 0             ? (void*)s.sa
+                   : wave == 1           ? (void*)s.sb
+                   : R > 4 && wave == 2  ? (void*)(s.sa + 64)
+                                         : (void*)unused);
     };
     clear(acc);
 #pragma unroll
@@ -225,12 +238,6 @@ __device__ __forceinline__ void panel_product(uint8_t* smem, const PanelLoads<C>
 // scales come in chunks of four K blocks, double-buffered, one barrier per
 // chunk; in between every wave runs on its own through its private ring of B.
 // (A lone workgroup on a CU streams 35 GB/s with the barrier per K block.)
-constexpr int kChunk = 4;
-
-// Direct loads of each of W waves for a chunk of A; load i = wave * this + j
-// takes rows 8 (i % 2R) .. + 7.
-constexpr int panel_a_loads(int R, int W) { return kChunk * 2 * R / W; }
-
 template <int R, int C, int D, int W>
 struct FreePanel {
     uint8_t b[D][W * C * 2048];
@@ -244,7 +251,8 @@ template <int R, int C, int D, int W, bool kE8, bool kExact>
 __device__ __forceinline__ void free_panel_product(uint8_t* smem, const PanelLoads<C>& p, int KB, int rows,
                                                    int wave, int lane, v4f (&acc)[R][C]) {
     static_assert(R <= 2, "A chunks of more rows do not fit beside the ring");
-    constexpr int kA = panel_a_loads(R, W);
+    constexpr int kA = panel_a_loads(R, W, kChunk);
+    static_assert(kA * W == 2 * R * kChunk, "every load of a chunk has a wave");
     FreePanel<R, C, D, W>& s = *reinterpret_cast<FreePanel<R, C, D, W>*>(smem);
     const int lr = lane & 15, lg = lane >> 4;
     auto issue_b = [&](int kb, int st) __attribute__((always_inline)) {

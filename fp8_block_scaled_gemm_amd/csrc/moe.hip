@@ -28,12 +28,39 @@ struct MoeJob {
     uint16_t start, count;
 };
 
-// A few pairs: the hidden rows fit the second product's LDS, and there are at
-// most 256 blocks of 128 hidden columns, so the first product takes 64 columns
-// a workgroup.  Then the second product adds up each token's experts itself.
-// More pairs: 128 columns quantized by the first product, the second writes
-// every pair's product, a third launch adds them up.
-inline bool few_pairs(int64_t T, int64_t k, int64_t I) { return T <= 16 && T * k * I <= 32768; }
+// LDS of the second product of a few pairs.
+constexpr int kDownWaves = 8, kDownRing = 3;
+
+struct MoeDownLds {
+    int ring, codes, scales, cols, slices, row_w, jobs, row_t, total;
+    __host__ __device__ MoeDownLds(int T, int P, int U, int I) {
+        ring = 0;
+        codes = kDownWaves * kDownRing * 2048;        // [P][I], chunk c of row r at c ^ (r & 7)
+        scales = codes + P * I;                       // [P][I / 128]
+        cols = scales + P * (I >> 7) * 4;             // [jobs][I / 128]
+        slices = cols + (U + P / 16) * (I >> 7) * 4;  // [wave][T][16]
+        slices = (slices + 15) & ~15;
+        row_w = slices + kDownWaves * T * 64;
+        jobs = row_w + ((P + 1) & ~1) * 4;
+        row_t = jobs + (U + P / 16) * (int)sizeof(MoeJob);
+        total = row_t + P * 2;
+    }
+};
+
+// A few pairs: the hidden rows fit the second product's LDS, which quantizes
+// them for itself and adds up each token's experts (two launches), and the
+// first product takes a part of a 128-column block a workgroup, as there are
+// fewer blocks than CUs.  More pairs: 128 columns quantized by the first
+// product, the second writes every pair's product, a third launch adds them up.
+// Above 80 KB one workgroup of the second product takes a CU, so all of its
+// H / 16 have to fit the 256 CUs at once (2 tokens, 8 experts of 7168 x 2048:
+// 124 us instead of 105 otherwise).
+inline bool few_pairs(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+    const int64_t P = T * k, U = std::min(P, E);
+    if (T > 16 || P * I > 131072 || U * (I / 128) > 256) return false;
+    const int lds = MoeDownLds((int)T, (int)P, (int)U, (int)I).total;
+    return lds <= 80 * 1024 || (lds <= 156 * 1024 && H <= 4096);
+}
 
 // Workspace layout, in bytes from its start.
 struct MoeLayout {
@@ -45,7 +72,7 @@ struct MoeLayout {
         order = units + up(U * sizeof(MoeUnit));
         place = order + up(P * 4);
         codes = place + up(P * 4);
-        const bool few = few_pairs(T, k, I);
+        const bool few = few_pairs(T, k, E, H, I);
         scales = codes + (few ? 0 : up(P * I));
         hidden = scales + (few ? 0 : up(P * ((I / 128 + 3) & ~int64_t(3)) * 4));
         out = hidden + (few ? up(P * I * 4) : 0);
@@ -169,9 +196,11 @@ __global__ __launch_bounds__(64 * W) void moe_gate_up_kernel(
     using S = typename std::conditional<kE8, uint8_t, float>::type;
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr bool kFree = R <= 2;
-    static_assert(W == kPanelWaves || (W == 4 && kFree), "whole 128-column blocks, or halves in fp32");
+    static_assert(W == kPanelWaves || kFree, "whole 128-column blocks, or a part of one in fp32");
+    constexpr int kA = panel_a_loads(R, W, kFree ? kChunk : 1);
     uint16_t* const list = reinterpret_cast<uint16_t*>(smem + gate_lds<R, D, W>());
-    __shared__ uint32_t tops[16 * R][kPanelWaves];
+    uint32_t* const tops = reinterpret_cast<uint32_t*>(smem);  // [16 R][W], once the ring is free
+    static_assert(16 * R * W * 4 <= sizeof(PanelStage<R, 2>), "the magnitudes fit the ring");
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
@@ -191,7 +220,7 @@ __global__ __launch_bounds__(64 * W) void moe_gate_up_kernel(
     PanelLoads<2> p;
     p.bufB = buffer_rsrc(w13 + (int64_t)u.e * 2 * I * H, (uint32_t)(2 * I) * (uint32_t)H);
     p.bufA = buffer_rsrc(x, (uint32_t)(P / k) * (uint32_t)H);
-    p.bufS = wave == 0 ? buffer_rsrc(sx_v, (uint32_t)(P / k) * SP * kSz)
+    p.bufS = wave != 1 ? buffer_rsrc(sx_v, (uint32_t)(P / k) * SP * kSz)
                        : buffer_rsrc(static_cast<const S*>(s13_v) + (int64_t)u.e * NB * SP, (uint32_t)NB * SP * kSz);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -200,11 +229,12 @@ __global__ __launch_bounds__(64 * W) void moe_gate_up_kernel(
     for (int m0 = 0; m0 < u.count; m0 += 16 * R) {
         const int rows = min(u.count - m0, 16 * R);
 #pragma unroll
-        for (int j = 0; j < (kFree ? panel_a_loads(R, W) : 1); ++j) {
-            const int arow = 8 * (kFree ? (wave * panel_a_loads(R, W) + j) % (2 * R) : wave) + sub;
+        for (int j = 0; j < kA; ++j) {
+            const int arow = 8 * (kFree ? (wave * kA + j) % (2 * R) : wave * kA + j) + sub;
             p.offA[j] = arow < rows ? (uint32_t)(list[m0 + arow] / k) * (uint32_t)H + chunk : kNoRow;
         }
-        p.offS = wave == 0 && lane < rows ? (uint32_t)(list[m0 + lane] / k) * SP * kSz
+        const int srow = wave == 0 ? lane : R > 4 && wave == 2 ? 64 + lane : rows;  // whose scale this lane loads
+        p.offS = srow < rows  ? (uint32_t)(list[m0 + srow] / k) * SP * kSz
                  : wave == 1 && lane < 2  ? (uint32_t)((lane * I + (int)blockIdx.x * 16 * W) >> 7) * SP * kSz
                                           : kNoRow;
         v4f acc[R][2];
@@ -213,22 +243,14 @@ __global__ __launch_bounds__(64 * W) void moe_gate_up_kernel(
         else
             panel_product<R, 2, D, kE8, true>(smem, p, KB, rows, wave, lane, acc);
 
-        // silu(gate) * up, then the block's largest magnitude per row across
-        // the waves, compared as bits so that a NaN wins
         v4f h[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            uint32_t top = 0;
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float g = acc[r][0][q];
                 h[r][q] = g / (1.0f + expf(-g)) * acc[r][1][q];
-                top = max(top, __float_as_uint(h[r][q]) & 0x7fffffffu);
             }
-            top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-            top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-            if (lg == 0) tops[16 * r + lr][wave] = top;
-        }
         if constexpr (W != kPanelWaves) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -237,13 +259,24 @@ __global__ __launch_bounds__(64 * W) void moe_gate_up_kernel(
                         h[r];
             continue;
         }
+        // the block's largest magnitude per row across the waves, compared as
+        // bits so that a NaN wins
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top = max(top, __float_as_uint(h[r][q]) & 0x7fffffffu);
+            top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+            if (lg == 0) tops[(16 * r + lr) * W + wave] = top;
+        }
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = 16 * r + lr;
             uint32_t top = 0;
 #pragma unroll
-            for (int w = 0; w < kPanelWaves; ++w) top = max(top, tops[row][w]);
+            for (int w = 0; w < kPanelWaves; ++w) top = max(top, tops[row * W + w]);
             if (row >= rows) continue;
             uint32_t packed;
             const auto scale = quantize_hidden<kE8>(top, h[r], packed);
@@ -274,18 +307,23 @@ __global__ __launch_bounds__(64 * kPanelWaves) void moe_down_rows_kernel(
     const int sub = lane >> 3, col = blockIdx.x * 128 + wave * 16;
     const uint32_t chunk = panel_chunk(lane), kSz = sizeof(S);
     for (int m0 = 0; m0 < count; m0 += 16 * R) {
-        const int rows = min(count - m0, 16 * R), arow = 8 * wave + sub, row0 = start + m0;
+        const int rows = min(count - m0, 16 * R), row0 = start + m0;
         PanelLoads<1> p;
         // offsets fit 31 bits: H I <= 2^28, 16 R rows of I
         p.bufB = buffer_rsrc(w2 + (int64_t)e * H * I, (uint32_t)H * (uint32_t)I);
         p.bufA = buffer_rsrc(codes + (int64_t)row0 * I, (uint32_t)rows * (uint32_t)I);
-        p.bufS = wave == 0
+        p.bufS = wave != 1
                      ? buffer_rsrc(static_cast<const S*>(sh_v) + (int64_t)row0 * SP, (uint32_t)rows * SP * kSz)
                      : buffer_rsrc(static_cast<const S*>(s2_v) + (int64_t)e * NB * SP, (uint32_t)NB * SP * kSz);
 #pragma unroll
         for (int j = 0; j < 2; ++j) p.offB[j] = (uint32_t)(col + 8 * j + sub) * (uint32_t)I + chunk;
-        p.offA[0] = arow < rows ? (uint32_t)arow * (uint32_t)I + chunk : kNoRow;
-        p.offS = wave == 0 && lane < rows ? (uint32_t)lane * SP * kSz
+#pragma unroll
+        for (int j = 0; j < panel_a_loads(R, kPanelWaves, 1); ++j) {
+            const int arow = 8 * (wave * panel_a_loads(R, kPanelWaves, 1) + j) + sub;
+            p.offA[j] = arow < rows ? (uint32_t)arow * (uint32_t)I + chunk : kNoRow;
+        }
+        const int srow = wave == 0 ? lane : R > 4 && wave == 2 ? 64 + lane : rows;  // whose scale this lane loads
+        p.offS = srow < rows                ? (uint32_t)srow * SP * kSz
                  : wave == 1 && lane == 0 ? (uint32_t)blockIdx.x * SP * kSz
                                           : kNoRow;
         v4f acc[R][1];
@@ -326,24 +364,6 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
 // each streaming its share of the weights through a ring of its own in LDS,
 // with no barrier.  A wave adds its weighted products to a slice of its own
 // ([token][16] fp32); the slices are summed in wave order at the end.
-constexpr int kDownWaves = 8, kDownRing = 3;
-
-struct MoeDownLds {
-    int ring, codes, scales, cols, slices, row_w, jobs, row_t, total;
-    __host__ __device__ MoeDownLds(int T, int P, int U, int I) {
-        ring = 0;
-        codes = kDownWaves * kDownRing * 2048;        // [P][I], chunk c of row r at c ^ (r & 7)
-        scales = codes + P * I;                       // [P][I / 128]
-        cols = scales + P * (I >> 7) * 4;             // [jobs][I / 128]
-        slices = cols + (U + P / 16) * (I >> 7) * 4;  // [wave][T][16]
-        slices = (slices + 15) & ~15;
-        row_w = slices + kDownWaves * T * 64;
-        jobs = row_w + ((P + 1) & ~1) * 4;
-        row_t = jobs + (U + P / 16) * (int)sizeof(MoeJob);
-        total = row_t + P * 2;
-    }
-};
-
 template <int kCtrl>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xf, 0xf, false);
@@ -389,7 +409,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(
             v[n][1] = *reinterpret_cast<const v4f*>(from + 4);
         }
     };
-    int pair = 0;  // of row threadIdx.x; P <= 256
+    int pair = 0;  // of row threadIdx.x: P <= 16 * 16
     if ((int)threadIdx.x < P) pair = order[threadIdx.x];
     fetch(0);
     if (wave == 0) {
@@ -536,6 +556,10 @@ int64_t moe_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     return MoeLayout(T, k, E, H, I).total;
 }
 
+// Whether a launch's dynamic LDS fits a CU's 160 KB beside a kernel's own few
+// hundred bytes (rounded up to 1 KB): a launch past it would abort the queue.
+static bool lds_fits(size_t bytes) { return bytes + 1024 <= 160 * 1024; }
+
 template <bool kE8>
 static dg_status moe_few(const MoeArgs& a, hipStream_t stream) {
     const MoeLayout at(a.T, a.k, a.E, a.H, a.I);
@@ -544,14 +568,24 @@ static dg_status moe_few(const MoeArgs& a, hipStream_t stream) {
     int32_t* const order = reinterpret_cast<int32_t*>(ws + at.order);
     float* const hidden = reinterpret_cast<float*>(ws + at.hidden);
     const int P = a.T * a.k, U = std::min(P, a.E);
-    constexpr int D = 4, W = 4;
-    hipLaunchKernelGGL((moe_gate_up_kernel<1, D, W, kE8>), dim3(a.I / 64, U), dim3(64 * W),
-                       (gate_lds<1, D, W>()) + P * 2, stream, a.x, a.sx, a.ids, a.w13, a.s13, units, order,
-                       reinterpret_cast<int32_t*>(ws + at.place), nullptr, nullptr, hidden, P, a.k, a.E, a.H,
-                       a.I, P <= a.E);
+    auto first = [&](auto waves, auto depth) {
+        constexpr int W = decltype(waves)::value, D = decltype(depth)::value;
+        static_assert(gate_lds<1, D, W>() + 512 + 1024 <= 160 * 1024, "P <= 16 * 16");
+        hipLaunchKernelGGL((moe_gate_up_kernel<1, D, W, kE8>), dim3(a.I / (16 * W), U), dim3(64 * W),
+                           (gate_lds<1, D, W>()) + P * 2, stream, a.x, a.sx, a.ids, a.w13, a.s13, units, order,
+                           reinterpret_cast<int32_t*>(ws + at.place), nullptr, nullptr, hidden, P, a.k, a.E, a.H,
+                           a.I, P <= a.E);
+    };
+    const size_t down_lds = MoeDownLds(a.T, P, U, a.I).total;
+    if (!lds_fits(down_lds)) return DG_ERR_UNSUPPORTED;
+    // 32 columns a workgroup where 64 would leave many CUs without one
+    if (U * (a.I / 64) >= 192)
+        first(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+    else
+        first(std::integral_constant<int, 2>{}, std::integral_constant<int, 6>{});
     if (launched() != DG_OK) return DG_ERR_HIP;
     hipLaunchKernelGGL((moe_down_kernel<kE8>), dim3(a.H / 16), dim3(64 * kDownWaves),
-                       MoeDownLds(a.T, P, U, a.I).total, stream, hidden, a.weights, a.w2, a.s2, units, order,
+                       down_lds, stream, hidden, a.weights, a.w2, a.s2, units, order,
                        a.y, a.T, U, a.k, a.H, a.I);
     return launched();
 }
@@ -564,9 +598,11 @@ static dg_status moe_many(const MoeArgs& a, hipStream_t stream) {
     int32_t* const place = reinterpret_cast<int32_t*>(ws + at.place);
     float* const out = reinterpret_cast<float*>(ws + at.out);
     const int P = a.T * a.k, U = std::min(P, a.E);
-    constexpr int D = R == 1 ? 4 : 3, D2 = 3;
+    constexpr int D = R == 1 ? 4 : 3, D2 = R == 8 ? 2 : 3;
+    const size_t gate = gate_lds<R, D, kPanelWaves>() + P * 2;
+    if (!lds_fits(gate) || !lds_fits(panel_lds<R, 1, D2>())) return DG_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((moe_gate_up_kernel<R, D, kPanelWaves, kE8>), dim3(a.I / 128, U), dim3(64 * kPanelWaves),
-                       (gate_lds<R, D, kPanelWaves>()) + P * 2, stream, a.x, a.sx, a.ids, a.w13, a.s13, units,
+                       gate, stream, a.x, a.sx, a.ids, a.w13, a.s13, units,
                        reinterpret_cast<int32_t*>(ws + at.order), place, ws + at.codes, ws + at.scales, nullptr,
                        P, a.k, a.E, a.H, a.I, P <= a.E);
     if (launched() != DG_OK) return DG_ERR_HIP;
@@ -581,10 +617,11 @@ static dg_status moe_many(const MoeArgs& a, hipStream_t stream) {
 
 template <bool kE8>
 static dg_status moe_scales(const MoeArgs& a, hipStream_t stream) {
-    if (few_pairs(a.T, a.k, a.I)) return moe_few<kE8>(a, stream);
+    if (few_pairs(a.T, a.k, a.E, a.H, a.I)) return moe_few<kE8>(a, stream);
     if (a.T <= 16) return moe_many<1, kE8>(a, stream);
     if (a.T <= 32) return moe_many<2, kE8>(a, stream);
-    return moe_many<4, kE8>(a, stream);
+    if (a.T <= 64) return moe_many<4, kE8>(a, stream);
+    return moe_many<8, kE8>(a, stream);
 }
 
 dg_status launch_moe(const MoeArgs& a, bool e8m0, hipStream_t stream) {
