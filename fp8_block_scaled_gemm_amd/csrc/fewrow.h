@@ -73,23 +73,38 @@ __device__ __forceinline__ void multiply_exact(const Block<R, C, kE8>& k, int ro
     v8bf b[C][4];
 #pragma unroll
     for (int c = 0; c < C; ++c) widen(k.b[c], b[c]);
+    // two row tiles at a time: four chains of dependent products in flight
+    constexpr int kPair = R >= 2 ? 2 : 1;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (r > 0 && 16 * r >= rows) break;
-        v8bf a[4];
-        widen(k.a[r], a);
+    for (int r0 = 0; r0 < R; r0 += kPair) {
+        if (r0 > 0 && 16 * r0 >= rows) break;
+        v8bf a[kPair][4];
+        v4f p[kPair][C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            v4f p = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < kPair; ++r) {
+            widen(k.a[r0 + r], a[r]);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[c][s], a[s], p, 0, 0, 0);
-            if constexpr (kE8) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[r][c][q] += scale_e8(p[q], k.sa[r], k.sb[c]);
-            } else {
-                acc[r][c] += (k.sa[r] * k.sb[c]) * p;
-            }
+            for (int c = 0; c < C; ++c) p[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
         }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int r = 0; r < kPair; ++r)
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    p[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[c][s], a[r][s], p[r][c], 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < kPair; ++r)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if constexpr (kE8) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        acc[r0 + r][c][q] += scale_e8(p[r][c][q], k.sa[r0 + r], k.sb[c]);
+                } else {
+                    acc[r0 + r][c] += (k.sa[r0 + r] * k.sb[c]) * p[r][c];
+                }
+            }
     }
 }
 
@@ -238,22 +253,25 @@ __device__ __forceinline__ void panel_product(uint8_t* smem, const PanelLoads<C>
 // scales come in chunks of four K blocks, double-buffered, one barrier per
 // chunk; in between every wave runs on its own through its private ring of B.
 // (A lone workgroup on a CU streams 35 GB/s with the barrier per K block.)
-template <int R, int C, int D, int W>
+// A chunk is asked for NA - 1 chunks ahead: a wave waits for its loads in order,
+// so waiting for the next chunk leaves the B loads of NA - 1 chunks in flight
+// (NA = 2: at most four K blocks, however deep the ring).
+template <int R, int C, int D, int W, int NA>
 struct FreePanel {
     uint8_t b[D][W * C * 2048];
-    uint8_t a[2][kChunk][16 * R * 128];
-    float sa[2][256];  // [row][kChunk]; E8M0: one word per row
-    float sb[2][256];  // [c][kChunk]
+    uint8_t a[NA][kChunk][16 * R * 128];
+    float sa[NA][256];  // [row][kChunk]; E8M0: one word per row
+    float sb[NA][256];  // [c][kChunk]
     uint8_t unused[1024];
 };
 
-template <int R, int C, int D, int W, bool kE8, bool kExact>
+template <int R, int C, int D, int W, int NA, bool kE8, bool kExact>
 __device__ __forceinline__ void free_panel_product(uint8_t* smem, const PanelLoads<C>& p, int KB, int rows,
                                                    int wave, int lane, v4f (&acc)[R][C]) {
     static_assert(R <= 2, "A chunks of more rows do not fit beside the ring");
     constexpr int kA = panel_a_loads(R, W, kChunk);
     static_assert(kA * W == 2 * R * kChunk, "every load of a chunk has a wave");
-    FreePanel<R, C, D, W>& s = *reinterpret_cast<FreePanel<R, C, D, W>*>(smem);
+    FreePanel<R, C, D, W, NA>& s = *reinterpret_cast<FreePanel<R, C, D, W, NA>*>(smem);
     const int lr = lane & 15, lg = lane >> 4;
     auto issue_b = [&](int kb, int st) __attribute__((always_inline)) {
 #pragma unroll
@@ -275,16 +293,17 @@ __device__ __forceinline__ void free_panel_product(uint8_t* smem, const PanelLoa
             load_lds_16(p.bufS, off, to);
     };
     clear(acc);
-    issue_chunk(0, 0);
+#pragma unroll
+    for (int c = 0; c < NA - 1; ++c) issue_chunk(c * kChunk, c);
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) issue_b(d, d);
     wait_vmcnt_lgkm0<2 * C * (D - 1)>();
     lds_barrier();
     const int lo = (lg ^ (lr & 7)) << 4, hi = lo ^ 64;
-    int at = 0;
+    int at = 0, buf = 0;
     for (int kb0 = 0; kb0 < KB; kb0 += kChunk) {
-        const int buf = (kb0 / kChunk) & 1;
-        issue_chunk(kb0 + kChunk, buf ^ 1);  // its last reader passed the barrier below
+        // into the buffer of the last chunk, whose readers passed the barrier below
+        issue_chunk(kb0 + (NA - 1) * kChunk, buf == 0 ? NA - 1 : buf - 1);
 #pragma unroll
         for (int kk = 0; kk < kChunk; ++kk) {
             const int kb = kb0 + kk;
@@ -320,8 +339,10 @@ __device__ __forceinline__ void free_panel_product(uint8_t* smem, const PanelLoa
                 at = at == D - 1 ? 0 : at + 1;
             }
         }
-        wait_vmcnt_lgkm0<2 * C * kChunk>();  // the next chunk, loaded before these K blocks' B
+        // the next chunk: NA - 1 chunks' K blocks of B and NA - 2 chunks follow it
+        wait_vmcnt_lgkm0<2 * C * kChunk*(NA - 1) + (kA + 1) * (NA - 2)>();
         lds_barrier();
+        buf = buf == NA - 1 ? 0 : buf + 1;
     }
     wait_vmcnt_lgkm0<0>();
     lds_barrier();

@@ -47,19 +47,16 @@ struct MoeDownLds {
     }
 };
 
-// A few pairs: the hidden rows fit the second product's LDS, which quantizes
+// A few pairs: the hidden rows fit half a CU's LDS in the second product (so
+// that two of its workgroups share a CU), which quantizes
 // them for itself and adds up each token's experts (two launches), and the
 // first product takes a part of a 128-column block a workgroup, as there are
 // fewer blocks than CUs.  More pairs: 128 columns quantized by the first
 // product, the second writes every pair's product, a third launch adds them up.
-// Above 80 KB one workgroup of the second product takes a CU, so all of its
-// H / 16 have to fit the 256 CUs at once (2 tokens, 8 experts of 7168 x 2048:
-// 124 us instead of 105 otherwise).
-inline bool few_pairs(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+// (2 tokens, 8 experts of 7168 x 2048 as a few pairs: 124 us instead of 104.)
+inline bool few_pairs(int64_t T, int64_t k, int64_t E, int64_t I) {
     const int64_t P = T * k, U = std::min(P, E);
-    if (T > 16 || P * I > 131072 || U * (I / 128) > 256) return false;
-    const int lds = MoeDownLds((int)T, (int)P, (int)U, (int)I).total;
-    return lds <= 80 * 1024 || (lds <= 156 * 1024 && H <= 4096);
+    return T <= 16 && P * I <= 32768 && MoeDownLds((int)T, (int)P, (int)U, (int)I).total <= 80 * 1024;
 }
 
 // Workspace layout, in bytes from its start.
@@ -72,7 +69,7 @@ struct MoeLayout {
         order = units + up(U * sizeof(MoeUnit));
         place = order + up(P * 4);
         codes = place + up(P * 4);
-        const bool few = few_pairs(T, k, E, H, I);
+        const bool few = few_pairs(T, k, E, I);
         scales = codes + (few ? 0 : up(P * I));
         hidden = scales + (few ? 0 : up(P * ((I / 128 + 3) & ~int64_t(3)) * 4));
         out = hidden + (few ? up(P * I * 4) : 0);
@@ -178,10 +175,11 @@ __device__ __forceinline__ typename std::conditional<kE8, int, float>::type quan
 // the second product to quantize: for a few pairs there are too few 128
 // column blocks to give every CU one, and a CU alone streams only 36 GB/s
 // (8 pairs of 7168 x 2048: 51 us with 128 workgroups of 128 columns).
+constexpr int gate_chunks(int W) { return W < kPanelWaves ? 4 : 2; }  // A buffers of a free panel
 template <int R, int D, int W>
 constexpr size_t gate_lds() {
     if constexpr (R <= 2)
-        return sizeof(FreePanel<R, 2, D, W>);
+        return sizeof(FreePanel<R, 2, D, W, gate_chunks(W)>);
     else
         return panel_lds<R, 2, D>();
 }
@@ -239,7 +237,7 @@ __global__ __launch_bounds__(64 * W) void moe_gate_up_kernel(
                                           : kNoRow;
         v4f acc[R][2];
         if constexpr (kFree)
-            free_panel_product<R, 2, D, W, kE8, true>(smem, p, KB, rows, wave, lane, acc);
+            free_panel_product<R, 2, D, W, gate_chunks(W), kE8, true>(smem, p, KB, rows, wave, lane, acc);
         else
             panel_product<R, 2, D, kE8, true>(smem, p, KB, rows, wave, lane, acc);
 
@@ -580,9 +578,9 @@ static dg_status moe_few(const MoeArgs& a, hipStream_t stream) {
     if (!lds_fits(down_lds)) return DG_ERR_UNSUPPORTED;
     // 32 columns a workgroup where 64 would leave many CUs without one
     if (U * (a.I / 64) >= 192)
-        first(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+        first(std::integral_constant<int, 4>{}, std::integral_constant<int, 5>{});
     else
-        first(std::integral_constant<int, 2>{}, std::integral_constant<int, 6>{});
+        first(std::integral_constant<int, 2>{}, std::integral_constant<int, 10>{});
     if (launched() != DG_OK) return DG_ERR_HIP;
     hipLaunchKernelGGL((moe_down_kernel<kE8>), dim3(a.H / 16), dim3(64 * kDownWaves),
                        down_lds, stream, hidden, a.weights, a.w2, a.s2, units, order,
@@ -617,7 +615,7 @@ static dg_status moe_many(const MoeArgs& a, hipStream_t stream) {
 
 template <bool kE8>
 static dg_status moe_scales(const MoeArgs& a, hipStream_t stream) {
-    if (few_pairs(a.T, a.k, a.E, a.H, a.I)) return moe_few<kE8>(a, stream);
+    if (few_pairs(a.T, a.k, a.E, a.I)) return moe_few<kE8>(a, stream);
     if (a.T <= 16) return moe_many<1, kE8>(a, stream);
     if (a.T <= 32) return moe_many<2, kE8>(a, stream);
     if (a.T <= 64) return moe_many<4, kE8>(a, stream);
