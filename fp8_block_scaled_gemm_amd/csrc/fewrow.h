@@ -253,25 +253,27 @@ __device__ __forceinline__ void panel_product(uint8_t* smem, const PanelLoads<C>
 // scales come in chunks of four K blocks, double-buffered, one barrier per
 // chunk; in between every wave runs on its own through its private ring of B.
 // (A lone workgroup on a CU streams 35 GB/s with the barrier per K block.)
-// A chunk is asked for NA - 1 chunks ahead: a wave waits for its loads in order,
-// so waiting for the next chunk leaves the B loads of NA - 1 chunks in flight
-// (NA = 2: at most four K blocks, however deep the ring).
-template <int R, int C, int D, int W, int NA>
+// A wave waits for its loads in order, so waiting for the next chunk leaves at
+// most the four K blocks of B behind it in flight: deeper rings gain nothing.
+template <int R, int C, int D, int W>
 struct FreePanel {
+    static_assert(W >= 2, "wave 0 loads the row scales, wave 1 the column scales");
     uint8_t b[D][W * C * 2048];
-    uint8_t a[NA][kChunk][16 * R * 128];
-    float sa[NA][256];  // [row][kChunk]; E8M0: one word per row
-    float sb[NA][256];  // [c][kChunk]
+    uint8_t a[2][kChunk][16 * R * 128];
+    float sa[2][256];  // [row][kChunk]; E8M0: one word per row
+    float sb[2][256];  // [c][kChunk]
     uint8_t unused[1024];
 };
 
-template <int R, int C, int D, int W, int NA, bool kE8, bool kExact>
-__device__ __forceinline__ void free_panel_product(uint8_t* smem, const PanelLoads<C>& p, int KB, int rows,
-                                                   int wave, int lane, v4f (&acc)[R][C]) {
+// `trips` chunks are walked (all waves of the workgroup alike), of which the
+// first KB K blocks exist.
+template <int R, int C, int D, int W, bool kE8, bool kExact>
+__device__ __forceinline__ void free_panel_product(uint8_t* smem, const PanelLoads<C>& p, int KB, int trips,
+                                                   int rows, int wave, int lane, v4f (&acc)[R][C]) {
     static_assert(R <= 2, "A chunks of more rows do not fit beside the ring");
     constexpr int kA = panel_a_loads(R, W, kChunk);
     static_assert(kA * W == 2 * R * kChunk, "every load of a chunk has a wave");
-    FreePanel<R, C, D, W, NA>& s = *reinterpret_cast<FreePanel<R, C, D, W, NA>*>(smem);
+    FreePanel<R, C, D, W>& s = *reinterpret_cast<FreePanel<R, C, D, W>*>(smem);
     const int lr = lane & 15, lg = lane >> 4;
     auto issue_b = [&](int kb, int st) __attribute__((always_inline)) {
 #pragma unroll
@@ -293,17 +295,15 @@ __device__ __forceinline__ void free_panel_product(uint8_t* smem, const PanelLoa
             load_lds_16(p.bufS, off, to);
     };
     clear(acc);
-#pragma unroll
-    for (int c = 0; c < NA - 1; ++c) issue_chunk(c * kChunk, c);
+    issue_chunk(0, 0);
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) issue_b(d, d);
     wait_vmcnt_lgkm0<2 * C * (D - 1)>();
     lds_barrier();
     const int lo = (lg ^ (lr & 7)) << 4, hi = lo ^ 64;
     int at = 0, buf = 0;
-    for (int kb0 = 0; kb0 < KB; kb0 += kChunk) {
-        // into the buffer of the last chunk, whose readers passed the barrier below
-        issue_chunk(kb0 + (NA - 1) * kChunk, buf == 0 ? NA - 1 : buf - 1);
+    for (int kb0 = 0; kb0 < trips * kChunk; kb0 += kChunk) {
+        issue_chunk(kb0 + kChunk, buf ^ 1);  // its last readers passed the barrier below
 #pragma unroll
         for (int kk = 0; kk < kChunk; ++kk) {
             const int kb = kb0 + kk;
@@ -339,10 +339,9 @@ __device__ __forceinline__ void free_panel_product(uint8_t* smem, const PanelLoa
                 at = at == D - 1 ? 0 : at + 1;
             }
         }
-        // the next chunk: NA - 1 chunks' K blocks of B and NA - 2 chunks follow it
-        wait_vmcnt_lgkm0<2 * C * kChunk*(NA - 1) + (kA + 1) * (NA - 2)>();
+        wait_vmcnt_lgkm0<2 * C * kChunk>();  // the next chunk, loaded before these K blocks' B
         lds_barrier();
-        buf = buf == NA - 1 ? 0 : buf + 1;
+        buf ^= 1;
     }
     wait_vmcnt_lgkm0<0>();
     lds_barrier();

@@ -175,17 +175,19 @@ __device__ __forceinline__ typename std::conditional<kE8, int, float>::type quan
 // the second product to quantize: for a few pairs there are too few 128
 // column blocks to give every CU one, and a CU alone streams only 36 GB/s
 // (8 pairs of 7168 x 2048: 51 us with 128 workgroups of 128 columns).
-constexpr int gate_chunks(int W) { return W < kPanelWaves ? 4 : 2; }  // A buffers of a free panel
-template <int R, int D, int W>
+// A wave alone takes about 0.37 us per K block of 4 KB (reads, widening and
+// products in sequence), so where even 64 columns leave CUs idle the workgroup
+// takes fewer columns and KS groups of W waves split K.
+template <int R, int D, int W, int KS>
 constexpr size_t gate_lds() {
     if constexpr (R <= 2)
-        return sizeof(FreePanel<R, 2, D, W, gate_chunks(W)>);
+        return KS * sizeof(FreePanel<R, 2, D, W>);
     else
         return panel_lds<R, 2, D>();
 }
 
-template <int R, int D, int W, bool kE8>
-__global__ __launch_bounds__(64 * W) void moe_gate_up_kernel(
+template <int R, int D, int W, int KS, bool kE8>
+__global__ __launch_bounds__(64 * W * KS) void moe_gate_up_kernel(
     const uint8_t* __restrict__ x, const void* __restrict__ sx_v, const int32_t* __restrict__ ids,
     const uint8_t* __restrict__ w13, const void* __restrict__ s13_v, MoeUnit* __restrict__ units,
     int32_t* __restrict__ order, int32_t* __restrict__ place, uint8_t* __restrict__ codes,
@@ -196,17 +198,19 @@ __global__ __launch_bounds__(64 * W) void moe_gate_up_kernel(
     constexpr bool kFree = R <= 2;
     static_assert(W == kPanelWaves || kFree, "whole 128-column blocks, or a part of one in fp32");
     constexpr int kA = panel_a_loads(R, W, kFree ? kChunk : 1);
-    uint16_t* const list = reinterpret_cast<uint16_t*>(smem + gate_lds<R, D, W>());
+    uint16_t* const list = reinterpret_cast<uint16_t*>(smem + gate_lds<R, D, W, KS>());
     uint32_t* const tops = reinterpret_cast<uint32_t*>(smem);  // [16 R][W], once the ring is free
     static_assert(16 * R * W * 4 <= sizeof(PanelStage<R, 2>), "the magnitudes fit the ring");
 
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    static_assert(KS == 1 || W < kPanelWaves, "K is split where there are few columns");
+    const int lane = threadIdx.x & 63, at = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = at % W, share = at / W;  // this wave's columns, its share of K
     const int lr = lane & 15, lg = lane >> 4;
-    const MoeUnit u = find_unit<W>(ids, P, E, blockIdx.y, by_pair, reinterpret_cast<int*>(smem), list);
+    const MoeUnit u = find_unit<W * KS>(ids, P, E, blockIdx.y, by_pair, reinterpret_cast<int*>(smem), list);
     if (blockIdx.x == 0 && threadIdx.x == 0) units[blockIdx.y] = u;
     if (u.count == 0) return;
     if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < u.count; i += 64 * W) {
+        for (int i = threadIdx.x; i < u.count; i += 64 * W * KS) {
             order[u.start + i] = list[i];
             place[list[i]] = u.start + i;
         }
@@ -236,9 +240,43 @@ __global__ __launch_bounds__(64 * W) void moe_gate_up_kernel(
                  : wave == 1 && lane < 2  ? (uint32_t)((lane * I + (int)blockIdx.x * 16 * W) >> 7) * SP * kSz
                                           : kNoRow;
         v4f acc[R][2];
-        if constexpr (kFree)
-            free_panel_product<R, 2, D, W, gate_chunks(W), kE8, true>(smem, p, KB, rows, wave, lane, acc);
-        else
+        if constexpr (kFree) {
+            using Panel = FreePanel<R, 2, D, W>;
+            const int chunks = (KB + kChunk - 1) / kChunk, trips = (chunks + KS - 1) / KS, kb0 = share * trips * kChunk;
+            PanelLoads<2> q = p;
+            if (KS > 1) {
+                q.offS += kb0 * kSz;
+#pragma unroll
+                for (int j = 0; j < kA; ++j) q.offA[j] += kb0 * 128;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q.offB[j] += kb0 * 128;
+            }
+            free_panel_product<R, 2, D, W, kE8, true>(
+                smem + share * sizeof(Panel), q, min(max(KB - kb0, 0), trips * kChunk), trips, rows, wave, lane, acc);
+            if constexpr (KS > 1) {
+                // the shares' sums meet in LDS, in order; the ring is free
+                v4f* const part = reinterpret_cast<v4f*>(smem);
+                static_assert(KS * W * R * 2 * 64 * 16 <= gate_lds<R, D, W, KS>(), "the sums fit the ring");
+                if (share > 0) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) part[((at * R + r) * 2 + c) * 64 + lane] = acc[r][c];
+                }
+                __syncthreads();
+                if (share == 0) {
+#pragma unroll
+                    for (int s = 1; s < KS; ++s)
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                acc[r][c] += part[(((s * W + wave) * R + r) * 2 + c) * 64 + lane];
+                }
+                __syncthreads();
+                if (share > 0) continue;
+            }
+        } else
             panel_product<R, 2, D, kE8, true>(smem, p, KB, rows, wave, lane, acc);
 
         v4f h[R];
@@ -566,21 +604,23 @@ static dg_status moe_few(const MoeArgs& a, hipStream_t stream) {
     int32_t* const order = reinterpret_cast<int32_t*>(ws + at.order);
     float* const hidden = reinterpret_cast<float*>(ws + at.hidden);
     const int P = a.T * a.k, U = std::min(P, a.E);
-    auto first = [&](auto waves, auto depth) {
-        constexpr int W = decltype(waves)::value, D = decltype(depth)::value;
-        static_assert(gate_lds<1, D, W>() + 512 + 1024 <= 160 * 1024, "P <= 16 * 16");
-        hipLaunchKernelGGL((moe_gate_up_kernel<1, D, W, kE8>), dim3(a.I / (16 * W), U), dim3(64 * W),
-                           (gate_lds<1, D, W>()) + P * 2, stream, a.x, a.sx, a.ids, a.w13, a.s13, units, order,
+    auto first = [&](auto waves, auto shares, auto depth) {
+        constexpr int W = decltype(waves)::value, KS = decltype(shares)::value, D = decltype(depth)::value;
+        static_assert(gate_lds<1, D, W, KS>() + 512 + 1024 <= 160 * 1024, "P <= 16 * 16");
+        hipLaunchKernelGGL((moe_gate_up_kernel<1, D, W, KS, kE8>), dim3(a.I / (16 * W), U), dim3(64 * W * KS),
+                           (gate_lds<1, D, W, KS>()) + P * 2, stream, a.x, a.sx, a.ids, a.w13, a.s13, units, order,
                            reinterpret_cast<int32_t*>(ws + at.place), nullptr, nullptr, hidden, P, a.k, a.E, a.H,
                            a.I, P <= a.E);
     };
     const size_t down_lds = MoeDownLds(a.T, P, U, a.I).total;
     if (!lds_fits(down_lds)) return DG_ERR_UNSUPPORTED;
-    // 32 columns a workgroup where 64 would leave many CUs without one
+    using std::integral_constant;
+    // 2 pairs of 4096 x 1792: 11.5 us as 112 workgroups with K in two shares,
+    // 14.5 as 56 of 64 columns, 17.8 as 112 of 32 with K whole
     if (U * (a.I / 64) >= 192)
-        first(std::integral_constant<int, 4>{}, std::integral_constant<int, 5>{});
+        first(integral_constant<int, 4>{}, integral_constant<int, 1>{}, integral_constant<int, 4>{});
     else
-        first(std::integral_constant<int, 2>{}, std::integral_constant<int, 10>{});
+        first(integral_constant<int, 2>{}, integral_constant<int, 2>{}, integral_constant<int, 5>{});
     if (launched() != DG_OK) return DG_ERR_HIP;
     hipLaunchKernelGGL((moe_down_kernel<kE8>), dim3(a.H / 16), dim3(64 * kDownWaves),
                        down_lds, stream, hidden, a.weights, a.w2, a.s2, units, order,
@@ -597,9 +637,9 @@ static dg_status moe_many(const MoeArgs& a, hipStream_t stream) {
     float* const out = reinterpret_cast<float*>(ws + at.out);
     const int P = a.T * a.k, U = std::min(P, a.E);
     constexpr int D = R == 1 ? 4 : 3, D2 = R == 8 ? 2 : 3;
-    const size_t gate = gate_lds<R, D, kPanelWaves>() + P * 2;
+    const size_t gate = gate_lds<R, D, kPanelWaves, 1>() + P * 2;
     if (!lds_fits(gate) || !lds_fits(panel_lds<R, 1, D2>())) return DG_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((moe_gate_up_kernel<R, D, kPanelWaves, kE8>), dim3(a.I / 128, U), dim3(64 * kPanelWaves),
+    hipLaunchKernelGGL((moe_gate_up_kernel<R, D, kPanelWaves, 1, kE8>), dim3(a.I / 128, U), dim3(64 * kPanelWaves),
                        gate, stream, a.x, a.sx, a.ids, a.w13, a.s13, units,
                        reinterpret_cast<int32_t*>(ws + at.order), place, ws + at.codes, ws + at.scales, nullptr,
                        P, a.k, a.E, a.H, a.I, P <= a.E);
