@@ -33,6 +33,7 @@
 //     time, so that concurrent tiles on one XCD share A and B slabs in its L2.
 #include "device_common.h"
 #include "launch.h"
+#include "wave_ops.h"
 
 #include <algorithm>
 #include <atomic>
@@ -232,9 +233,7 @@ __device__ __forceinline__ void add_lora(v4f (&acc)[T::TM][T::TN], uint8_t* smem
         int low = kNone;
         for (int r = lane; r < T::BM; r += 64)
             if (ids[r] > after) low = min(low, ids[r]);
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) low = min(low, __shfl_xor(low, d, 64));
-        return __builtin_amdgcn_readfirstlane(low);
+        return wave_min(low);
     };
     const int first = next_id(-1);
     if (first == kNone) return;

@@ -15,6 +15,7 @@
 
 #include "fewrow.h"
 #include "quantize_common.h"
+#include "wave_ops.h"
 
 namespace dg {
 
@@ -400,11 +401,6 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
 // each streaming its share of the weights through a ring of its own in LDS,
 // with no barrier.  A wave adds its weighted products to a slice of its own
 // ([token][16] fp32); the slices are summed in wave order at the end.
-template <int kCtrl>
-__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xf, 0xf, false);
-}
-
 template <bool kE8>
 __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(
     const float* __restrict__ hidden, const float* __restrict__ weights, const uint8_t* __restrict__ w2,
@@ -490,10 +486,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(
             uint32_t top = 0;
 #pragma unroll
             for (int q = 0; q < 8; ++q) top = max(top, __float_as_uint(v[n][q >> 2][q & 3]) & 0x7fffffffu);
-            top = max(top, dpp_u32<0xb1>(top));   // over 16 lanes: swap neighbours, pairs,
-            top = max(top, dpp_u32<0x4e>(top));   // then mirror 8 and 16
-            top = max(top, dpp_u32<0x141>(top));
-            top = max(top, dpp_u32<0x140>(top));
+            top = row_max(top);
             uint32_t w[2];
             const V s = quantize_hidden<kE8>(top, v[n][0], w[0]);
             quantize_hidden<kE8>(top, v[n][1], w[1]);
