@@ -3,7 +3,7 @@
 Every function here has the name of the C-ABI entry point it calls
 (include/dg_fp8.h, include/dg_ops.h) and only marshals arguments: it checks torch tensor
 dtypes, shapes and devices, passes raw device pointers and the current HIP
-stream, and raises ``DGError`` on a nonzero status.  All arithmetic runs in
+stream (the operators of dg_ops.h through the compiled binding _binding.so), and raises ``DGError`` on a nonzero status.  All arithmetic runs in
 the HIP kernels of ``libdgfp8.so``; there is no CPU fallback, and importing a
 function fails loudly when the library has not been built
 (``python -m fp8_block_scaled_gemm_amd.build``).
@@ -17,7 +17,6 @@ are contiguous and 16-byte aligned.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -350,75 +349,45 @@ def dg_quantize_fp8_per_block_e8m0(x, q=None, s=None):
 
 # ------------------------------- operators around the products (dg_ops.h)
 
+# Argument checks, allocation and the call itself run in _binding.so
+# (csrc/binding.cpp): these operators take microseconds, and checking ten
+# tensors in Python took as long as they do.
+
 _SCORING = {"softmax": 0, "sigmoid": 1}
+_native = None
 
 
-def _ptr(t, what, dtype, shape, dev):
-    """The data pointer of a contiguous tensor of this dtype and shape on this
-    device, which is a GPU; raises like ``_check`` otherwise.  The common case
-    is one comparison each: these calls are a few microseconds long."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _check(t, what, dtype, shape)
-    raise ValueError(f"all tensors of a call must be on one device, got {dev} and {t.device}")
+def _ops():
+    """The compiled binding; raises if it has not been built."""
+    global _native
+    if _native is None:
+        load_library()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError("the compiled binding is missing or does not load: build it with "
+                              "`python -m fp8_block_scaled_gemm_amd.build`") from e
+        _native = _binding
+    return _native
 
 
-def _codes_ptr(t, what, shape, dev):
-    if getattr(t, "dtype", None) is torch.float8_e4m3fn:
-        t = t.view(torch.uint8)
-    return _ptr(t, what, torch.uint8, shape, dev)
+def _raw_stream(t):
+    """torch.cuda.current_stream(t.device).cuda_stream, without its object."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if getattr(t, "is_cuda", False) else 0
 
 
-def _bf16_ptr(t, what, shape, dev):
-    dtype = getattr(t, "dtype", None)
-    return _ptr(t, what, dtype if dtype in _D_TYPES else _D_TYPES, shape, dev)
+def _done(name, result):
+    if type(result) is int:
+        raise DGError(name, result)
+    return result
 
 
-def _dims(t, what, n):
-    """Shape of a GPU tensor of n dimensions."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what} must be a torch.Tensor")
-    shape = t.shape
-    if len(shape) != n:
-        raise ValueError(f"{what} must have {n} dimensions, got shape {tuple(shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on the GPU")
-    return shape
-
-
-def _enqueue(dev, name, *args):
-    """Call a C entry point on the device's current stream (its last argument)."""
-    fn = getattr(_lib or load_library(), name)
-    stream = torch._C._cuda_getCurrentRawStream(dev.index)  # torch.cuda.current_stream without its object
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, stream)
-    if status != DG_OK:
-        raise DGError(name, status)
-
-
-@functools.lru_cache(maxsize=1024)
 def _workspace_bytes(name: str, *sizes) -> int:
     out = ctypes.c_int64()
     status = getattr(load_library(), name)(*sizes, ctypes.byref(out))
     if status != DG_OK:
         raise DGError(name, status)
     return out.value
-
-
-def _workspace(ws, nbytes, dev):
-    """The caller's workspace, or a new one from the caching allocator (safe to
-    drop once the call is enqueued), with its pointer and bytes."""
-    if ws is None:
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    elif ws.dtype is not torch.uint8 or ws.dim() != 1 or ws.device != dev or not ws.is_contiguous():
-        raise ValueError("workspace must be a contiguous one-dimensional uint8 tensor on the call's device")
-    return ws, ws.data_ptr(), ws.numel()
 
 
 def _score_mode(scoring):
@@ -431,99 +400,42 @@ def dg_moe_topk(logits, k, ids=None, weights=None, *, bias=None, n_group=1, topk
                 scoring="softmax", renormalize=True, scale=1.0):
     """Router: logits[T][E] (fp32 or bf16) -> (ids[T][k] int32, weights[T][k]
     fp32), best expert first, -1 and 0 where a row has fewer open experts."""
-    T, E = _dims(logits, "logits", 2)
-    dev, mode = logits.device, _score_mode(scoring)
-    name = "dg_moe_topk_bf16" if logits.dtype is torch.bfloat16 else "dg_moe_topk"
-    x = _ptr(logits, "logits", torch.bfloat16 if name.endswith("bf16") else torch.float32, (T, E), dev)
-    b = None if bias is None else _ptr(bias, "bias", torch.float32, (E,), dev)
-    if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    _enqueue(dev, name, x, b, _ptr(ids, "ids", torch.int32, (T, k), dev),
-             _ptr(weights, "weights", torch.float32, (T, k), dev), T, E, k, n_group, topk_group,
-             mode, int(renormalize), scale)
-    return ids, weights
+    return _done("dg_moe_topk", _ops().moe_topk(logits, k, ids, weights, bias, n_group, topk_group,
+                                                _score_mode(scoring), bool(renormalize), scale,
+                                                _raw_stream(logits)))
 
 
 def dg_moe_topk_backward(logits, ids, grad_weights, grad_logits=None, *, scoring="softmax",
                          renormalize=True, scale=1.0):
     """Gradient of ``dg_moe_topk``'s weights with respect to the logits (same
     dtype as the logits), the chosen experts held fixed."""
-    T, E = _dims(logits, "logits", 2)
-    k = _dims(ids, "ids", 2)[1]
-    dev, mode = logits.device, _score_mode(scoring)
-    bf16 = logits.dtype is torch.bfloat16
-    dtype = torch.bfloat16 if bf16 else torch.float32
-    x = _ptr(logits, "logits", dtype, (T, E), dev)
-    if grad_logits is None:
-        grad_logits = torch.empty((T, E), dtype=dtype, device=dev)
-    _enqueue(dev, "dg_moe_topk_backward_bf16" if bf16 else "dg_moe_topk_backward", x,
-             _ptr(ids, "ids", torch.int32, (T, k), dev),
-             _ptr(grad_weights, "grad_weights", torch.float32, (T, k), dev),
-             _ptr(grad_logits, "grad_logits", dtype, (T, E), dev), T, E, k, mode, int(renormalize), scale)
-    return grad_logits
-
-
-def _moe_mlp(name, e8, x, sx, ids, weights, w13, s13, w2, s2, y, workspace):
-    T, H = _dims(x, "x", 2)
-    k = _dims(ids, "ids", 2)[1]
-    E, _, I = _dims(w2, "w2", 3)
-    dev = x.device
-    if e8:
-        st, kh, ki = torch.uint8, e8m0_pitch(H // 128), e8m0_pitch(I // 128)
-    else:
-        st, kh, ki = torch.float32, H // 128, I // 128
-    if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    ptrs = (_codes_ptr(x, "x", (T, H), dev), _ptr(sx, "sx", st, (T, kh), dev),
-            _ptr(ids, "ids", torch.int32, (T, k), dev), _ptr(weights, "weights", torch.float32, (T, k), dev),
-            _codes_ptr(w13, "w13", (E, 2 * I, H), dev), _ptr(s13, "s13", st, (E, (2 * I + 127) // 128, kh), dev),
-            _codes_ptr(w2, "w2", (E, H, I), dev), _ptr(s2, "s2", st, (E, (H + 127) // 128, ki), dev),
-            _bf16_ptr(y, "y", (T, H), dev))
-    ws, at, n = _workspace(workspace, _workspace_bytes("dg_moe_mlp_fp8_workspace", T, k, E, H, I), dev)
-    _enqueue(dev, name, *ptrs, T, k, E, H, I, at, n)
-    return y
+    return _done("dg_moe_topk_backward", _ops().moe_topk_backward(
+        logits, ids, grad_weights, grad_logits, _score_mode(scoring), bool(renormalize), scale, _raw_stream(logits)))
 
 
 def dg_moe_mlp_fp8(x, sx, ids, weights, w13, s13, w2, s2, y=None, workspace=None):
     """Gated expert layer for up to 256 tokens: y[T][H] bf16 = sum over j of
     weights[t][j] * (quantize(silu(gate) * up) @ w2[e]^T), e = ids[t][j],
     (gate, up) = x @ w13[e]^T; ids outside [0, E) add nothing."""
-    return _moe_mlp("dg_moe_mlp_fp8", False, x, sx, ids, weights, w13, s13, w2, s2, y, workspace)
+    return _done("dg_moe_mlp_fp8", _ops().moe_mlp(False, x, sx, ids, weights, w13, s13, w2, s2, y, workspace,
+                                                  _raw_stream(x)))
 
 
 def dg_moe_mlp_fp8_e8m0(x, sx, ids, weights, w13, s13, w2, s2, y=None, workspace=None):
     """``dg_moe_mlp_fp8`` with E8M0 scale bytes (rows of ``e8m0_pitch`` bytes)."""
-    return _moe_mlp("dg_moe_mlp_fp8_e8m0", True, x, sx, ids, weights, w13, s13, w2, s2, y, workspace)
-
-
-def _gemm_lora(name, e8, A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling, workspace):
-    M, K = _dims(A, "A", 2)
-    N = _dims(B, "B", 2)[0]
-    L, R, _ = _dims(lora_a, "lora_a", 3)
-    dev, NB = A.device, (N + 127) // 128
-    st, kb = (torch.uint8, e8m0_pitch(K // 128)) if e8 else (torch.float32, K // 128)
-    ptrs = (_codes_ptr(A, "A", (M, K), dev), _ptr(sa, "sa", st, (M, kb), dev),
-            _codes_ptr(B, "B", (N, K), dev), _ptr(sb, "sb", st, (NB, kb), dev),
-            _bf16_ptr(D, "D", (M, N), dev), _ptr(x, "x", torch.bfloat16, (M, K), dev),
-            _ptr(lora_a, "lora_a", torch.bfloat16, (L, R, K), dev),
-            _ptr(lora_b, "lora_b", torch.bfloat16, (L, N, R), dev),
-            _ptr(ids, "ids", torch.int32, (M,), dev), _ptr(scaling, "scaling", torch.float32, (L,), dev))
-    ws, at, n = _workspace(workspace, _workspace_bytes("dg_fp8_gemm_nt_lora_workspace", M, N, K, L, R), dev)
-    _enqueue(dev, name, *ptrs, M, N, K, L, R, at, n)
-    return D
+    return _done("dg_moe_mlp_fp8_e8m0", _ops().moe_mlp(True, x, sx, ids, weights, w13, s13, w2, s2, y, workspace,
+                                                       _raw_stream(x)))
 
 
 def dg_fp8_gemm_nt_lora(A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling, workspace=None):
     """Dense form plus each row's low-rank adapter: D[m] = bf16(dense sum +
     scaling[a] * (x_m @ lora_a[a]^T) @ lora_b[a]^T), a = ids[m], nothing added
     where ids[m] is outside [0, L).  x is the bf16 activation behind A."""
-    return _gemm_lora("dg_fp8_gemm_nt_lora", False, A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling,
-                      workspace)
+    return _done("dg_fp8_gemm_nt_lora", _ops().gemm_lora(False, A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling,
+                                                         workspace, _raw_stream(A)))
 
 
 def dg_fp8_gemm_nt_lora_e8m0(A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling, workspace=None):
     """``dg_fp8_gemm_nt_lora`` with E8M0 scale bytes for A and B."""
-    return _gemm_lora("dg_fp8_gemm_nt_lora_e8m0", True, A, sa, B, sb, D, x, lora_a, lora_b, ids,
-                      scaling, workspace)
+    return _done("dg_fp8_gemm_nt_lora_e8m0", _ops().gemm_lora(True, A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling,
+                                                              workspace, _raw_stream(A)))

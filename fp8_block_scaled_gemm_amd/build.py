@@ -1,4 +1,5 @@
-"""Build the gfx950 HIP library libdgfp8.so in-tree with hipcc.
+"""Build the gfx950 HIP library libdgfp8.so in-tree with hipcc, and the
+compiled Python binding of its operators, _binding.so, with the host compiler.
 
 Usage: python -m fp8_block_scaled_gemm_amd.build   (or call build()).
 """
@@ -8,6 +9,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import time
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdgfp8.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["api.hip", "gemm.hip", "quantize.hip", "api_ops.hip", "router.hip", "moe.hip", "lora.hip"]
 ARCH = "gfx950"
 
@@ -78,7 +81,28 @@ def build(verbose: bool = False, jobs: int = 6) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile csrc/binding.cpp against torch and link it to libdgfp8.so, which
+    it finds beside itself."""
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    rocm = os.path.dirname(os.path.dirname(hipcc()))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{p}" for p in include_paths()), f"-I{os.path.join(rocm, 'include')}",
+           f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", os.path.join(CSRC, "binding.cpp"),
+           "-o", BINDING + ".tmp", *(f"-L{p}" for p in library_paths()), "-lc10", "-ltorch_cpu", "-ltorch_python",
+           f"-L{HERE}", "-l:libdgfp8.so", f"-L{os.path.join(rocm, 'lib')}", "-lamdhip64", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":
