@@ -38,13 +38,108 @@ struct ShrinkArgs {
     int64_t M, K;
     int L, R;
     int blocks, slots, parts;
+    bool grouped;
 };
 
+// The rows of block `b` when rows are grouped by adapter: adapters in order,
+// each one's rows in order, cut into blocks of kRows.  Every workgroup works
+// it out from the ids (a few microseconds, the same in all of them).  Returns
+// the adapter, or -1 past the last block; `row` is lane l's row, `n` their
+// number.  `lds`: L + kRows + 16 ints, free again on return.
+template <int kRows>
+__device__ __forceinline__ int find_group(const int32_t* __restrict__ ids, int M, int L, int b, int* lds, int& row,
+                                          int& n) {
+    int* const count = lds;
+    int* const list = lds + L;
+    int* const below = list + kRows;  // per wave
+    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 63, wave = tid >> 6;
+    for (int i = tid; i < L; i += threads) count[i] = 0;
+    __syncthreads();
+    // a thread's ids are consecutive, so ranks follow thread order
+    const int per = ((M + threads - 1) / threads + 3) & ~3, r0 = tid * per, r1 = min(r0 + per, M);
+    auto each = [&](auto f) __attribute__((always_inline)) {
+        for (int r = r0; r < r1; r += 4) {
+            int4 v = make_int4(-1, -1, -1, -1);
+            if (r + 4 <= M) {
+                v = *reinterpret_cast<const int4*>(ids + r);
+            } else {
+                v.x = ids[r];
+                if (r + 1 < M) v.y = ids[r + 1];
+                if (r + 2 < M) v.z = ids[r + 2];
+            }
+            f(r, v.x);
+            f(r + 1, v.y);
+            f(r + 2, v.z);
+            f(r + 3, v.w);
+        }
+    };
+    int same = -1, times = 0;  // runs of one id are counted with one addition
+    auto flush = [&]() __attribute__((always_inline)) {
+        if (times > 0) atomicAdd(&count[same], times);
+    };
+    each([&](int, int id) {
+        if (id == same) {
+            ++times;
+        } else if (id >= 0 && id < L) {
+            flush();
+            same = id;
+            times = 1;
+        }
+    });
+    flush();
+    __syncthreads();
+    int a = -1, first = 0, total = 0;
+    for (int a0 = 0, before = 0; a0 < L; a0 += 64) {
+        const int c = a0 + lane < L ? count[a0 + lane] : 0, blocks = (c + kRows - 1) / kRows;
+        int upto = blocks;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += o;
+        }
+        const uint64_t past = __ballot(before + upto > b);
+        if (past != 0) {
+            const int at = __builtin_ctzll(past);
+            a = a0 + at;
+            total = __builtin_amdgcn_readlane(c, at);
+            first = (b - before - __builtin_amdgcn_readlane(upto - blocks, at)) * kRows;
+            break;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    if (a < 0) return -1;
+    int mine = 0;
+    each([&](int, int id) { mine += id == a; });
+    int rank = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(rank, d, 64);
+        if (lane >= d) rank += o;
+    }
+    if (lane == 63) below[wave] = rank;
+    __syncthreads();
+    rank -= mine;
+    for (int w = 0; w < wave; ++w) rank += below[w];
+    each([&](int r, int id) {
+        if (id == a) {
+            if (rank >= first && rank < first + kRows) list[rank - first] = r;
+            ++rank;
+        }
+    });
+    __syncthreads();
+    n = __builtin_amdgcn_readfirstlane(min(kRows, total - first));
+    row = list[min(lane, n - 1)];
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(a);
+}
+
 // low[part][m][0..R) = x_m lora_a[a]^T over the part's share of K,
-// for the rows m that have an adapter.  A workgroup takes 16 RX rows, the
-// distinct adapters number `slot`, + slots, .. among them, and one part of K,
-// which its waves split; the waves' sums meet in LDS.  A product row belongs to one x row only, so rows of other adapters are
-// computed beside it and dropped.
+// for the rows m that have an adapter.  A workgroup takes 16 RX rows and one
+// part of K, which its waves split; the waves' sums meet in LDS.  With rows
+// grouped by adapter they are rows of one adapter.  Without, they are adjacent
+// rows, and the workgroup takes the distinct adapters number `slot`, + slots,
+// .. among them, one after the other; a product row belongs to one x row only,
+// so rows of other adapters are computed beside it and dropped.
 //
 // 64 columns of bf16 are 128 bytes, so a step of a wave looks like a K block of
 // the FP8 products and streams the same way: whole lines straight to a ring of
@@ -57,22 +152,36 @@ __device__ __forceinline__ void shrink_block(uint8_t* smem, const ShrinkArgs& g,
     float* const part = reinterpret_cast<float*>(smem);  // [W][16 RX][kPitch], once the ring is done
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4, R = g.R;
-    const int64_t m0 = (int64_t)block * 16 * RX, K = g.K;
-    const int rows = (int)std::min<int64_t>(16 * RX, g.M - m0);
-    int id = lane < rows ? g.ids[m0 + lane] : -1;  // lane l: row l
-    if (id < 0 || id >= g.L) id = -1;
-    // the first row of each distinct adapter
-    bool first = id >= 0;
+    const int64_t m0 = g.grouped ? 0 : (int64_t)block * 16 * RX, K = g.K;
+    int rows, id, row = lane;  // lane l: row m0 + row and its adapter
+    uint32_t leaders;          // the first row of each distinct adapter
+    if (g.grouped) {
+        const int a = find_group<16 * RX>(g.ids, (int)g.M, g.L, block, reinterpret_cast<int*>(smem), row, rows);
+        if (a < 0) return;
+        id = lane < rows ? a : -1;
+        leaders = 1;
+    } else {
+        rows = (int)std::min<int64_t>(16 * RX, g.M - m0);
+        id = lane < rows ? g.ids[m0 + lane] : -1;
+        if (id < 0 || id >= g.L) id = -1;
+        bool first = id >= 0;
 #pragma unroll
-    for (int d = 0; d < 16 * RX - 1; ++d)
-        if (d < lane && __builtin_amdgcn_readlane(id, d) == id) first = false;
-    uint32_t leaders = (uint32_t)__ballot(first);
+        for (int d = 0; d < 16 * RX - 1; ++d)
+            if (d < lane && __builtin_amdgcn_readlane(id, d) == id) first = false;
+        leaders = (uint32_t)__ballot(first);
+    }
     const int steps = (int)(K >> 6), shares = g.parts * W, share = z * W + wave;
     const int s0 = (int)((int64_t)share * steps / shares), s1 = (int)((int64_t)(share + 1) * steps / shares);
     // rows past the last one read as zero; K < 2^23, so R <= 128 rows of K bf16
-    // fit 31-bit offsets
+    // fit 31-bit offsets, and grouped rows are below 2^31 bytes of x
     const uint32_t pitch = (uint32_t)K * 2;
-    const v4u bufX = buffer_rsrc(g.x + m0 * K, (uint32_t)rows * pitch);
+    const v4u bufX = buffer_rsrc(g.x + m0 * K, (uint32_t)__builtin_amdgcn_readfirstlane(g.grouped ? (int)g.M : rows) * pitch);
+    uint32_t offX[2 * RX];
+#pragma unroll
+    for (int j = 0; j < 2 * RX; ++j) {
+        const int i = 8 * j + (lane >> 3), at = __shfl(row, i, 64);
+        offX[j] = i < rows ? (uint32_t)at * pitch + panel_chunk(lane) : kNoRow;
+    }
     const uint32_t off = (uint32_t)(lane >> 3) * pitch + panel_chunk(lane);
     uint8_t* const ring = smem + wave * D * kStage;
     const int lo = (lg ^ (lr & 7)) << 4, hi = lo ^ 64;
@@ -85,7 +194,7 @@ __device__ __forceinline__ void shrink_block(uint8_t* smem, const ShrinkArgs& g,
                 uint8_t* const to = ring + slot * kStage;
 #pragma unroll
                 for (int j = 0; j < 2 * RX; ++j)
-                    load_lds_16(bufX, s < s1 ? off + (uint32_t)(8 * j) * pitch + s * 128 : kNoRow, to + j * 1024);
+                    load_lds_16(bufX, s < s1 ? offX[j] + s * 128 : kNoRow, to + j * 1024);
 #pragma unroll
                 for (int j = 0; j < 2 * RT; ++j)
                     load_lds_16(bufA, s < s1 ? off + (uint32_t)(8 * j) * pitch + s * 128 : kNoRow,
@@ -137,8 +246,9 @@ __device__ __forceinline__ void shrink_block(uint8_t* smem, const ShrinkArgs& g,
             v4f sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < W; ++w) sum += *reinterpret_cast<const v4f*>(part + (w * 16 * RX + mi) * kPitch + r);
+            const int at = __shfl(row, mi, 64);
             if (__shfl(id, mi, 64) == a && r < R)  // R is a multiple of 8
-                *reinterpret_cast<v4f*>(g.low + ((int64_t)z * g.M + m0 + mi) * R + r) = sum;
+                *reinterpret_cast<v4f*>(g.low + ((int64_t)z * g.M + m0 + at) * R + r) = sum;
         }
         __syncthreads();  // the sums have been read: the ring is free again
     }
@@ -264,6 +374,7 @@ struct LoraPlan {
     bool few;
     int T, row_tiles, col_tiles, shares, per;  // few rows
     int blocks, slots, parts;                  // the shrink
+    bool grouped;
     int64_t low, sums, total;                  // workspace, in bytes from its start
     LoraPlan(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
         // Up to 512 rows.  Where every row has its own adapter the dense tiles
@@ -280,10 +391,16 @@ struct LoraPlan {
         per = (KB4 + want - 1) / want * 4;
         shares = (KB4 * 4 + per - 1) / per;
         const int rows = 16 * (few ? 1 : R <= 64 ? 2 : 1);
-        blocks = (int)((M + rows - 1) / rows);
+        // Beyond a few row blocks, rows are grouped by adapter, so that one is
+        // read once per block of its rows however they are mixed (1455 rows of
+        // 36 adapters in turn: see find_group; ungrouped the shrink takes
+        // 95 us).  One adapter, or more ids than a workgroup looks through at
+        // a time, are taken as they come.
+        grouped = M > 64 && M <= 8192 && L > 1 && L <= 1024 && M * K < (int64_t(1) << 30);
+        blocks = (int)((M + rows - 1) / rows + (grouped ? std::min(L, M) : 0));
         // alone a shrink's workgroup holds a CU's LDS, so none is launched that
         // may find no adapter
-        slots = few ? (int)std::min<int64_t>(L, 16) : 1;
+        slots = few && !grouped ? (int)std::min<int64_t>(L, 16) : 1;
         // few row blocks give few workgroups, so K is split over more of them
         parts = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxParts, (few ? 64 : 256) / blocks, K / 256}));
         auto up = [](int64_t v) { return (v + 255) & ~int64_t(255); };
@@ -325,7 +442,8 @@ static dg_status lora_rank(const LoraArgs& a, hipStream_t stream) {
     const LoraPlan at(a.M, a.N, a.K, a.L, a.R);
     uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
     float* const low = reinterpret_cast<float*>(ws + at.low);
-    const ShrinkArgs g{a.x, a.lora_a, a.ids, low, a.M, a.K, a.L, a.R, at.blocks, at.slots, at.parts};
+    const ShrinkArgs g{a.x, a.lora_a, a.ids, low, a.M, a.K, a.L, a.R, at.blocks, at.slots, at.parts,
+                       at.grouped};
     if (at.few) {
         float* const sums = reinterpret_cast<float*>(ws + at.sums);
         const FewArgs f{a.A, a.sa, a.B, a.sb, sums, (int)a.M, (int)a.N, (int)a.K, at.row_tiles, at.col_tiles,
