@@ -229,10 +229,16 @@ __device__ __forceinline__ void add_lora(v4f (&acc)[T::TM][T::TN], uint8_t* smem
     constexpr int kNone = kNoAdapter;
     const int lr = lane & 15, lg = lane >> 4, R = lora.R;
     // the lowest adapter above `after` among the tile's rows, the same for every wave
+    int some[T::BM / 64], own_id[T::TM];  // 64 ids of the tile each; those of the lane's rows
+#pragma unroll
+    for (int i = 0; i < T::BM / 64; ++i) some[i] = ids[64 * i + lane];
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) own_id[i] = ids[16 * (T::WAVES_M * i + wm) + lr];
     auto next_id = [&](int after) __attribute__((always_inline)) {
         int low = kNone;
-        for (int r = lane; r < T::BM; r += 64)
-            if (ids[r] > after) low = min(low, ids[r]);
+#pragma unroll
+        for (int i = 0; i < T::BM / 64; ++i)
+            if (some[i] > after) low = min(low, some[i]);
         return wave_min(low);
     };
     const int first = next_id(-1);
@@ -320,7 +326,7 @@ __device__ __forceinline__ void add_lora(v4f (&acc)[T::TM][T::TN], uint8_t* smem
                 for (int i = 0; i < T::TM; ++i) {
                     __builtin_amdgcn_sched_barrier(0);
                     const int row = 16 * (T::WAVES_M * i + wm) + lr;
-                    const bool own = ids[row] == cur;
+                    const bool own = own_id[i] == cur;
                     if (__ballot(own) == 0) continue;
                     const uint8_t* const pv = smem + row * 128;
                     v4f sum[kCols];
