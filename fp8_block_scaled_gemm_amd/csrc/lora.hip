@@ -78,9 +78,10 @@ __device__ __forceinline__ int find_group(const int32_t* __restrict__ ids, int M
         if (times > 0) atomicAdd(&count[same], times);
     };
     each([&](int, int id) {
+        if (id < 0 || id >= L) return;
         if (id == same) {
             ++times;
-        } else if (id >= 0 && id < L) {
+        } else {
             flush();
             same = id;
             times = 1;
@@ -381,8 +382,12 @@ struct LoraPlan {
         // take a load latency per adapter, one after the other, and the few-row
         // form spreads them over all CUs: 512 rows of 7168 x 2048, rank 32, 124
         // against 55 us (200 rows 71 / 31); with 8 packed prompts it is 35
-        // against 46 us (256 rows of 2112 x 7168: 36 / 26).
-        few = M <= 512 && N <= 65536 && K <= 65536;
+        // against 46 us (256 rows of 2112 x 7168: 36 / 26).  With many adapters
+        // the turn comes later, dense against few rows: 1455 rows of 424 x 6400,
+        // 36 adapters in turn, 47 / 30 us; 1024 of 7168 x 2048, 64 in turn, 122 /
+        // 72 us, 64 in runs 55 / 76 us.  With few of them dense tiles win there:
+        // 1388 rows of 816 x 3584, 13 mixed, 50 / 54 us.
+        few = (M <= 512 || (M <= 1536 && L >= 16)) && N <= 65536 && K <= 65536;
         const int KB4 = (int)((K / 128 + 3) / 4);
         T = M <= 16 ? 1 : M <= 32 ? 2 : 4;
         row_tiles = few ? (int)((M + 16 * T - 1) / (16 * T)) : 0;
@@ -392,10 +397,11 @@ struct LoraPlan {
         shares = (KB4 * 4 + per - 1) / per;
         const int rows = 16 * (few ? 1 : R <= 64 ? 2 : 1);
         // Beyond a few row blocks, rows are grouped by adapter, so that one is
-        // read once per block of its rows however they are mixed (1455 rows of
-        // 36 adapters in turn: see find_group; ungrouped the shrink takes
-        // 95 us).  One adapter, or more ids than a workgroup looks through at
-        // a time, are taken as they come.
+        // read once per block of its rows however they are mixed: the shrink of
+        // 1455 rows of K 6400, 36 adapters of rank 16 in turn, 93 -> 10.3 us;
+        // 4096 rows of K 2048, 8 packed prompts, rank 64, 12.4 -> 14.6 us.  One
+        // adapter, or more ids than a workgroup looks through in a few
+        // microseconds, are taken as they come.
         grouped = M > 64 && M <= 8192 && L > 1 && L <= 1024 && M * K < (int64_t(1) << 30);
         blocks = (int)((M + rows - 1) / rows + (grouped ? std::min(L, M) : 0));
         // alone a shrink's workgroup holds a CU's LDS, so none is launched that

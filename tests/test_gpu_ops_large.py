@@ -111,3 +111,26 @@ def test_lora_adapters_past_four_gib(M):
     dg.dg_fp8_gemm_nt_lora(d["A"], d["sa"], d["B"], d["sb"], D, d["x"], d["la"], d["lb"], ids, d["scaling"])
     want, tol = lora_ref(c, "fp32")
     assert (np.abs(host(D) - want) <= tol + ref.BF16 * (np.abs(want) + tol)).all()
+
+
+@pytest.mark.parametrize("kind", ["fp32", "e8m0"])
+@pytest.mark.parametrize("M,N,K,R,L,rows", [
+    (65, 136, 256, 128, 2, "mixed"), (70, 40, 128, 8, 1024, "each"), (70, 40, 128, 8, 1025, "each"),
+    (515, 72, 384, 24, 16, "mixed"), (1535, 136, 640, 72, 36, "each"), (1537, 136, 256, 40, 64, "each"),
+    (1601, 264, 128, 16, 900, "mixed"), (2050, 48, 256, 104, 16, "runs"), (1000, 64, 128, 16, 40, "none")])
+def test_lora_rows_grouped_by_adapter(M, N, K, R, L, rows, kind):
+    check_lora(lora_case(2 * M + N, M, N, K, R, L, kind, rows), kind)
+
+
+@pytest.mark.parametrize("M,L", [(8189, 1024), (8192, 5), (8193, 5)])
+def test_lora_the_most_rows_that_are_grouped(M, L):
+    check_lora(lora_case(M, M, 40, 128, 8, L, "fp32", "mixed"), "fp32")
+
+
+def test_lora_grouping_passes_over_rows_of_no_adapter():
+    c = lora_case(31, 700, 72, 256, 32, 6, "fp32", "each")
+    c["ids"][::2] = -1
+    c["ids"][1::10] = 6         # past the last adapter: none either
+    c["ids"][3::10] = 2 ** 31 - 1
+    c["ids"][5:40] = 5
+    check_lora(c, "fp32")
