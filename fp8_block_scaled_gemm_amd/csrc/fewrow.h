@@ -1,11 +1,8 @@
-// The inner product of a few activation rows with streamed FP8 weights, shared
-// by the decode-sized operators: one wave multiplies up to 16 R rows of A by
-// 16 C rows of B, K block by K block, straight from memory to registers.
-//
-// Every byte of B is used by one wave only, so staging it through LDS would
-// buy nothing; what counts is how many bytes are in flight.  A wave therefore
-// keeps a ring of K blocks loading ahead of the one it multiplies.  The rows
-// of A are few and shared by every wave of the launch: they come from cache.
+// The product of a few activation rows with streamed FP8 weights, shared by
+// the decode-sized operators: one wave multiplies up to 16 R rows of A by 16 C
+// rows of B, K block by K block.  Every byte of B is used once, so what counts
+// is how many bytes are in flight: rings in LDS, filled by direct loads, keep
+// K blocks loading ahead of the one that is multiplied (see panels, below).
 //
 // Fragment layout (v_mfma_f32_16x16x128_f8f6f4, B first): lane (lr, lg) holds
 // 16-byte chunks lg and lg + 4 of row lr's 128-byte K block, for A and for B,
@@ -24,24 +21,9 @@ struct Block {
     Scale sa[R], sb[C];
 };
 
-__device__ __forceinline__ void load_chunks(const uint8_t* p, v4u (&v)[2]) {
-    v[0] = *reinterpret_cast<const v4u*>(p);
-    v[1] = *reinterpret_cast<const v4u*>(p + 64);
-}
-
 // Rows that are not there read as zero through a bounds-checked buffer load,
 // which touches no memory for them: offset kNoRow is past every buffer here.
 constexpr uint32_t kNoRow = 0x80000000u;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)(uint32_t)bytes,
-                                             0x00020000);
-}
-
-__device__ __forceinline__ void load_chunks(__amdgpu_buffer_rsrc_t buf, uint32_t off, v4u (&v)[2]) {
-    v[0] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(buf, off, 0, 0));
-    v[1] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(buf, off + 64, 0, 0));
-}
 
 // The K block's codes of one fragment as bf16, which holds every e4m3 value,
 // in the four 32-wide steps of the bf16 matrix instruction.
@@ -252,7 +234,6 @@ __device__ __forceinline__ void panel_product(uint8_t* smem, const PanelLoads<C>
 // For few rows of A the same panel without a barrier per K block: A and the
 // scales come in chunks of four K blocks, double-buffered, one barrier per
 // chunk; in between every wave runs on its own through its private ring of B.
-// (A lone workgroup on a CU streams 35 GB/s with the barrier per K block.)
 // A wave waits for its loads in order, so waiting for the next chunk leaves at
 // most the four K blocks of B behind it in flight: deeper rings gain nothing.
 template <int R, int C, int D, int W>

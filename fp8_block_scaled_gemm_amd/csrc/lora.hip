@@ -134,13 +134,13 @@ __device__ __forceinline__ int find_group(const int32_t* __restrict__ ids, int M
     return __builtin_amdgcn_readfirstlane(a);
 }
 
-// low[part][m][0..R) = x_m lora_a[a]^T over the part's share of K,
-// for the rows m that have an adapter.  A workgroup takes 16 RX rows and one
-// part of K, which its waves split; the waves' sums meet in LDS.  With rows
-// grouped by adapter they are rows of one adapter.  Without, they are adjacent
-// rows, and the workgroup takes the distinct adapters number `slot`, + slots,
-// .. among them, one after the other; a product row belongs to one x row only,
-// so rows of other adapters are computed beside it and dropped.
+// low[part][m][0..R) = x_m lora_a[a]^T over the part's share of K, for the rows
+// m that have an adapter.  A workgroup takes 16 RX rows and one part of K,
+// which its waves split; the waves' sums meet in LDS.  With rows grouped by
+// adapter they are rows of one adapter.  Without, they are adjacent rows, and
+// the workgroup takes the distinct adapters number `slot`, + slots, .. among
+// them, one after the other; a product row belongs to one x row only, so rows
+// of other adapters are computed beside it and dropped.
 //
 // 64 columns of bf16 are 128 bytes, so a step of a wave looks like a K block of
 // the FP8 products and streams the same way: whole lines straight to a ring of
@@ -176,7 +176,8 @@ __device__ __forceinline__ void shrink_block(uint8_t* smem, const ShrinkArgs& g,
     // rows past the last one read as zero; K < 2^23, so R <= 128 rows of K bf16
     // fit 31-bit offsets, and grouped rows are below 2^31 bytes of x
     const uint32_t pitch = (uint32_t)K * 2;
-    const v4u bufX = buffer_rsrc(g.x + m0 * K, (uint32_t)__builtin_amdgcn_readfirstlane(g.grouped ? (int)g.M : rows) * pitch);
+    const int reach = __builtin_amdgcn_readfirstlane(g.grouped ? (int)g.M : rows);
+    const v4u bufX = buffer_rsrc(g.x + m0 * K, (uint32_t)reach * pitch);
     uint32_t offX[2 * RX];
 #pragma unroll
     for (int j = 0; j < 2 * RX; ++j) {
@@ -404,8 +405,8 @@ struct LoraPlan {
         // microseconds, are taken as they come.
         grouped = M > 64 && M <= 8192 && L > 1 && L <= 1024 && M * K < (int64_t(1) << 30);
         blocks = (int)((M + rows - 1) / rows + (grouped ? std::min(L, M) : 0));
-        // alone a shrink's workgroup holds a CU's LDS, so none is launched that
-        // may find no adapter
+        // ungrouped, few row blocks take their adapters side by side; many have
+        // the CUs' LDS to fill without workgroups that may find no adapter
         slots = few && !grouped ? (int)std::min<int64_t>(L, 16) : 1;
         // few row blocks give few workgroups, so K is split over more of them
         parts = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxParts, (few ? 64 : 256) / blocks, K / 256}));
@@ -448,8 +449,7 @@ static dg_status lora_rank(const LoraArgs& a, hipStream_t stream) {
     const LoraPlan at(a.M, a.N, a.K, a.L, a.R);
     uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
     float* const low = reinterpret_cast<float*>(ws + at.low);
-    const ShrinkArgs g{a.x, a.lora_a, a.ids, low, a.M, a.K, a.L, a.R, at.blocks, at.slots, at.parts,
-                       at.grouped};
+    const ShrinkArgs g{a.x, a.lora_a, a.ids, low, a.M, a.K, a.L, a.R, at.blocks, at.slots, at.parts, at.grouped};
     if (at.few) {
         float* const sums = reinterpret_cast<float*>(ws + at.sums);
         const FewArgs f{a.A, a.sa, a.B, a.sb, sums, (int)a.M, (int)a.N, (int)a.K, at.row_tiles, at.col_tiles,

@@ -210,8 +210,9 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_kernel(
     // apart by their upper halves (an open one's is never 0); only when those
     // tie do the lower halves decide, then the index.  The comparisons' lane
     // masks are scalars, so a round is about 20 vector instructions for 256
-    // experts; with 64-bit comparisons and selects per lane it was 55, and a
-    // batch of rows is bound by their issue.
+    // experts; with 64-bit comparisons and selects per lane it was 55.  (4096
+    // rows of 256, 8 chosen in 4 of 8 groups: 12.6 -> 12.2 us, as what a round
+    // waits for is the chain of its wave-wide maximum.)
     uint32_t hi[NV], lo[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
