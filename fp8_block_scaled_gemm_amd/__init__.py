@@ -1,11 +1,12 @@
 """MI355X (gfx950) FP8 block-scaled NT GEMM: thin Python binding.
 
 Every function here has the name of the C-ABI entry point it calls
-(include/dg_fp8.h, include/dg_ops.h) and only marshals arguments: it checks torch tensor
-dtypes, shapes and devices, passes raw device pointers and the current HIP
-stream (the operators of dg_ops.h through the compiled binding _binding.so), and raises ``DGError`` on a nonzero status.  All arithmetic runs in
-the HIP kernels of ``libdgfp8.so``; there is no CPU fallback, and importing a
-function fails loudly when the library has not been built
+(include/dg_fp8.h, include/dg_ops.h) and only marshals arguments: it checks
+torch tensor dtypes, shapes and devices, passes raw device pointers and the
+current HIP stream, and raises ``DGError`` on a nonzero status.  For the
+operators of dg_ops.h a compiled extension, ``_binding.so``, does so.  All
+arithmetic runs in the HIP kernels of ``libdgfp8.so``; there is no CPU
+fallback, and a call fails loudly when the library has not been built
 (``python -m fp8_block_scaled_gemm_amd.build``).
 
 Tensor conventions: e4m3 codes are ``torch.uint8`` (or

@@ -2,7 +2,9 @@
 // definition.
 //
 // Floor: the weights of the experts in use, 3 H I bytes each, read once;
-// everything else is small.
+// everything else is small.  Experts of 7168 x 2048: one token of 8 of them
+// 68 us in two launches (352 MB, 5.2 TB/s); 64 tokens, 16 experts, 144 us in
+// three (704 MB, 4.9 TB/s), where a large copy moves 5.04 TB/s.
 //
 // The routed pairs (token, choice) are kept in expert order ("routed rows"):
 // row start_e + i is the i-th pair of expert e.  A unit is one expert's rows;
@@ -170,7 +172,8 @@ __device__ __forceinline__ typename std::conditional<kE8, int, float>::type quan
 // activations.
 //
 // The sums go through the bf16 matrix instruction (see multiply_exact): the
-// FP8 one would move about one code in 600 of the quantized result.
+// FP8 one would move about one code in 600 of the quantized result.  Bound by
+// the weights (470 MB of 16 experts for 64 tokens: 90 us, 5.2 TB/s).
 //
 // With four waves a workgroup takes 64 columns and leaves them in fp32, for
 // the second product to quantize: for a few pairs there are too few 128
@@ -327,7 +330,10 @@ __global__ __launch_bounds__(64 * W * KS) void moe_gate_up_kernel(
 }
 
 // Second product of a batch, unweighted: out[row] = h w2^T in fp32, one 128
-// column block of one unit per workgroup.
+// column block of one unit per workgroup.  Bound by the weights (235 MB for 64
+// tokens, 16 experts: 47.5 us, 4.9 TB/s).  With the tokens' weighted sum in
+// the same launch, which has to gather a column block's experts in one
+// workgroup, it took 134 us.
 template <int R, int D, bool kE8>
 __global__ __launch_bounds__(64 * kPanelWaves) void moe_down_rows_kernel(
     const uint8_t* __restrict__ codes, const void* __restrict__ sh_v, const uint8_t* __restrict__ w2,
@@ -372,7 +378,9 @@ __global__ __launch_bounds__(64 * kPanelWaves) void moe_down_rows_kernel(
     }
 }
 
-// y_t = bf16(sum over j of weight * out[place of (t, j)]), four columns a thread.
+// y_t = bf16(sum over j of weight * out[place of (t, j)]), four columns a
+// thread; one rounding, after the whole sum.  Bound by latency: 15 MB from L2
+// and beyond for 64 tokens, 5.6 us.
 __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restrict__ out,
                                                           const int32_t* __restrict__ ids,
                                                           const int32_t* __restrict__ place,
@@ -401,6 +409,9 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
 // each streaming its share of the weights through a ring of its own in LDS,
 // with no barrier.  A wave adds its weighted products to a slice of its own
 // ([token][16] fp32); the slices are summed in wave order at the end.
+// One token, 8 experts of 7168 x 2048: 25.4 us for 117 MB (4.6 TB/s), of which
+// about 5 us pass before the first product (ids, hidden rows, first weights,
+// one load's latency after the other).
 template <bool kE8>
 __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(
     const float* __restrict__ hidden, const float* __restrict__ weights, const uint8_t* __restrict__ w2,
