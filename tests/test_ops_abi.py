@@ -142,3 +142,11 @@ def test_binding_refuses_host_tensors_and_bad_modes(lib):
         dg.dg_fp8_gemm_nt_lora(c, None, c, None, None, None, None, None, None, None)
     with pytest.raises(ValueError, match="scoring"):
         dg._score_mode("relu")
+
+
+@pytest.mark.parametrize("name", ["dg_fp8_gemm_nt_lora", "dg_fp8_gemm_nt_lora_e8m0"])
+def test_lora_refuses_a_grid_too_large_before_the_first_launch(lib, name):
+    M, N = 2 ** 31 - 1, 2 ** 22 - 8
+    n = ctypes.c_int64(-1)
+    assert lib.dg_fp8_gemm_nt_lora_workspace(M, N, 128, 2, 8, ctypes.byref(n)) == DG_ERR_SHAPE and n.value == -1
+    assert getattr(lib, name)(*[FAKE] * 10, M, N, 128, 2, 8, FAKE, 1 << 60, None) == DG_ERR_SHAPE
