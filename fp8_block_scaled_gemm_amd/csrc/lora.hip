@@ -383,16 +383,21 @@ struct LoraPlan {
     bool grouped;
     int64_t low, sums, total;                  // workspace, in bytes from its start
     LoraPlan(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
-        // Up to 512 rows.  Where every row has its own adapter the dense tiles
-        // take a load latency per adapter, one after the other, and the few-row
-        // form spreads them over all CUs: 512 rows of 7168 x 2048, rank 32, 124
-        // against 55 us (200 rows 71 / 31); with 8 packed prompts it is 35
-        // against 46 us (256 rows of 2112 x 7168: 36 / 26).  With many adapters
-        // the turn comes later, dense against few rows: 1455 rows of 424 x 6400,
-        // 36 adapters in turn, 47 / 30 us; 1024 of 7168 x 2048, 64 in turn, 122 /
-        // 72 us, 64 in runs 55 / 76 us.  With few of them dense tiles win there:
-        // 1388 rows of 816 x 3584, 13 mixed, 50 / 54 us.
-        few = (M <= 512 || (M <= 1536 && L >= 16)) && N <= 65536 && K <= 65536;
+        // The few-row form splits K over workgroups and reads each row's adapter
+        // by itself: its second launch costs about M N R.  The dense tiles walk K
+        // whole and take a step for each adapter among a tile's rows, at most L.
+        // So M N R / K decides, against a limit that grows with L.  Measured, few
+        // rows / dense tiles, us: 300 x 2048 x 1024, rank 64, 12 adapters in turn,
+        // 22.0 / 21.7; 512 x 7168 x 2048, rank 32, 15 mixed, 44.8 / 47.8, rank
+        // 128, 2 in runs, 91.3 / 41.8, rank 16, 64 in turn, 40.0 / 81.9;
+        // 700 x 1024, 4 mixed, K 4096, rank 16, 20.1 / 26.8, rank 64, 31.4 / 29.1;
+        // 64 x 7168 x 2048, rank 64, 8 in turn, 22.1 / 39.2, rank 128, 2 in runs,
+        // 23.4 / 18.5; 1024 x 7168 x 2048, rank 32, 64 in turn, 72 / 122, in
+        // runs 76 / 55; 1024 x 1024 x 7168, rank 32, 8 in runs, 33.4 / 37.5.  K
+        // below 1024 saves no more (64 x 7168 x 256, rank 32, 9.6 / 15.8).
+        const int64_t work = M * N * R / std::max<int64_t>(K, 1024);
+        few = (M <= 32 || (M <= 1536 && work <= 4096 * std::max<int64_t>(4, std::min<int64_t>(L, 32)))) &&
+              N <= 65536 && K <= 65536;
         const int KB4 = (int)((K / 128 + 3) / 4);
         T = M <= 16 ? 1 : M <= 32 ? 2 : 4;
         row_tiles = few ? (int)((M + 16 * T - 1) / (16 * T)) : 0;

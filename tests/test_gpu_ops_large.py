@@ -134,3 +134,61 @@ def test_lora_grouping_passes_over_rows_of_no_adapter():
     c["ids"][3::10] = 2 ** 31 - 1
     c["ids"][5:40] = 5
     check_lora(c, "fp32")
+
+
+@pytest.mark.parametrize("shape", ["256x256", "256x224", "256x192", "256x160", "128x256", "128x128",
+                                   "128x64", "128x32", "256x256t"])
+def test_lora_every_dense_tile_shape_past_the_few_row_form(shape, monkeypatch):
+    monkeypatch.setenv("DG_FP8_DENSE_TILE", shape)
+    kind = "e8m0" if shape.endswith("t") else "fp32"
+    check_lora(lora_case(3, 1540, 328, 256, 72, 5, kind, "mixed"), kind)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "e8m0"])
+@pytest.mark.parametrize("M,N,K,R,L,rows", [
+    (33, 4096, 128, 128, 1, "mixed"), (50, 3000, 128, 128, 4, "each"), (160, 1032, 256, 128, 3, "runs"),
+    (257, 1032, 384, 72, 2, "mixed"), (1540, 136, 256, 40, 64, "each"), (1552, 264, 640, 24, 6, "runs"),
+    (1537, 8, 128, 64, 600, "each"), (1600, 256, 1152, 16, 2, "none")])
+def test_lora_dense_tiles(M, N, K, R, L, rows, kind):
+    check_lora(lora_case(M + 3 * N, M, N, K, R, L, kind, rows), kind)
+
+
+def test_lora_infinities_stay_in_their_rows_past_the_few_row_form():
+    c = lora_case(11, 1540, 136, 256, 16, 4, "fp32", "each")
+    c["la"][1, 3, 7] = INF
+    c["lb"][2] = NAN
+    c["scaling"][3] = INF
+    c["x"][5, 9] = NAN
+    c["ids"][5] = -1
+    clean = np.isin(c["ids"], [-1, 0])
+    check_lora(c, "fp32", rows=clean)
+    got = host(run_lora(c, "fp32"))
+    assert np.isnan(got[c["ids"] == 2]).all()
+    assert not np.isfinite(got[c["ids"] == 3]).any()
+
+
+def test_lora_dense_tiles_graph_and_stream():
+    c = lora_case(23, 1540, 264, 256, 24, 3, "fp32", "runs")
+    d = {n: v.cuda() if isinstance(v, torch.Tensor) else to_dev(v) for n, v in c.items()}
+    D = torch.empty(1540, 264, dtype=torch.bfloat16, device="cuda")
+    call = lambda out: dg.dg_fp8_gemm_nt_lora(  # noqa: E731
+        d["A"], d["sa"], d["B"], d["sb"], out, d["x"], d["la"], d["lb"], d["ids"], d["scaling"])
+    eager = call(torch.empty_like(D))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(D)
+    for _ in range(3):
+        D.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(D, eager)
+        call(torch.empty_like(D))
+        torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = call(torch.empty_like(D))
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(other, eager)
