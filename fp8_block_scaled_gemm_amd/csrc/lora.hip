@@ -375,7 +375,7 @@ __global__ __launch_bounds__(256) void lora_combine_kernel(
             __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, v2bf));
 }
 
-// What a call launches, from its sizes.
+// What a call launches, from its sizes; M >= 1 (no rows: no launch, no plan).
 struct LoraPlan {
     bool few;
     int T, row_tiles, col_tiles, shares, per;  // few rows
@@ -427,7 +427,7 @@ struct LoraPlan {
 };
 
 int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
-    return LoraPlan(M, N, K, L, R).total;
+    return M == 0 ? 0 : LoraPlan(M, N, K, L, R).total;
 }
 
 template <int RT>

@@ -122,7 +122,7 @@ dg_status dg_fp8_gemm_nt_lora_e8m0(const uint8_t* A, const uint8_t* sa, const ui
                                    const int32_t* ids, const float* scaling, int64_t M, int64_t N,
                                    int64_t K, int64_t L, int64_t R, void* workspace,
                                    int64_t workspace_bytes, void* stream);
-/* Bytes of workspace for either call, into *bytes (host memory). */
+/* Bytes of workspace for either call, into *bytes (host memory); 0 for M = 0. */
 dg_status dg_fp8_gemm_nt_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R,
                                         int64_t* bytes);
 
