@@ -107,7 +107,8 @@ dg_status dg_moe_mlp_fp8_workspace(int64_t T, int64_t k, int64_t E, int64_t H, i
  *   D[m] = bf16( the dense form's sum + scaling[a] * (x_m lora_a[a]^T) lora_b[a]^T ),
  * a = ids[m], rounded once; the adapter's products are held in fp32 (the
  * rank-R vector enters its second product as a sum of two bf16 parts, 16 bits
- * of mantissa, when M is large).  Rows of one adapter need not be adjacent.
+ * of mantissa, when M is large).  Infinities and NaN give what the formula
+ * gives, in their own rows.  Rows of one adapter need not be adjacent.
  * Sizes: as dg_fp8_gemm_nt, N < 2^22, K < 2^23, 1 <= L <= 65536, R a multiple
  * of 8 up to 128. */
 dg_status dg_fp8_gemm_nt_lora(const uint8_t* A, const float* sa, const uint8_t* B, const float* sb,
