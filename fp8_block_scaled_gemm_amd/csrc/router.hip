@@ -329,8 +329,11 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_backward_kernel(
     int id = lane < k ? ids[t * k + lane] : -1;
     if (id < 0 || id >= E) id = -1;
     float g = id >= 0 ? grad_w[t * k + lane] * scale : 0.0f;
-    float xs = id >= 0 ? to_float(row[id]) : -INFINITY;
-    if (!(xs > -INFINITY)) xs = -INFINITY;
+    const float xs = id >= 0 ? to_float(row[id]) : -INFINITY;
+    if (!(xs > -INFINITY)) {  // a masked expert's weight is 0 whatever its gradient
+        id = -1;
+        g = 0.0f;
+    }
     float out[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) dense[w][lane + 64 * i] = 0.0f;
@@ -364,7 +367,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_backward_kernel(
     }
     rsum = wave_sum(rsum);
     rsum = rsum > 0.0f ? 1.0f / rsum : 0.0f;  // 0: no expert is open
-    const float p = id >= 0 && xs > -INFINITY ? exp_below<float>(xs, top) * rsum : 0.0f;
+    const float p = id >= 0 ? exp_below<float>(xs, top) * rsum : 0.0f;
     if (renormalize) {
         const float total = wave_sum(p) + (float)kTopkEps;
         const float mean = wave_sum(g * p) / total;
@@ -374,7 +377,8 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_backward_kernel(
     if (id >= 0) atomicAdd(&dense[w][id], g);
     wave_sync();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) out[i] = e[i] * rsum * (dense[w][lane * NV + i] - dot);
+    for (int i = 0; i < NV; ++i)  // masked: 0, also where `dot` is not finite
+        out[i] = x[i] > -INFINITY ? e[i] * rsum * (dense[w][lane * NV + i] - dot) : 0.0f;
     store_row<In, NV>(grad + t * E, E, lane, out);
 }
 

@@ -53,10 +53,11 @@ dg_status dg_moe_topk_bf16(const uint16_t* logits, const float* bias, int32_t* i
 /* Gradient of the router's weights with respect to its logits, the choice of
  * experts held fixed.
  *   ids          [T][k] int32 as the router returned them (entries outside
- *                [0, E) are skipped)
+ *                [0, E) and masked experts are skipped)
  *   grad_weights [T][k] fp32
  *   grad_logits  [T][E] fp32 or bf16 bits like the logits (output, every
- *                element written; masked experts get 0)
+ *                element written; masked experts get 0 whatever grad_weights
+ *                holds)
  * Same scoring, renormalize and scale as the forward call.  Sizes: T >= 0,
  * 1 <= E <= 1024, 1 <= k <= 64. */
 dg_status dg_moe_topk_backward(const float* logits, const int32_t* ids, const float* grad_weights,

@@ -56,3 +56,42 @@ def test_lora_nonfinite_values_follow_the_definition(M, R, kind):
 def test_lora_nonfinite_values_in_every_dense_tile(shape, monkeypatch):
     monkeypatch.setenv("DG_FP8_DENSE_TILE", shape)
     test_lora_nonfinite_values_follow_the_definition(1540, 72, "e8m0" if shape.endswith("t") else "fp32")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+def test_topk_backward_masked_experts_get_zero_beside_a_nonfinite_gradient(value, scoring, renorm, dtype):
+    rng = np.random.default_rng(3)
+    T, E, k = 6, 70, 3
+    x = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32))
+    x[:, 5:40] = -INF
+    x[:, 50] = NAN
+    x = x.to(dtype).cuda()
+    ids, _ = dg.dg_moe_topk(x, k)
+    gw = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+    clean = dg.dg_moe_topk_backward(x, ids, gw, scoring=scoring, renormalize=renorm)
+    gw[1, 1] = value
+    got = dg.dg_moe_topk_backward(x, ids, gw, scoring=scoring, renormalize=renorm)
+    masked = ~(x > -INF)
+    assert bool((got[masked] == 0).all())
+    assert not bool(torch.isfinite(got[1]).all())
+    others = torch.arange(T, device="cuda") != 1
+    assert torch.equal(got[others], clean[others])
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_topk_backward_passes_over_a_masked_expert_that_is_listed(scoring, renorm):
+    """Its weight is 0 whatever its gradient: as if the entry were -1."""
+    x = torch.randn(3, 20, device="cuda")
+    x[:, 4] = -INF
+    x[:, 9] = NAN
+    ids = torch.tensor([[1, 4, 9], [4, 2, 3], [9, 7, 4]], dtype=torch.int32, device="cuda")
+    gw = torch.randn(3, 3, device="cuda")
+    gw[0, 1], gw[1, 0], gw[2, 0] = INF, NAN, -INF
+    got = dg.dg_moe_topk_backward(x, ids, gw, scoring=scoring, renormalize=renorm)
+    skipped = torch.where((ids == 4) | (ids == 9), torch.full_like(ids, -1), ids)
+    assert torch.equal(got, dg.dg_moe_topk_backward(x, skipped, gw, scoring=scoring, renormalize=renorm))
+    assert bool(torch.isfinite(got).all())
