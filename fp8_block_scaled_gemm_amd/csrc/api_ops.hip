@@ -80,9 +80,9 @@ dg_status check_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     if (K <= 0 || K % 128 != 0 || K >= (int64_t(1) << 23)) return DG_ERR_SHAPE;
     if (M < 0 || M > 0x7fffffffLL || L < 1 || L > 65536) return DG_ERR_SHAPE;
     if (R < 8 || R > 128 || R % 8 != 0) return DG_ERR_SHAPE;
-    // refused here, as the dense launch would do so behind the adapters' own:
-    // its grid, in the smallest tiles
-    if (((M + 127) / 128) * ((N + 31) / 32) > 0x7fffffffLL - 8) return DG_ERR_SHAPE;
+    // refused here, as the dense launch would do so behind the adapters' own;
+    // below these sizes no grid is too large, in the smallest tiles
+    if (M > (1 << 24) || ((M + 127) / 128) * ((N + 31) / 32) > (1 << 23)) return dg::lora_limits(M, N, K, L, R);
     return DG_OK;
 }
 

@@ -752,12 +752,13 @@ static dg_status launch_tiled(const GemmArgs& a, hipStream_t stream) {
         grid = (m_blocks * n_blocks + kNumXcds - 1) / kNumXcds * kNumXcds;
     }
     if (grid == 0) return DG_OK;
-    if (grid > 0x7fffffff) return DG_ERR_SHAPE;
+    if (!grid_fits(grid, T::kThreads)) return DG_ERR_SHAPE;
     // per-lane 32-bit offsets: a tile's rows of K bytes, its A scales
     if ((int64_t)std::max(T::BM, T::BN) * a.K >= (int64_t(1) << 32)) return DG_ERR_SHAPE;
     // and a tile's rows of fp32 C
     if (kForm == Form::DenseAcc && (int64_t)T::BM * a.N * 4 >= (int64_t(1) << 32))
         return DG_ERR_SHAPE;
+    if (a.check_only) return DG_OK;
     TailOf<kForm> tail;
     if constexpr (kForm == Form::DenseLora) tail = a.lora;
     hipLaunchKernelGGL((gemm_kernel<T, kForm, kE8>), dim3((unsigned)grid), dim3(T::kThreads), 0, stream,

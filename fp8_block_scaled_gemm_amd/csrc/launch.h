@@ -12,6 +12,13 @@
 
 namespace dg {
 
+// Whether one dimension of a grid can be launched.  Its work-items are counted
+// in 32 bits; a larger one runs only what is left of it modulo 2^32, without an
+// error.
+inline bool grid_fits(int64_t blocks, int64_t threads) {
+    return blocks <= 0x7fffffff && blocks * threads <= 0xffffffffLL;
+}
+
 // Status of the launch just enqueued.
 inline dg_status launched() { return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP; }
 
@@ -40,6 +47,7 @@ struct GemmArgs {
     const float* C;       // DenseAcc: fp32 [rows][N] added before the bf16 rounding
     bool e8m0 = false;    // scales are E8M0 exponent bytes, SP = K/128 rounded up to 4
     LoraTail lora = {};   // DenseLora
+    bool check_only = false;  // only the checks of sizes; nothing is enqueued
 };
 
 dg_status launch_gemm(Form form, const GemmArgs& args, hipStream_t stream);

@@ -379,7 +379,8 @@ __global__ __launch_bounds__(256) void lora_combine_kernel(
 struct LoraPlan {
     bool few;
     int T, row_tiles, col_tiles, shares, per;  // few rows
-    int blocks, slots, parts;                  // the shrink
+    int64_t blocks;                            // the shrink
+    int slots, parts;
     bool grouped;
     int64_t low, sums, total;                  // workspace, in bytes from its start
     LoraPlan(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
@@ -413,7 +414,7 @@ struct LoraPlan {
         // adapter, or more ids than a workgroup looks through in a few
         // microseconds, are taken as they come.
         grouped = M > 64 && M <= 8192 && L > 1 && L <= 1024 && M * K < (int64_t(1) << 30);
-        blocks = (int)((M + rows - 1) / rows + (grouped ? std::min(L, M) : 0));
+        blocks = (M + rows - 1) / rows + (grouped ? std::min(L, M) : 0);
         // ungrouped, few row blocks take their adapters side by side; many have
         // the CUs' LDS to fill without workgroups that may find no adapter
         slots = few && !grouped ? (int)std::min<int64_t>(L, 16) : 1;
@@ -428,6 +429,18 @@ struct LoraPlan {
 
 int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     return M == 0 ? 0 : LoraPlan(M, N, K, L, R).total;
+}
+
+dg_status lora_limits(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+    const LoraPlan at(M, N, K, L, R);
+    if (at.few) return DG_OK;
+    static_assert(ShrinkShape<1, true>::W == 8 && ShrinkShape<2, true>::W == 4 && ShrinkShape<4, true>::W == 4 &&
+                      ShrinkShape<8, true>::W == 4,
+                  "the shrink's workgroups");
+    if (!grid_fits(at.blocks, R <= 16 ? 512 : 256)) return DG_ERR_SHAPE;
+    GemmArgs d{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, M, N, K, 1, nullptr};
+    d.check_only = true;
+    return launch_gemm(Form::DenseLora, d, nullptr);
 }
 
 template <int RT>
@@ -458,7 +471,7 @@ static dg_status lora_rank(const LoraArgs& a, hipStream_t stream) {
     const LoraPlan at(a.M, a.N, a.K, a.L, a.R);
     uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
     float* const low = reinterpret_cast<float*>(ws + at.low);
-    const ShrinkArgs g{a.x, a.lora_a, a.ids, low, a.M, a.K, a.L, a.R, at.blocks, at.slots, at.parts, at.grouped};
+    const ShrinkArgs g{a.x, a.lora_a, a.ids, low, a.M, a.K, a.L, a.R, (int)at.blocks, at.slots, at.parts, at.grouped};
     if (at.few) {
         float* const sums = reinterpret_cast<float*>(ws + at.sums);
         const FewArgs f{a.A, a.sa, a.B, a.sb, sums, (int)a.M, (int)a.N, (int)a.K, at.row_tiles, at.col_tiles,

@@ -62,6 +62,8 @@ struct LoraArgs {
     void* workspace;
 };
 int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
+// DG_ERR_SHAPE where a launch of these sizes is past what a grid holds.
+dg_status lora_limits(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
 dg_status launch_lora(const LoraArgs& a, bool e8m0, hipStream_t stream);
 
 }  // namespace dg

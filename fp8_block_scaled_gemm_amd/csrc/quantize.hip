@@ -166,7 +166,7 @@ static dg_status launch_per_token(const In* x, int64_t M, int64_t K, uint8_t* q,
                                    hipStream_t stream) {
     const int64_t total = M * (K >> 7);
     const int64_t grid = (total + 31) / 32;
-    if (grid > 0x7fffffff) return DG_ERR_SHAPE;
+    if (!grid_fits(grid, 256)) return DG_ERR_SHAPE;
     hipLaunchKernelGGL((quantize_per_token_kernel<In, kE8>), dim3((unsigned)grid), dim3(256), 0,
                        stream, x, total, K, q, s);
     return launched();
@@ -176,7 +176,7 @@ template <bool kE8>
 static dg_status launch_per_block(const float* x, int64_t N, int64_t K, uint8_t* q, void* s,
                                    hipStream_t stream) {
     const int64_t NB = (N + 127) / 128, KB = K >> 7;
-    if (NB > 65535 || KB > 0x7fffffff) return DG_ERR_SHAPE;
+    if (NB > 65535 || !grid_fits(KB, 256)) return DG_ERR_SHAPE;
     hipLaunchKernelGGL(quantize_per_block_kernel<kE8>, dim3((unsigned)KB, (unsigned)NB), dim3(256),
                        0, stream, x, N, K, q, s);
     return launched();

@@ -17,6 +17,7 @@
 #include "ops_launch.h"
 #include "wave_ops.h"
 
+#include <algorithm>
 #include <cmath>
 
 namespace dg {
@@ -384,6 +385,9 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void topk_backward_kernel(
 
 static int64_t row_blocks(int64_t T) { return (T + kRowsPerBlock - 1) / kRowsPerBlock; }
 
+// More rows than one grid holds (2^26 of 64 lanes) take several launches.
+constexpr int64_t kMaxRows = int64_t(1) << 25;
+
 template <class In, int NV>
 static dg_status topk_nv(const TopkArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((topk_kernel<In, NV>), dim3((unsigned)row_blocks(a.T)), dim3(64 * kRowsPerBlock),
@@ -403,7 +407,16 @@ static dg_status topk_in(const TopkArgs& a, hipStream_t stream) {
 
 dg_status launch_topk(const TopkArgs& a, bool bf16, hipStream_t stream) {
     if (row_blocks(a.T) > 0x7fffffff) return DG_ERR_SHAPE;
-    return bf16 ? topk_in<uint16_t>(a, stream) : topk_in<float>(a, stream);
+    for (int64_t t = 0; t < a.T; t += kMaxRows) {
+        TopkArgs part = a;
+        part.logits = static_cast<const char*>(a.logits) + t * a.E * (bf16 ? 2 : 4);
+        part.ids = a.ids + t * a.k;
+        part.weights = a.weights + t * a.k;
+        part.T = std::min(a.T - t, kMaxRows);
+        const dg_status s = bf16 ? topk_in<uint16_t>(part, stream) : topk_in<float>(part, stream);
+        if (s != DG_OK) return s;
+    }
+    return DG_OK;
 }
 
 template <class In, int NV>
@@ -426,7 +439,17 @@ static dg_status backward_in(const TopkBackwardArgs& a, hipStream_t stream) {
 
 dg_status launch_topk_backward(const TopkBackwardArgs& a, bool bf16, hipStream_t stream) {
     if (row_blocks(a.T) > 0x7fffffff) return DG_ERR_SHAPE;
-    return bf16 ? backward_in<uint16_t>(a, stream) : backward_in<float>(a, stream);
+    for (int64_t t = 0; t < a.T; t += kMaxRows) {
+        TopkBackwardArgs part = a;
+        part.logits = static_cast<const char*>(a.logits) + t * a.E * (bf16 ? 2 : 4);
+        part.ids = a.ids + t * a.k;
+        part.grad_weights = a.grad_weights + t * a.k;
+        part.grad_logits = static_cast<char*>(a.grad_logits) + t * a.E * (bf16 ? 2 : 4);
+        part.T = std::min(a.T - t, kMaxRows);
+        const dg_status s = bf16 ? backward_in<uint16_t>(part, stream) : backward_in<float>(part, stream);
+        if (s != DG_OK) return s;
+    }
+    return DG_OK;
 }
 
 }  // namespace dg

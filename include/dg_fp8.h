@@ -34,7 +34,8 @@
  *     contiguous form, rows past masked_m in the masked form) are never
  *     written.
  *   - Sizes that pass a call's rules but would need a grid of more than
- *     2^31 - 1 workgroups return DG_ERR_SHAPE, with nothing enqueued.
+ *     2^31 - 1 workgroups, or of more than 2^32 - 1 work-items, return
+ *     DG_ERR_SHAPE, with nothing enqueued.
  *   - A launch failure reported by the HIP runtime returns DG_ERR_HIP.
  *   - Calls on different streams may run concurrently; they share nothing.
  */

@@ -41,7 +41,7 @@ typedef enum { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 } dg_scoring;
  * by (sum of the row's k weights + 1e-20); then times `scale`.  Logits of
  * +infinity share a softmax row's whole probability equally.  Where fewer
  * than k experts are open the rest of the row is id -1, weight 0.
- * Sizes: T >= 0, 1 <= E <= 1024, 1 <= k <= 64, n_group >= 1 divides E and is
+ * Sizes: 0 <= T <= 2^33 - 4, 1 <= E <= 1024, 1 <= k <= 64, n_group >= 1 divides E and is
  * at most 64, 1 <= topk_group <= n_group, k <= topk_group * (E / n_group). */
 dg_status dg_moe_topk(const float* logits, const float* bias, int32_t* ids, float* weights,
                       int64_t T, int64_t E, int64_t k, int64_t n_group, int64_t topk_group,
@@ -58,7 +58,7 @@ dg_status dg_moe_topk_bf16(const uint16_t* logits, const float* bias, int32_t* i
  *   grad_logits  [T][E] fp32 or bf16 bits like the logits (output, every
  *                element written; masked experts get 0 whatever grad_weights
  *                holds)
- * Same scoring, renormalize and scale as the forward call.  Sizes: T >= 0,
+ * Same scoring, renormalize and scale as the forward call.  Sizes: 0 <= T <= 2^33 - 4,
  * 1 <= E <= 1024, 1 <= k <= 64. */
 dg_status dg_moe_topk_backward(const float* logits, const int32_t* ids, const float* grad_weights,
                                float* grad_logits, int64_t T, int64_t E, int64_t k, int scoring,
