@@ -568,12 +568,20 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(
         multiply(f, 16, acc);
         slot = slot == D - 1 ? 0 : slot + 1;
         if (++kb == KB || s + 1 == last) {
-            if (lr < count) {
-                // two rows may be one token: LDS adds, in lane order
-                const float w = row_w[start + lr];
-                float* const to = mine + row_t[start + lr] * 16 + 4 * lg;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) atomicAdd(to + q, w * acc[0][0][q]);
+            const v4f part = row_w[row] * acc[0][0];
+            const int t = row_t[row];
+            float* const to = mine + t * 16 + 4 * lg;
+            // rows of one token (an expert listed more than once) are adjacent;
+            // they are added one after the other, so that the order is fixed
+            const bool again = lr > 0 && lr < count && row_t[row - 1] == t;
+            if (__ballot(again) == 0) {
+                if (lr < count) *reinterpret_cast<v4f*>(to) += part;
+                wave_sync();
+            } else {
+                for (int r = 0; r < count; ++r) {
+                    if (lr == r) *reinterpret_cast<v4f*>(to) += part;
+                    wave_sync();
+                }
             }
             clear(acc);
             kb = 0;
