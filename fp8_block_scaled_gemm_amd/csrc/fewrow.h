@@ -49,14 +49,22 @@ __device__ __forceinline__ float scale_e8(float p, int ea, int eb) {
 // The same as `multiply` below through the bf16 matrix instruction: its sums
 // are exact to fp32 rounding, where the FP8 instruction aligns its 128
 // products to about 16 bits (measured: 1.5e-5 against 1e-8 relative error of
-// a K block).  For sums that are quantized next: an error there moves codes.
+// a K block).  The expert layer's products take it: the first one's sums are
+// quantized next, where an error moves codes, and the second one's are promised
+// in 32 bits (two products that cancel would take the bits of the others with
+// them).  It costs the widening, 16 conversions a fragment: the second product
+// 0 to 5% of a call (one token of 8 experts of 7168 x 2048 68.7 -> 69.5 us, 64
+// tokens of 16 148.7 -> 152.9, 251 tokens, one pair in eight here, 146.2 ->
+// 146.4, 256 tokens of 16 experts of 4096 x 1024 161 -> 169).
 template <int R, int C, bool kE8>
 __device__ __forceinline__ void multiply_exact(const Block<R, C, kE8>& k, int rows, v4f (&acc)[R][C]) {
     v8bf b[C][4];
 #pragma unroll
     for (int c = 0; c < C; ++c) widen(k.b[c], b[c]);
-    // two row tiles at a time: four chains of dependent products in flight
-    constexpr int kPair = R >= 2 ? 2 : 1;
+    // Two row tiles at a time with two column tiles: four chains of dependent
+    // products in flight.  With one column tile it is one, as most experts of a
+    // spread batch have few rows (the 251 tokens above: 164 us in pairs).
+    constexpr int kPair = R >= 2 && C >= 2 ? 2 : 1;
 #pragma unroll
     for (int r0 = 0; r0 < R; r0 += kPair) {
         if (r0 > 0 && 16 * r0 >= rows) break;
@@ -91,6 +99,7 @@ __device__ __forceinline__ void multiply_exact(const Block<R, C, kE8>& k, int ro
 }
 
 // acc += this block's scaled product; `rows` (uniform) of the 16 R rows count.
+// The FP8 instruction, as in the dense form, whose sum this is to be.
 template <int R, int C, bool kE8>
 __device__ __forceinline__ void multiply(const Block<R, C, kE8>& k, int rows, v4f (&acc)[R][C]) {
 #pragma unroll
@@ -248,7 +257,7 @@ struct FreePanel {
 
 // `trips` chunks are walked (all waves of the workgroup alike), of which the
 // first KB K blocks exist.
-template <int R, int C, int D, int W, bool kE8, bool kExact>
+template <int R, int C, int D, int W, bool kE8>
 __device__ __forceinline__ void free_panel_product(uint8_t* smem, const PanelLoads<C>& p, int KB, int trips,
                                                    int rows, int wave, int lane, v4f (&acc)[R][C]) {
     static_assert(R <= 2, "A chunks of more rows do not fit beside the ring");
@@ -313,10 +322,7 @@ __device__ __forceinline__ void free_panel_product(uint8_t* smem, const PanelLoa
                     else
                         f.sa[r] = s.sa[buf][(16 * r + lr) * kChunk + kk];
                 }
-                if constexpr (kExact)
-                    multiply_exact(f, rows, acc);
-                else
-                    multiply(f, rows, acc);
+                multiply_exact(f, rows, acc);
                 at = at == D - 1 ? 0 : at + 1;
             }
         }

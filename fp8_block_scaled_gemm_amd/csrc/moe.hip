@@ -255,7 +255,7 @@ __global__ __launch_bounds__(64 * W * KS) void moe_gate_up_kernel(
 #pragma unroll
                 for (int j = 0; j < 4; ++j) q.offB[j] += kb0 * 128;
             }
-            free_panel_product<R, 2, D, W, kE8, true>(
+            free_panel_product<R, 2, D, W, kE8>(
                 smem + share * sizeof(Panel), q, min(max(KB - kb0, 0), trips * kChunk), trips, rows, wave, lane, acc);
             if constexpr (KS > 1) {
                 // the shares' sums meet in LDS, in order; the ring is free
@@ -370,7 +370,7 @@ __global__ __launch_bounds__(64 * kPanelWaves) void moe_down_rows_kernel(
                  : wave == 1 && lane == 0 ? (uint32_t)blockIdx.x * SP * kSz
                                           : kNoRow;
         v4f acc[R][1];
-        panel_product<R, 1, D, kE8, false>(smem, p, KB, rows, wave, lane, acc);
+        panel_product<R, 1, D, kE8, true>(smem, p, KB, rows, wave, lane, acc);
 #pragma unroll
         for (int r = 0; r < R; ++r)
             if (16 * r + lr < rows)
@@ -565,7 +565,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(
         f.a[0][1] = *reinterpret_cast<const v4u*>(pa + (((lg + 4) ^ (row & 7)) << 4));
         f.sa[0] = scales[row * KB + kb];
         f.sb[0] = cols[j * KB + kb];
-        multiply(f, 16, acc);
+        multiply_exact(f, 16, acc);
         slot = slot == D - 1 ? 0 : slot + 1;
         if (++kb == KB || s + 1 == last) {
             const v4f part = row_w[row] * acc[0][0];

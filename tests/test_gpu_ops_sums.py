@@ -43,3 +43,34 @@ def test_moe_bits_repeat_with_experts_repeated_in_a_row(T, kind):
         assert torch.equal(call(*d), first)
     want, tol = ref.moe(*[c[n] for n in MOE_ORDER], kind)
     assert (np.abs(host(first) - want) <= tol + ref.BF16 * (np.abs(want) + tol) + 1e-37).all()
+
+
+@pytest.mark.parametrize("kind", ["fp32", "e8m0"])
+@pytest.mark.parametrize("T", [2, 20, 70, 200])
+def test_moe_second_product_is_held_in_32_bits(T, kind):
+    """Every hidden value is the same, so column n of the second product is its
+    code times w2's row n: two products of 448 * 448 that cancel, and one
+    2^-18 of their size, which fewer bits than fp32's would drop."""
+    H, I = 256, 256
+    c = moe_case(43, T, 1, 2, H, I, kind)
+    c["w13"][:] = 0
+    c["w13"][:, :, 0] = 0x38              # 1.0: gate and up are x's first value
+    c["x"][:, 0] = 0x40                   # 2.0
+    c["sx"][:] = 127 if kind == "e8m0" else 1.0
+    for s in ("s13", "s2"):
+        c[s][:] = 127 if kind == "e8m0" else 1.0
+    c["w2"][:] = 0
+    k = np.arange(H) % 120
+    c["w2"][:, np.arange(H), k] = 0x7E                # 448
+    c["w2"][:, np.arange(H), (k + 3) % 128] = 0xFE    # -448
+    c["w2"][:, np.arange(H), (k + 5) % 128] = 0x01    # 2^-9
+    c["weights"][:] = 1
+    h = 2.0 / (1 + np.exp(-2.0)) * 2
+    d = h / 448 if kind == "fp32" else 2.0 ** np.ceil(np.log2(h / 448))
+    q = float(ref.e4m3_round(np.float64(h / d)))
+    want = q * d * 2.0 ** -9
+    # three products and the sums between them: at most 4 roundings of the largest
+    tol = 4 * ref.FP32 * 2 * q * d * 448 + (ref.BF16 + 32 * ref.FP32) * want
+    got = host(run_moe(c, kind))
+    assert tol < 0.9 * want
+    assert (np.abs(got - want) <= tol).all(), (got.min(), got.max(), want)
