@@ -95,7 +95,7 @@ def build_binding(verbose: bool = False) -> str:
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-I{p}" for p in include_paths()), f"-I{os.path.join(rocm, 'include')}",
-           f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", os.path.join(CSRC, "binding.cpp"),
+           f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", f"-I{CSRC}", os.path.join(CSRC, "binding.cpp"),
            "-o", BINDING + ".tmp", *(f"-L{p}" for p in library_paths()), "-lc10", "-ltorch_cpu", "-ltorch_python",
            f"-L{HERE}", "-l:libdgfp8.so", f"-L{os.path.join(rocm, 'lib')}", "-lamdhip64", "-Wl,-rpath,$ORIGIN"]
     if verbose:

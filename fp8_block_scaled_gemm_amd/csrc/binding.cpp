@@ -11,7 +11,6 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
-#include <hip/hip_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <sstream>
@@ -19,6 +18,7 @@
 #include <string>
 
 #include "dg_ops.h"
+#include "on_device.h"
 
 namespace {
 
@@ -117,19 +117,6 @@ at::Tensor workspace(PyObject* o, int64_t bytes, at::Device dev) {
     return t;
 }
 
-// The library launches on the current device.
-struct OnDevice {
-    int before = -1;
-    explicit OnDevice(at::Device dev) {
-        int now = -1;
-        if (hipGetDevice(&now) == hipSuccess && now != dev.index() && hipSetDevice(dev.index()) == hipSuccess)
-            before = now;
-    }
-    ~OnDevice() {
-        if (before >= 0) (void)hipSetDevice(before);
-    }
-};
-
 void* stream_of(PyObject* o) { return reinterpret_cast<void*>((uintptr_t)integer(o)); }
 
 // A function's body behind Python's calling convention: argument count and
@@ -164,7 +151,7 @@ PyObject* moe_topk(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const at::Tensor weights = given_or_new(a[3], "weights", {T, k}, at::kFloat, dev);
         int32_t* const pi = (int32_t*)pointer(ids, "ids", {at::kInt}, {T, k}, dev);
         float* const pw = (float*)pointer(weights, "weights", {at::kFloat}, {T, k}, dev);
-        const OnDevice on(dev);
+        const OnDevice on(dev.index());
         const dg_status s =
             bf16 ? dg_moe_topk_bf16((const uint16_t*)px, (const float*)pb, pi, pw, T, E, k, integer(a[5]), integer(a[6]),
                                     (int)integer(a[7]), (int)integer(a[8]), number(a[9]), stream_of(a[10]))
@@ -191,7 +178,7 @@ PyObject* moe_topk_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const float* const pg = (const float*)pointer(a[2], "grad_weights", {at::kFloat}, {T, k}, dev);
         const at::Tensor out = given_or_new(a[3], "grad_logits", {T, E}, x.scalar_type(), dev);
         void* const po = pointer(out, "grad_logits", {x.scalar_type()}, {T, E}, dev);
-        const OnDevice on(dev);
+        const OnDevice on(dev.index());
         const dg_status s =
             bf16 ? dg_moe_topk_backward_bf16((const uint16_t*)px, pi, pg, (uint16_t*)po, T, E, k, (int)integer(a[4]),
                                              (int)integer(a[5]), number(a[6]), stream_of(a[7]))
@@ -229,7 +216,7 @@ PyObject* moe_mlp(PyObject*, PyObject* const* args, Py_ssize_t n) {
         dg_status s = dg_moe_mlp_fp8_workspace(T, k, E, H, I, &bytes);
         if (s != DG_OK) return PyLong_FromLong(s);
         const at::Tensor ws = workspace(a[10], bytes, dev);
-        const OnDevice on(dev);
+        const OnDevice on(dev.index());
         s = e8 ? dg_moe_mlp_fp8_e8m0(px, (const uint8_t*)psx, pi, pw, p13, (const uint8_t*)ps13, p2, (const uint8_t*)ps2,
                                      py, T, k, E, H, I, ws.data_ptr(), ws.numel(), stream_of(a[11]))
                : dg_moe_mlp_fp8(px, (const float*)psx, pi, pw, p13, (const float*)ps13, p2, (const float*)ps2, py, T, k,
@@ -264,7 +251,7 @@ PyObject* gemm_lora(PyObject*, PyObject* const* args, Py_ssize_t n) {
         dg_status s = dg_fp8_gemm_nt_lora_workspace(M, N, K, L, R, &bytes);
         if (s != DG_OK) return PyLong_FromLong(s);
         const at::Tensor ws = workspace(a[11], bytes, dev);
-        const OnDevice on(dev);
+        const OnDevice on(dev.index());
         s = e8 ? dg_fp8_gemm_nt_lora_e8m0(pA, (const uint8_t*)psa, pB, (const uint8_t*)psb, pD, px, pa, pb, pi, ps, M, N,
                                           K, L, R, ws.data_ptr(), ws.numel(), stream_of(a[12]))
                : dg_fp8_gemm_nt_lora(pA, (const float*)psa, pB, (const float*)psb, pD, px, pa, pb, pi, ps, M, N, K, L, R,

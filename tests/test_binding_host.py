@@ -1,0 +1,48 @@
+"""CPU tests of the compiled binding's own parts (csrc/binding.cpp)."""
+import os
+import subprocess
+
+from fp8_block_scaled_gemm_amd import build
+
+DEVICE_PROGRAM = r"""
+// on_device.h against a runtime whose calls fail on demand
+#include "on_device.h"
+#include <cstdio>
+#include <cstdlib>
+static int current = 1, get_fails = 0, set_fails = 0, sets = 0;
+extern "C" hipError_t hipGetDevice(int* d) { *d = current; return get_fails ? hipErrorNoDevice : hipSuccess; }
+extern "C" hipError_t hipSetDevice(int d) {
+    ++sets;
+    if (set_fails) return hipErrorInvalidDevice;
+    current = d;
+    return hipSuccess;
+}
+static bool refused(int index) {
+    try {
+        const OnDevice on(index);
+        if (current != index) std::exit(9);  // went on, on another GPU
+        return false;
+    } catch (const std::exception&) { return true; }
+}
+int main() {
+    if (refused(1) || sets != 0) return 1;               // current already
+    if (refused(3) || sets != 2 || current != 1) return 2;  // made current, and back
+    set_fails = 1;
+    if (!refused(3) || current != 1 || sets != 3) return 3;
+    if (refused(1)) return 4;
+    set_fails = 0, get_fails = 1;
+    if (!refused(1)) return 5;
+    std::puts("ok");
+    return 0;
+}
+"""
+
+
+def test_a_gpu_that_cannot_be_made_current_is_an_error(tmp_path):
+    src, exe = tmp_path / "on_device.cpp", tmp_path / "on_device"
+    src.write_text(DEVICE_PROGRAM)
+    rocm = os.path.dirname(os.path.dirname(build.hipcc()))
+    subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-D__HIP_PLATFORM_AMD__", f"-I{build.CSRC}",
+                    f"-I{rocm}/include", str(src), "-o", str(exe)], check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert got.returncode == 0 and got.stdout == "ok\n", got
