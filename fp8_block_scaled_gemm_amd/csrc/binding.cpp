@@ -117,6 +117,23 @@ at::Tensor workspace(PyObject* o, int64_t bytes, at::Device dev) {
     return t;
 }
 
+// The interpreter lock is given up while the library enqueues: a launch waits
+// where the stream's queue is full, and other threads (one of which may be what
+// the stream waits for) go on meanwhile.
+struct Unlocked {
+    PyThreadState* const state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    Unlocked& operator=(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+template <class F>
+dg_status unlocked(F call) {
+    const Unlocked on;
+    return call();
+}
+
 void* stream_of(PyObject* o) { return reinterpret_cast<void*>((uintptr_t)integer(o)); }
 
 // A function's body behind Python's calling convention: argument count and
@@ -151,12 +168,17 @@ PyObject* moe_topk(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const at::Tensor weights = given_or_new(a[3], "weights", {T, k}, at::kFloat, dev);
         int32_t* const pi = (int32_t*)pointer(ids, "ids", {at::kInt}, {T, k}, dev);
         float* const pw = (float*)pointer(weights, "weights", {at::kFloat}, {T, k}, dev);
+        const int64_t groups = integer(a[5]), kept = integer(a[6]);
+        const int scoring = (int)integer(a[7]), renormalize = (int)integer(a[8]);
+        const float scale = number(a[9]);
+        void* const stream = stream_of(a[10]);
         const OnDevice on(dev.index());
-        const dg_status s =
-            bf16 ? dg_moe_topk_bf16((const uint16_t*)px, (const float*)pb, pi, pw, T, E, k, integer(a[5]), integer(a[6]),
-                                    (int)integer(a[7]), (int)integer(a[8]), number(a[9]), stream_of(a[10]))
-                 : dg_moe_topk((const float*)px, (const float*)pb, pi, pw, T, E, k, integer(a[5]), integer(a[6]),
-                               (int)integer(a[7]), (int)integer(a[8]), number(a[9]), stream_of(a[10]));
+        const dg_status s = unlocked([&] {
+            return bf16 ? dg_moe_topk_bf16((const uint16_t*)px, (const float*)pb, pi, pw, T, E, k, groups, kept, scoring,
+                                           renormalize, scale, stream)
+                        : dg_moe_topk((const float*)px, (const float*)pb, pi, pw, T, E, k, groups, kept, scoring,
+                                      renormalize, scale, stream);
+        });
         if (s != DG_OK) return PyLong_FromLong(s);
         PyObject* const out = PyTuple_New(2);
         if (out == nullptr) return nullptr;
@@ -178,12 +200,16 @@ PyObject* moe_topk_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const float* const pg = (const float*)pointer(a[2], "grad_weights", {at::kFloat}, {T, k}, dev);
         const at::Tensor out = given_or_new(a[3], "grad_logits", {T, E}, x.scalar_type(), dev);
         void* const po = pointer(out, "grad_logits", {x.scalar_type()}, {T, E}, dev);
+        const int scoring = (int)integer(a[4]), renormalize = (int)integer(a[5]);
+        const float scale = number(a[6]);
+        void* const stream = stream_of(a[7]);
         const OnDevice on(dev.index());
-        const dg_status s =
-            bf16 ? dg_moe_topk_backward_bf16((const uint16_t*)px, pi, pg, (uint16_t*)po, T, E, k, (int)integer(a[4]),
-                                             (int)integer(a[5]), number(a[6]), stream_of(a[7]))
-                 : dg_moe_topk_backward((const float*)px, pi, pg, (float*)po, T, E, k, (int)integer(a[4]),
-                                        (int)integer(a[5]), number(a[6]), stream_of(a[7]));
+        const dg_status s = unlocked([&] {
+            return bf16 ? dg_moe_topk_backward_bf16((const uint16_t*)px, pi, pg, (uint16_t*)po, T, E, k, scoring,
+                                                    renormalize, scale, stream)
+                        : dg_moe_topk_backward((const float*)px, pi, pg, (float*)po, T, E, k, scoring, renormalize, scale,
+                                               stream);
+        });
         if (s != DG_OK) return PyLong_FromLong(s);
         return a[3] == Py_None ? THPVariable_Wrap(out) : Py_NewRef(a[3]);
     });
@@ -216,11 +242,15 @@ PyObject* moe_mlp(PyObject*, PyObject* const* args, Py_ssize_t n) {
         dg_status s = dg_moe_mlp_fp8_workspace(T, k, E, H, I, &bytes);
         if (s != DG_OK) return PyLong_FromLong(s);
         const at::Tensor ws = workspace(a[10], bytes, dev);
+        void* const pws = ws.data_ptr();
+        void* const stream = stream_of(a[11]);
         const OnDevice on(dev.index());
-        s = e8 ? dg_moe_mlp_fp8_e8m0(px, (const uint8_t*)psx, pi, pw, p13, (const uint8_t*)ps13, p2, (const uint8_t*)ps2,
-                                     py, T, k, E, H, I, ws.data_ptr(), ws.numel(), stream_of(a[11]))
-               : dg_moe_mlp_fp8(px, (const float*)psx, pi, pw, p13, (const float*)ps13, p2, (const float*)ps2, py, T, k,
-                                E, H, I, ws.data_ptr(), ws.numel(), stream_of(a[11]));
+        s = unlocked([&] {
+            return e8 ? dg_moe_mlp_fp8_e8m0(px, (const uint8_t*)psx, pi, pw, p13, (const uint8_t*)ps13, p2,
+                                            (const uint8_t*)ps2, py, T, k, E, H, I, pws, ws.numel(), stream)
+                      : dg_moe_mlp_fp8(px, (const float*)psx, pi, pw, p13, (const float*)ps13, p2, (const float*)ps2, py,
+                                       T, k, E, H, I, pws, ws.numel(), stream);
+        });
         if (s != DG_OK) return PyLong_FromLong(s);
         return a[9] == Py_None ? THPVariable_Wrap(y) : Py_NewRef(a[9]);
     });
@@ -251,11 +281,15 @@ PyObject* gemm_lora(PyObject*, PyObject* const* args, Py_ssize_t n) {
         dg_status s = dg_fp8_gemm_nt_lora_workspace(M, N, K, L, R, &bytes);
         if (s != DG_OK) return PyLong_FromLong(s);
         const at::Tensor ws = workspace(a[11], bytes, dev);
+        void* const pws = ws.data_ptr();
+        void* const stream = stream_of(a[12]);
         const OnDevice on(dev.index());
-        s = e8 ? dg_fp8_gemm_nt_lora_e8m0(pA, (const uint8_t*)psa, pB, (const uint8_t*)psb, pD, px, pa, pb, pi, ps, M, N,
-                                          K, L, R, ws.data_ptr(), ws.numel(), stream_of(a[12]))
-               : dg_fp8_gemm_nt_lora(pA, (const float*)psa, pB, (const float*)psb, pD, px, pa, pb, pi, ps, M, N, K, L, R,
-                                     ws.data_ptr(), ws.numel(), stream_of(a[12]));
+        s = unlocked([&] {
+            return e8 ? dg_fp8_gemm_nt_lora_e8m0(pA, (const uint8_t*)psa, pB, (const uint8_t*)psb, pD, px, pa, pb, pi, ps,
+                                                 M, N, K, L, R, pws, ws.numel(), stream)
+                      : dg_fp8_gemm_nt_lora(pA, (const float*)psa, pB, (const float*)psb, pD, px, pa, pb, pi, ps, M, N, K,
+                                            L, R, pws, ws.numel(), stream);
+        });
         if (s != DG_OK) return PyLong_FromLong(s);
         return Py_NewRef(a[5]);
     });
