@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -397,13 +398,58 @@ def _score_mode(scoring):
     return _SCORING[scoring]
 
 
+def _warn_no_grad(name, where, depth=3):
+    warnings.warn(f"{name} records no gradient {where}, though an argument requires one", stacklevel=depth)
+
+
+class _Topk(torch.autograd.Function):
+    """``dg_moe_topk`` with ``dg_moe_topk_backward`` as the gradient of its weights."""
+
+    @staticmethod
+    def forward(ctx, logits, k, bias, n_group, topk_group, mode, renormalize, scale):
+        ids, weights = _done("dg_moe_topk", _ops().moe_topk(logits, k, None, None, bias, n_group, topk_group, mode,
+                                                            renormalize, scale, _raw_stream(logits)))
+        ctx.save_for_backward(logits, ids)
+        ctx.how = mode, renormalize, scale
+        ctx.mark_non_differentiable(ids)
+        return ids, weights
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _, grad_weights):
+        logits, ids = ctx.saved_tensors
+        grad = _done("dg_moe_topk_backward", _ops().moe_topk_backward(
+            logits, ids, grad_weights.contiguous(), None, *ctx.how, _raw_stream(logits)))
+        return (grad,) + (None,) * 7
+
+
+class _NoGradient(torch.autograd.Function):
+    """The output of a call without a backward pass: going back through it is an error."""
+
+    @staticmethod
+    def forward(ctx, name, call, *tensors):
+        ctx.name = name
+        return call()
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise NotImplementedError(f"{ctx.name} has no gradient: call it under torch.no_grad() or on detached tensors")
+
+
 def dg_moe_topk(logits, k, ids=None, weights=None, *, bias=None, n_group=1, topk_group=1,
                 scoring="softmax", renormalize=True, scale=1.0):
     """Router: logits[T][E] (fp32 or bf16) -> (ids[T][k] int32, weights[T][k]
-    fp32), best expert first, -1 and 0 where a row has fewer open experts."""
-    return _done("dg_moe_topk", _ops().moe_topk(logits, k, ids, weights, bias, n_group, topk_group,
-                                                _score_mode(scoring), bool(renormalize), scale,
-                                                _raw_stream(logits)))
+    fp32), best expert first, -1 and 0 where a row has fewer open experts.
+    Where the logits require a gradient, the weights carry it (the bias, which
+    only ranks, has none); outputs that the caller gives carry none."""
+    mode, renormalize = _score_mode(scoring), bool(renormalize)
+    ops = _ops()
+    if ops.wants_grad(logits):
+        if ids is None and weights is None:
+            return _Topk.apply(logits, k, bias, n_group, topk_group, mode, renormalize, scale)
+        _warn_no_grad("dg_moe_topk", "in outputs that are given")
+    return _done("dg_moe_topk", ops.moe_topk(logits, k, ids, weights, bias, n_group, topk_group, mode, renormalize, scale,
+                                             _raw_stream(logits)))
 
 
 def dg_moe_topk_backward(logits, ids, grad_weights, grad_logits=None, *, scoring="softmax",
@@ -417,26 +463,50 @@ def dg_moe_topk_backward(logits, ids, grad_weights, grad_logits=None, *, scoring
 def dg_moe_mlp_fp8(x, sx, ids, weights, w13, s13, w2, s2, y=None, workspace=None):
     """Gated expert layer for up to 256 tokens: y[T][H] bf16 = sum over j of
     weights[t][j] * (quantize(silu(gate) * up) @ w2[e]^T), e = ids[t][j],
-    (gate, up) = x @ w13[e]^T; ids outside [0, E) add nothing."""
-    return _done("dg_moe_mlp_fp8", _ops().moe_mlp(False, x, sx, ids, weights, w13, s13, w2, s2, y, workspace,
-                                                  _raw_stream(x)))
+    (gate, up) = x @ w13[e]^T; ids outside [0, E) add nothing.  It has no
+    backward pass: going back through a new y is an error."""
+    ops = _ops()
+    if ops.wants_grad(weights, sx, s13, s2):
+        return _moe_mlp_no_grad("dg_moe_mlp_fp8", False, x, sx, ids, weights, w13, s13, w2, s2, y, workspace)
+    return _done("dg_moe_mlp_fp8", ops.moe_mlp(False, x, sx, ids, weights, w13, s13, w2, s2, y, workspace,
+                                               _raw_stream(x)))
 
 
 def dg_moe_mlp_fp8_e8m0(x, sx, ids, weights, w13, s13, w2, s2, y=None, workspace=None):
     """``dg_moe_mlp_fp8`` with E8M0 scale bytes (rows of ``e8m0_pitch`` bytes)."""
-    return _done("dg_moe_mlp_fp8_e8m0", _ops().moe_mlp(True, x, sx, ids, weights, w13, s13, w2, s2, y, workspace,
-                                                       _raw_stream(x)))
+    ops = _ops()
+    if ops.wants_grad(weights):
+        return _moe_mlp_no_grad("dg_moe_mlp_fp8_e8m0", True, x, sx, ids, weights, w13, s13, w2, s2, y, workspace)
+    return _done("dg_moe_mlp_fp8_e8m0", ops.moe_mlp(True, x, sx, ids, weights, w13, s13, w2, s2, y, workspace,
+                                                    _raw_stream(x)))
+
+
+def _moe_mlp_no_grad(name, e8m0, x, sx, ids, weights, w13, s13, w2, s2, y, workspace):
+    """The call where an argument requires a gradient: a new y refuses to pass one back."""
+    def call():
+        return _done(name, _ops().moe_mlp(e8m0, x, sx, ids, weights, w13, s13, w2, s2, y, workspace, _raw_stream(x)))
+    if y is None:
+        return _NoGradient.apply(name, call, weights, sx, s13, s2)
+    _warn_no_grad(name, "in a y that is given", 4)
+    return call()
 
 
 def dg_fp8_gemm_nt_lora(A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling, workspace=None):
     """Dense form plus each row's low-rank adapter: D[m] = bf16(dense sum +
     scaling[a] * (x_m @ lora_a[a]^T) @ lora_b[a]^T), a = ids[m], nothing added
-    where ids[m] is outside [0, L).  x is the bf16 activation behind A."""
-    return _done("dg_fp8_gemm_nt_lora", _ops().gemm_lora(False, A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling,
-                                                         workspace, _raw_stream(A)))
+    where ids[m] is outside [0, L).  x is the bf16 activation behind A.  No
+    gradient is recorded in D."""
+    ops = _ops()
+    if ops.wants_grad(x, lora_a, lora_b, scaling, sa, sb):
+        _warn_no_grad("dg_fp8_gemm_nt_lora", "in D")
+    return _done("dg_fp8_gemm_nt_lora", ops.gemm_lora(False, A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling,
+                                                      workspace, _raw_stream(A)))
 
 
 def dg_fp8_gemm_nt_lora_e8m0(A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling, workspace=None):
     """``dg_fp8_gemm_nt_lora`` with E8M0 scale bytes for A and B."""
-    return _done("dg_fp8_gemm_nt_lora_e8m0", _ops().gemm_lora(True, A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling,
-                                                              workspace, _raw_stream(A)))
+    ops = _ops()
+    if ops.wants_grad(x, lora_a, lora_b, scaling):
+        _warn_no_grad("dg_fp8_gemm_nt_lora_e8m0", "in D")
+    return _done("dg_fp8_gemm_nt_lora_e8m0", ops.gemm_lora(True, A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling,
+                                                           workspace, _raw_stream(A)))

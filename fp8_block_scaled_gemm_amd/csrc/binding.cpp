@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <sstream>
@@ -295,8 +296,17 @@ PyObject* gemm_lora(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// Whether gradients are recorded and any of the arguments is a tensor that requires one.
+PyObject* wants_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (c10::GradMode::is_enabled())
+        for (Py_ssize_t i = 0; i < n; ++i)
+            if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad()) Py_RETURN_TRUE;
+    Py_RETURN_FALSE;
+}
+
 #define DG_METHOD(name) {#name, (PyCFunction)(void (*)())name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {DG_METHOD(moe_topk), DG_METHOD(moe_topk_backward), DG_METHOD(moe_mlp), DG_METHOD(gemm_lora),
+                         DG_METHOD(wants_grad),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
