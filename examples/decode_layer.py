@@ -42,8 +42,11 @@ class DecodeLayer:
         self.lora_a = (randn(adapters, rank, hidden) * hidden ** -0.5).to(torch.bfloat16)
         self.lora_b = (randn(adapters, hidden, rank) * 0.1).to(torch.bfloat16)
         self.scaling = torch.full((adapters,), 2.0, device=device)
-        # the projection's output, and its workspace, kept for every step
+        # the projection's output and the calls' workspaces, kept for every step
         self.mid = torch.empty(tokens, hidden, dtype=torch.bfloat16, device=device)
+        scratch = lambda n: torch.empty(n, dtype=torch.uint8, device=device)  # noqa: E731
+        self.lora_ws = scratch(dg.dg_fp8_gemm_nt_lora_workspace(tokens, hidden, hidden, adapters, rank))
+        self.moe_ws = scratch(dg.dg_moe_mlp_fp8_workspace(tokens, topk, experts, hidden, inner))
 
     def logits(self, x):
         return torch.mm(x.float(), self.router.t())
@@ -52,11 +55,12 @@ class DecodeLayer:
         """x [T][H] bf16, adapter [T] int32 (-1: none) -> [T][H] bf16, expert ids."""
         q, s = dg.dg_quantize_fp8_per_token_bf16(x)
         dg.dg_fp8_gemm_nt_lora(q, s, self.proj, self.proj_s, self.mid, x, self.lora_a, self.lora_b, adapter,
-                               self.scaling)
+                               self.scaling, self.lora_ws)
         h = x + self.mid
         ids, weights = dg.dg_moe_topk(self.logits(h), self.topk, bias=self.bias, scoring="sigmoid")
         q, s = dg.dg_quantize_fp8_per_token_bf16(h)
-        return h + dg.dg_moe_mlp_fp8(q, s, ids, weights, self.w13, self.s13, self.w2, self.s2), ids
+        return h + dg.dg_moe_mlp_fp8(q, s, ids, weights, self.w13, self.s13, self.w2, self.s2,
+                                     workspace=self.moe_ws), ids
 
 
 def train_router(layer, x, steps=20, rate=1.0):

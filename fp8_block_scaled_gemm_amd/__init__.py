@@ -33,6 +33,7 @@ __all__ = [
     "dg_status_string",
     "dg_moe_topk", "dg_moe_topk_backward", "dg_moe_mlp_fp8", "dg_moe_mlp_fp8_e8m0",
     "dg_fp8_gemm_nt_lora", "dg_fp8_gemm_nt_lora_e8m0",
+    "dg_moe_mlp_fp8_workspace", "dg_fp8_gemm_nt_lora_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -390,6 +391,18 @@ def _workspace_bytes(name: str, *sizes) -> int:
     if status != DG_OK:
         raise DGError(name, status)
     return out.value
+
+
+def dg_moe_mlp_fp8_workspace(T, k, E, H, I) -> int:
+    """Bytes of a uint8 tensor to pass as ``workspace`` to either form of
+    ``dg_moe_mlp_fp8`` with T tokens, k choices, E experts of H x I."""
+    return _workspace_bytes("dg_moe_mlp_fp8_workspace", T, k, E, H, I)
+
+
+def dg_fp8_gemm_nt_lora_workspace(M, N, K, L, R) -> int:
+    """Bytes of a uint8 tensor to pass as ``workspace`` to either form of
+    ``dg_fp8_gemm_nt_lora`` with M rows, N x K weights, L adapters of rank R."""
+    return _workspace_bytes("dg_fp8_gemm_nt_lora_workspace", M, N, K, L, R)
 
 
 def _score_mode(scoring):

@@ -46,3 +46,23 @@ def test_a_gpu_that_cannot_be_made_current_is_an_error(tmp_path):
                     f"-I{rocm}/include", str(src), "-o", str(exe)], check=True)
     got = subprocess.run([str(exe)], capture_output=True, text=True)
     assert got.returncode == 0 and got.stdout == "ok\n", got
+
+
+def test_workspaces_have_a_size_that_a_caller_can_ask_for():
+    import ctypes
+
+    import fp8_block_scaled_gemm_amd as dg
+
+    lib, n = dg.load_library(), ctypes.c_int64()
+    for name, sizes, bad in (("dg_moe_mlp_fp8_workspace", (4, 2, 8, 256, 128), (4, 2, 8, 200, 128)),
+                             ("dg_fp8_gemm_nt_lora_workspace", (64, 264, 512, 4, 16), (64, 264, 512, 4, 12))):
+        assert name in dg.__all__
+        assert getattr(lib, name)(*sizes, ctypes.byref(n)) == 0
+        assert getattr(dg, name)(*sizes) == n.value > 0
+        try:
+            getattr(dg, name)(*bad)
+        except dg.DGError as e:
+            assert name in str(e)
+        else:
+            raise AssertionError(name)
+    assert dg.dg_fp8_gemm_nt_lora_workspace(0, 264, 512, 4, 16) == 0
