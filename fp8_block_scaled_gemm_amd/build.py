@@ -1,7 +1,8 @@
 """Build the gfx950 HIP library libdgfp8.so in-tree with hipcc, and the
 compiled Python binding of its operators, _binding.so, with the host compiler.
 
-Usage: python -m fp8_block_scaled_gemm_amd.build   (or call build()).
+Usage: python -m fp8_block_scaled_gemm_amd.build   (or call build());
+with --library only the library, which needs neither torch nor a host compiler.
 """
 from __future__ import annotations
 
@@ -40,8 +41,30 @@ def compile_flags() -> list[str]:
 
 
 def build(verbose: bool = False, jobs: int = 6) -> str:
-    """Compile every source to an object in parallel, then link the shared
-    library; always recompiles."""
+    """Compile and link the library and the binding, always anew; neither is
+    replaced before both are built."""
+    lib = _link_library(verbose, jobs)
+    binding = _link_binding(lib, verbose)
+    os.replace(lib, LIB)
+    os.replace(binding, BINDING)
+    return LIB
+
+
+def build_library(verbose: bool = False, jobs: int = 6) -> str:
+    """The library alone, for callers of the C ABI."""
+    os.replace(_link_library(verbose, jobs), LIB)
+    return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """The binding alone, for the library that is there."""
+    os.replace(_link_binding(LIB, verbose), BINDING)
+    return BINDING
+
+
+def _link_library(verbose: bool, jobs: int) -> str:
+    """Compile every source to an object in parallel and link them; the path
+    of the result, which is not in its place yet."""
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     cc = hipcc()
@@ -76,18 +99,16 @@ def build(verbose: bool = False, jobs: int = 6) -> str:
     if failed:
         raise RuntimeError(f"hipcc failed for {failed}")
     tmp = LIB + ".tmp"
-    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
+    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", f"-Wl,-soname,{os.path.basename(LIB)}", *objs, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
-    build_binding(verbose)
-    return LIB
+    return tmp
 
 
-def build_binding(verbose: bool = False) -> str:
-    """Compile csrc/binding.cpp against torch and link it to libdgfp8.so, which
-    it finds beside itself."""
+def _link_binding(lib: str, verbose: bool) -> str:
+    """Compile csrc/binding.cpp against torch and link it to the library,
+    which it finds beside itself; the path of the result."""
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
 
@@ -97,13 +118,12 @@ def build_binding(verbose: bool = False) -> str:
            *(f"-I{p}" for p in include_paths()), f"-I{os.path.join(rocm, 'include')}",
            f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", f"-I{CSRC}", os.path.join(CSRC, "binding.cpp"),
            "-o", BINDING + ".tmp", *(f"-L{p}" for p in library_paths()), "-lc10", "-ltorch_cpu", "-ltorch_python",
-           f"-L{HERE}", "-l:libdgfp8.so", f"-L{os.path.join(rocm, 'lib')}", "-lamdhip64", "-Wl,-rpath,$ORIGIN"]
+           lib, f"-L{os.path.join(rocm, 'lib')}", "-lamdhip64", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(BINDING + ".tmp", BINDING)
-    return BINDING
+    return BINDING + ".tmp"
 
 
 if __name__ == "__main__":
-    print(build(verbose=True))
+    print(build_library(verbose=True) if "--library" in sys.argv[1:] else build(verbose=True))

@@ -66,3 +66,23 @@ def test_workspaces_have_a_size_that_a_caller_can_ask_for():
         else:
             raise AssertionError(name)
     assert dg.dg_fp8_gemm_nt_lora_workspace(0, 264, 512, 4, 16) == 0
+
+
+def test_a_binding_that_does_not_compile_leaves_the_library_in_its_place(tmp_path, monkeypatch):
+    lib, binding = tmp_path / "libdgfp8.so", tmp_path / "_binding.so"
+    for f in (lib, binding):
+        f.write_bytes(b"before")
+    monkeypatch.setattr(build, "HERE", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(lib))
+    monkeypatch.setattr(build, "BINDING", str(binding))
+    monkeypatch.setattr(build, "SOURCES", ["quantize.hip"])
+    monkeypatch.setenv("CXX", "false")
+    try:
+        build.build()
+    except subprocess.CalledProcessError:
+        pass
+    else:
+        raise AssertionError("a host compiler that fails went unnoticed")
+    assert lib.read_bytes() == b"before" and binding.read_bytes() == b"before"
+    assert build.build_library() == str(lib)  # which needs no host compiler
+    assert lib.read_bytes()[:4] == b"\x7fELF" and binding.read_bytes() == b"before"
