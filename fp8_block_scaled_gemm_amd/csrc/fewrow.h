@@ -99,7 +99,10 @@ __device__ __forceinline__ void multiply_exact(const Block<R, C, kE8>& k, int ro
 }
 
 // acc += this block's scaled product; `rows` (uniform) of the 16 R rows count.
-// The FP8 instruction, as in the dense form, whose sum this is to be.
+// The FP8 instruction, as in the dense form, whose sum this is to be: a row takes
+// the same sum in either form, to about 16 bits of a K block's largest product.
+// (multiply_exact here: 64 rows of 2112 x 7168 with adapters 17.6 -> 18.7 us,
+// 1024 rows of 7168 x 2048 69 -> 85; the dense tiles would halve their rate.)
 template <int R, int C, bool kE8>
 __device__ __forceinline__ void multiply(const Block<R, C, kE8>& k, int rows, v4f (&acc)[R][C]) {
 #pragma unroll

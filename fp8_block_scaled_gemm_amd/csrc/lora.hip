@@ -146,8 +146,9 @@ __device__ __forceinline__ int find_group(const int32_t* __restrict__ ids, int M
 // the FP8 products and streams the same way: whole lines straight to a ring of
 // the wave's own in LDS (fragment-shaped loads to registers are bound by the
 // cache's tag rate, 16 bytes per clock).  4096 rows of K 2048, 8 packed
-// prompts, rank 64: 13.3 us; 16.8 MB of x at 1.3 TB/s, so latency bounds it:
-// a workgroup's search for its rows and one pass over K.
+// prompts, rank 64: 13.1 us; 16.8 MB of x at 1.3 TB/s.  Bound by a workgroup's
+// chain of its search for its rows and one pass over K, with 136 workgroups at
+// most one to a CU: 120 CUs have none.
 template <int RT, bool kMany>
 __device__ __forceinline__ void shrink_block(uint8_t* smem, const ShrinkArgs& g, int block, int slot0, int z) {
     using Shape = ShrinkShape<RT, kMany>;
@@ -269,7 +270,7 @@ __global__ __launch_bounds__((64 * ShrinkShape<RT, true>::W)) void lora_shrink_k
 // order 64 rows of 64 adapters take 17.9 us instead of 15.0).  One burst of
 // loads has about 2 us of latency, so what counts is that all of B is asked
 // for at once: K is split until every CU has a workgroup.  64 rows of
-// 2112 x 7168, 64 adapters of rank 32: 12.4 us for 47 MB, and 6.3 us for the
+// 2112 x 7168, 64 adapters of rank 32: 13 us for 47 MB, and 5.4 us for the
 // combine (15.6 MB); the two products alone would take a copy's rate 11 us.
 constexpr int kFewRing = 3;
 

@@ -3,8 +3,8 @@
 //
 // Floor: the weights of the experts in use, 3 H I bytes each, read once;
 // everything else is small.  Experts of 7168 x 2048: one token of 8 of them
-// 68 us in two launches (352 MB, 5.2 TB/s); 64 tokens, 16 experts, 144 us in
-// three (704 MB, 4.9 TB/s), where a large copy moves 5.04 TB/s.
+// 69 us in two launches (352 MB, 5.1 TB/s); 64 tokens, 16 experts, 148 us in
+// three (704 MB, 4.8 TB/s), where a large copy moves 5.04 TB/s.
 //
 // The routed pairs (token, choice) are kept in expert order ("routed rows"):
 // row start_e + i is the i-th pair of expert e.  A unit is one expert's rows;
@@ -173,7 +173,7 @@ __device__ __forceinline__ typename std::conditional<kE8, int, float>::type quan
 //
 // The sums go through the bf16 matrix instruction (see multiply_exact): the
 // FP8 one would move about one code in 600 of the quantized result.  Bound by
-// the weights (470 MB of 16 experts for 64 tokens: 90 us, 5.2 TB/s).
+// the weights (470 MB of 16 experts for 64 tokens: 91 us, 5.2 TB/s).
 //
 // With four waves a workgroup takes 64 columns and leaves them in fp32, for
 // the second product to quantize: for a few pairs there are too few 128
@@ -331,7 +331,7 @@ __global__ __launch_bounds__(64 * W * KS) void moe_gate_up_kernel(
 
 // Second product of a batch, unweighted: out[row] = h w2^T in fp32, one 128
 // column block of one unit per workgroup.  Bound by the weights (235 MB for 64
-// tokens, 16 experts: 47.5 us, 4.9 TB/s).  With the tokens' weighted sum in
+// tokens, 16 experts: 50.8 us, 4.6 TB/s).  With the tokens' weighted sum in
 // the same launch, which has to gather a column block's experts in one
 // workgroup, it took 134 us.
 template <int R, int D, bool kE8>
@@ -409,7 +409,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
 // each streaming its share of the weights through a ring of its own in LDS,
 // with no barrier.  A wave adds its weighted products to a slice of its own
 // ([token][16] fp32); the slices are summed in wave order at the end.
-// One token, 8 experts of 7168 x 2048: 25.4 us for 117 MB (4.6 TB/s), of which
+// One token, 8 experts of 7168 x 2048: 26.5 us for 117 MB (4.4 TB/s), of which
 // about 5 us pass before the first product (ids, hidden rows, first weights,
 // one load's latency after the other).
 template <bool kE8>

@@ -8,11 +8,13 @@
 // plus bias.  The 64-bit rank keeps the choice of experts independent of how
 // an fp32 exponential rounds; scores that become weights are fp32.
 //
-// Bound: a row is E loads and k dependent rounds of a wave-wide maximum, so
-// latency, not bandwidth, sets the time.  256 fp32 experts, 8 chosen in 4 of 8
-// groups by biased sigmoid: one row 5.4 us, 4096 rows 11.1 us (4.5 MB; 1, 2, 8 or
-// 16 rows a workgroup instead of 4 take as long).  The gradient of
-// 8192 x 128 bf16, softmax: 5.1 us for 4.7 MB.
+// Bound: a row is E loads and k dependent rounds of a wave-wide maximum, so for
+// one row latency sets the time.  256 fp32 experts, 8 chosen in 4 of 8 groups by
+// biased sigmoid: one row 5.4 us, 4096 rows 11.1 us, 9.8 in a sequence of calls
+// (4.5 MB; 1, 2, 8 or 16 rows a workgroup instead of 4 take as long).  All 4096
+// waves are resident at once, so what they take beyond one row's time is issue:
+// 256 64-bit scores a row and rounds that cost a whole wave.  The gradient of
+// 8192 x 128 bf16, softmax: 5.2 us for 4.7 MB.
 #include "device_common.h"
 #include "ops_launch.h"
 #include "wave_ops.h"
