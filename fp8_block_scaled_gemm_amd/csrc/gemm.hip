@@ -221,11 +221,11 @@ constexpr int kNoAdapter = 0x7fffffff;
 // one request's adapter stays in that request's rows).  The vector is fp32; its
 // first part is its upper 16 bits, the second the rest rounded to bf16, off by
 // at most 2^-16 of the value, far below the final rounding to bf16.  Cut off and
-// not rounded, the parts have one sign, and the second is never 0 beside a first
-// that is not (2^-24 of it instead, within fp32's own rounding): so an infinity
-// in the adapter gives the infinity that it gives with the vector itself, where
-// a second part of 0 or of the other sign would make it NaN, and a number past
-// the largest bf16 stays finite.  Both parts of an infinity are infinite.  Bound by the steps: each adapter of a tile costs its reads
+// not rounded, the parts have one sign, and where there is no rest both are half
+// of the value: so an infinity in the adapter gives the infinity that it gives
+// with the vector itself, where a second part of 0 or of the other sign would
+// make it NaN (values below 2^-102 may leave no rest), both parts of an infinity
+// are infinite, and a number past the largest bf16 stays finite.  Bound by the steps: each adapter of a tile costs its reads
 // of the vectors, products and a barrier (4096 x 7168 x 2048, rank
 // 64: 82 us with 8 packed prompts, 115 us with 8 adapters in every tile,
 // against 69 us without adapters); four slabs in flight instead of two gained
@@ -305,9 +305,9 @@ __device__ __forceinline__ void add_lora(v4f (&acc)[T::TM][T::TN], uint8_t* smem
             for (int q = 0; q < 8; ++q) {
                 const float v = in ? scale[i] * f[i][q >> 2][q & 3] : 0.0f;
                 const float top = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
-                const float rest = v == top ? (fabsf(v) < INFINITY ? v * 0x1p-24f : v) : v - top;
-                hi[q] = (__bf16)top;
-                lo[q] = (__bf16)rest;
+                const bool whole = v == top;
+                hi[q] = (__bf16)(whole ? 0.5f * v : top);
+                lo[q] = (__bf16)(whole ? 0.5f * v : v - top);
             }
             uint8_t* const to = smem + r * 128 + ((c ^ (r & 7)) << 4);
             *reinterpret_cast<v8bf*>(to) = hi;
