@@ -53,9 +53,9 @@ __device__ __forceinline__ float scale_e8(float p, int ea, int eb) {
 // quantized next, where an error moves codes, and the second one's are promised
 // in 32 bits (two products that cancel would take the bits of the others with
 // them).  It costs the widening, 16 conversions a fragment: the second product
-// 0 to 5% of a call (one token of 8 experts of 7168 x 2048 68.7 -> 69.5 us, 64
-// tokens of 16 148.7 -> 152.9, 251 tokens, one pair in eight here, 146.2 ->
-// 146.4, 256 tokens of 16 experts of 4096 x 1024 161 -> 169).
+// 0 to 5% of a call (one token of 8 experts of 7168 x 2048 68.4 -> 69.1 us, 64
+// tokens of 16 146 -> 149.5, 251 tokens, one pair in eight here, 145.5 -> 146.0,
+// 256 tokens of 16 experts of 4096 x 1024 160 -> 168.5).
 template <int R, int C, bool kE8>
 __device__ __forceinline__ void multiply_exact(const Block<R, C, kE8>& k, int rows, v4f (&acc)[R][C]) {
     v8bf b[C][4];
