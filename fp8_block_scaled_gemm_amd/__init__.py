@@ -1,17 +1,17 @@
 """MI355X (gfx950) FP8 block-scaled NT GEMM: thin Python binding.
 
 Every function here has the name of the C-ABI entry point it calls
-(include/dg_fp8.h, include/dg_ops.h) and only marshals arguments: it checks
-torch tensor dtypes, shapes and devices, passes raw device pointers and the
-current HIP stream, and raises ``DGError`` on a nonzero status.  For the
-operators of dg_ops.h a compiled extension, ``_binding.so``, does so.  All
+(include/dg_fp8.h, dg_ops.h, dg_experts.h, dg_int8.h) and only marshals
+arguments: it checks torch tensor dtypes, shapes and devices, passes raw device
+pointers and the current HIP stream, and raises ``DGError`` on a nonzero status.
+For the operators of the last three a compiled extension, ``_binding.so``, does so.  All
 arithmetic runs in the HIP kernels of ``libdgfp8.so``; there is no CPU
 fallback, and a call fails loudly when the library has not been built
 (``python -m fp8_block_scaled_gemm_amd.build``).
 
 Tensor conventions: e4m3 codes are ``torch.uint8`` (or
-``torch.float8_e4m3fn``, viewed as bytes), scales ``torch.float32``, group
-arrays ``torch.int32``, and D is ``torch.bfloat16`` (or ``torch.uint16`` /
+``torch.float8_e4m3fn``, viewed as bytes), scales ``torch.float32``, int8 codes
+``torch.int8``, group arrays ``torch.int32``, and D is ``torch.bfloat16`` (or ``torch.uint16`` /
 ``torch.int16`` holding bf16 bit patterns).  All tensors live on the GPU,
 are contiguous and 16-byte aligned.
 """
@@ -34,6 +34,12 @@ __all__ = [
     "dg_moe_topk", "dg_moe_topk_backward", "dg_moe_mlp_fp8", "dg_moe_mlp_fp8_e8m0",
     "dg_fp8_gemm_nt_lora", "dg_fp8_gemm_nt_lora_e8m0",
     "dg_moe_mlp_fp8_workspace", "dg_fp8_gemm_nt_lora_workspace",
+    "dg_moe_sort", "dg_moe_sort_rows", "dg_moe_sort_workspace",
+    "dg_moe_dispatch", "dg_moe_dispatch_fp8", "dg_moe_dispatch_fp8_e8m0", "dg_moe_dispatch_int8",
+    "dg_moe_unpermute", "dg_moe_unpermute_backward",
+    "dg_swiglu", "dg_swiglu_quantize_fp8", "dg_swiglu_quantize_fp8_e8m0", "dg_swiglu_quantize_int8",
+    "dg_swiglu_backward",
+    "dg_int8_gemm_nt", "dg_int8_gemm_grouped_contiguous", "dg_quantize_int8_per_row",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -87,6 +93,24 @@ def load_library():
         ("dg_fp8_gemm_nt_lora", [p] * 10 + [i64] * 5 + [p, i64, p]),
         ("dg_fp8_gemm_nt_lora_e8m0", [p] * 10 + [i64] * 5 + [p, i64, p]),
         ("dg_fp8_gemm_nt_lora_workspace", [i64] * 5 + [pi64]),
+        ("dg_moe_sort", [p] * 4 + [i64] * 4 + [p, i64, p]),
+        ("dg_moe_sort_rows", [i64] * 3 + [pi64]),
+        ("dg_moe_sort_workspace", [i64] * 3 + [pi64]),
+        ("dg_moe_dispatch", [p] * 6 + [i64] * 5 + [p, i64, p]),
+        ("dg_moe_dispatch_fp8", [p] * 7 + [i64] * 5 + [p, i64, p]),
+        ("dg_moe_dispatch_fp8_e8m0", [p] * 7 + [i64] * 5 + [p, i64, p]),
+        ("dg_moe_dispatch_int8", [p] * 7 + [i64] * 5 + [p, i64, p]),
+        ("dg_moe_unpermute", [p] * 4 + [i64] * 4 + [p]),
+        ("dg_moe_unpermute_backward", [p] * 7 + [i64] * 4 + [p]),
+        ("dg_swiglu", [p] * 3 + [i64] * 2 + [p]),
+        ("dg_swiglu_quantize_fp8", [p] * 4 + [i64] * 2 + [p]),
+        ("dg_swiglu_quantize_fp8_e8m0", [p] * 4 + [i64] * 2 + [p]),
+        ("dg_swiglu_quantize_int8", [p] * 4 + [i64] * 2 + [p]),
+        ("dg_swiglu_backward", [p] * 4 + [i64] * 2 + [p]),
+        ("dg_int8_gemm_nt", [p] * 5 + [i64] * 3 + [p]),
+        ("dg_int8_gemm_grouped_contiguous", [p] * 6 + [i64] * 4 + [p]),
+        ("dg_quantize_int8_per_row", [p, i64, i64, p, p, p]),
+        ("dg_quantize_int8_per_row_bf16", [p, i64, i64, p, p, p]),
     ]:
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -523,3 +547,219 @@ def dg_fp8_gemm_nt_lora_e8m0(A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling, w
         _warn_no_grad("dg_fp8_gemm_nt_lora_e8m0", "in D")
     return _done("dg_fp8_gemm_nt_lora_e8m0", ops.gemm_lora(True, A, sa, B, sb, D, x, lora_a, lora_b, ids, scaling,
                                                            workspace, _raw_stream(A)))
+
+
+# ------- expert layers for many tokens (dg_experts.h), int8 products (dg_int8.h)
+
+_BF16, _FP8, _FP8_E8M0, _INT8 = range(4)  # how rows are held, as in csrc/binding.cpp
+
+
+def dg_moe_sort_rows(T, k, E) -> int:
+    """The most sorted rows that T tokens of k choices among E experts can need
+    (a multiple of 128): the rows of the buffers of a dispatch call."""
+    return _workspace_bytes("dg_moe_sort_rows", T, k, E)
+
+
+def dg_moe_sort_workspace(T, k, E) -> int:
+    """Bytes of a uint8 tensor to pass as ``workspace`` to ``dg_moe_sort`` or a
+    dispatch call."""
+    return _workspace_bytes("dg_moe_sort_workspace", T, k, E)
+
+
+def dg_moe_sort(ids, E, rows=None, layout=None, offsets=None, workspace=None):
+    """Tokens sorted by expert: ids[T][k] int32 -> (rows[T][k], layout[M],
+    offsets[E + 1]), all int32.  rows holds each pair's sorted row (-1 where the
+    id is outside [0, E)), layout each sorted row's expert (-1 for padding: a
+    grouped_layout), offsets each expert's first row; every expert's rows are
+    padded to 128.  M is ``dg_moe_sort_rows(T, k, E)``, or what a given layout has."""
+    return _done("dg_moe_sort", _ops().moe_sort(ids, E, rows, layout, offsets, workspace, _raw_stream(ids)))
+
+
+class _Dispatch(torch.autograd.Function):
+    """``dg_moe_dispatch`` with ``dg_moe_unpermute`` without weights as its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, ids, E, workspace):
+        out, rows, layout, offsets = _done("dg_moe_dispatch", _ops().moe_dispatch(
+            _BF16, x, ids, E, None, None, None, None, None, workspace, _raw_stream(x)))
+        ctx.save_for_backward(rows)
+        ctx.mark_non_differentiable(rows, layout, offsets)
+        return out, rows, layout, offsets
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, *_):
+        rows, = ctx.saved_tensors
+        grad = grad.contiguous()
+        return (_done("dg_moe_unpermute", _ops().moe_unpermute(grad, rows, None, None, _raw_stream(grad))),
+                None, None, None)
+
+
+def dg_moe_dispatch(x, ids, E, out=None, rows=None, layout=None, offsets=None, workspace=None):
+    """Sorting and copying in one call: x[T][H] bf16, ids[T][k] -> (out[M][H]
+    bf16, rows, layout, offsets), the plan as in ``dg_moe_sort``; rows of padding
+    are zeros.  Where x requires a gradient and no buffer is given, out carries it."""
+    ops = _ops()
+    if ops.wants_grad(x):
+        if out is None and rows is None and layout is None and offsets is None:
+            return _Dispatch.apply(x, ids, E, workspace)
+        _warn_no_grad("dg_moe_dispatch", "in outputs that are given")
+    return _done("dg_moe_dispatch", ops.moe_dispatch(_BF16, x, ids, E, out, None, rows, layout, offsets, workspace,
+                                                     _raw_stream(x)))
+
+
+def _no_grad_rows(name, call, x, *given):
+    """A quantizing call: new outputs refuse to pass a gradient back, given ones warn."""
+    def done():
+        return _done(name, call())
+    if not _ops().wants_grad(x):
+        return done()
+    if all(g is None for g in given):
+        return _NoGradient.apply(name, done, x)
+    _warn_no_grad(name, "in outputs that are given", 4)
+    return done()
+
+
+def _dispatch_codes(name, held, x, ids, E, q, s, rows, layout, offsets, workspace):
+    return _no_grad_rows(name, lambda: _ops().moe_dispatch(held, x, ids, E, q, s, rows, layout, offsets, workspace,
+                                                           _raw_stream(x)), x, q, s)
+
+
+def dg_moe_dispatch_fp8(x, ids, E, q=None, s=None, rows=None, layout=None, offsets=None, workspace=None):
+    """``dg_moe_dispatch`` into e4m3 codes, quantized once per token: (q[M][H]
+    uint8, s[M][H/128] fp32, rows, layout, offsets); rows of padding in q and s
+    are left as they were."""
+    return _dispatch_codes("dg_moe_dispatch_fp8", _FP8, x, ids, E, q, s, rows, layout, offsets, workspace)
+
+
+def dg_moe_dispatch_fp8_e8m0(x, ids, E, q=None, s=None, rows=None, layout=None, offsets=None, workspace=None):
+    """``dg_moe_dispatch_fp8`` with E8M0 scale bytes s[M][e8m0_pitch(H/128)]."""
+    return _dispatch_codes("dg_moe_dispatch_fp8_e8m0", _FP8_E8M0, x, ids, E, q, s, rows, layout, offsets, workspace)
+
+
+def dg_moe_dispatch_int8(x, ids, E, q=None, s=None, rows=None, layout=None, offsets=None, workspace=None):
+    """``dg_moe_dispatch_fp8`` into int8 with one scale per row: q[M][H] int8, s[M] fp32."""
+    return _dispatch_codes("dg_moe_dispatch_int8", _INT8, x, ids, E, q, s, rows, layout, offsets, workspace)
+
+
+class _Unpermute(torch.autograd.Function):
+    """``dg_moe_unpermute`` with its gradients for the rows and the weights."""
+
+    @staticmethod
+    def forward(ctx, y, rows, weights, layout):
+        out = _done("dg_moe_unpermute", _ops().moe_unpermute(y, rows, weights, None, _raw_stream(y)))
+        ctx.save_for_backward(y, rows, weights, layout)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        y, rows, weights, layout = ctx.saved_tensors
+        want_y, _, want_weights, _ = ctx.needs_input_grad
+        gy, gw = _done("dg_moe_unpermute_backward", _ops().moe_unpermute_backward(
+            grad.contiguous(), y, rows, weights, layout, None, None, want_y, want_weights, _raw_stream(y)))
+        return gy, None, gw, None
+
+
+def dg_moe_unpermute(y, rows, weights=None, out=None, *, layout=None):
+    """Sorted rows back to their tokens: out[T][H] bf16 = sum over j of
+    weights[t][j] * y[rows[t][j]] (weights None: ones), entries of rows outside
+    [0, M) add nothing.  Where y or the weights require a gradient and no out is
+    given, out carries it; layout is used by that gradient alone, which clears
+    only the rows of padding where it is given and all of them where it is not."""
+    ops = _ops()
+    if ops.wants_grad(y, weights):
+        if out is None:
+            return _Unpermute.apply(y, rows, weights, layout)
+        _warn_no_grad("dg_moe_unpermute", "in an out that is given")
+    return _done("dg_moe_unpermute", ops.moe_unpermute(y, rows, weights, out, _raw_stream(y)))
+
+
+def dg_moe_unpermute_backward(grad, y, rows, weights=None, layout=None, grad_y=None, grad_weights=None):
+    """Gradients of ``dg_moe_unpermute``: grad[T][H] bf16 -> (grad_y[M][H] bf16,
+    grad_weights[T][k] fp32, or None where weights is None and none is given).
+    Rows of padding are zeros in grad_y where layout is given or grad_y is new;
+    a given grad_y keeps them without layout."""
+    want_weights = weights is not None or grad_weights is not None
+    return _done("dg_moe_unpermute_backward", _ops().moe_unpermute_backward(
+        grad, y, rows, weights, layout, grad_y, grad_weights, True, want_weights, _raw_stream(y)))
+
+
+class _Swiglu(torch.autograd.Function):
+    """``dg_swiglu`` with ``dg_swiglu_backward`` as its gradient."""
+
+    @staticmethod
+    def forward(ctx, z, layout):
+        ctx.save_for_backward(z, layout)
+        return _done("dg_swiglu", _ops().swiglu(_BF16, z, layout, None, None, _raw_stream(z)))
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        z, layout = ctx.saved_tensors
+        return _done("dg_swiglu_backward", _ops().swiglu_backward(z, grad.contiguous(), layout, None, _raw_stream(z))), None
+
+
+def dg_swiglu(z, layout=None, h=None):
+    """Gate between an expert's products: z[M][2I] bf16 -> h[M][I] bf16 =
+    silu(z[:, :I]) * z[:, I:]; rows whose layout entry is negative are zeros.
+    Where z requires a gradient and no h is given, h carries it."""
+    ops = _ops()
+    if ops.wants_grad(z):
+        if h is None:
+            return _Swiglu.apply(z, layout)
+        _warn_no_grad("dg_swiglu", "in an h that is given")
+    return _done("dg_swiglu", ops.swiglu(_BF16, z, layout, h, None, _raw_stream(z)))
+
+
+def _swiglu_codes(name, held, z, layout, q, s):
+    return _no_grad_rows(name, lambda: _ops().swiglu(held, z, layout, q, s, _raw_stream(z)), z, q, s)
+
+
+def dg_swiglu_quantize_fp8(z, layout=None, q=None, s=None):
+    """``dg_swiglu`` into e4m3 codes without a rounding between: (q[M][I] uint8,
+    s[M][I/128] fp32); rows whose layout entry is negative are left as they were."""
+    return _swiglu_codes("dg_swiglu_quantize_fp8", _FP8, z, layout, q, s)
+
+
+def dg_swiglu_quantize_fp8_e8m0(z, layout=None, q=None, s=None):
+    """``dg_swiglu_quantize_fp8`` with E8M0 scale bytes s[M][e8m0_pitch(I/128)]."""
+    return _swiglu_codes("dg_swiglu_quantize_fp8_e8m0", _FP8_E8M0, z, layout, q, s)
+
+
+def dg_swiglu_quantize_int8(z, layout=None, q=None, s=None):
+    """``dg_swiglu_quantize_fp8`` into int8 with one scale per row: q[M][I] int8, s[M] fp32."""
+    return _swiglu_codes("dg_swiglu_quantize_int8", _INT8, z, layout, q, s)
+
+
+def dg_swiglu_backward(z, grad_h, layout=None, grad_z=None):
+    """Gradient of ``dg_swiglu``: (z[M][2I], grad_h[M][I]) bf16 -> grad_z[M][2I]
+    bf16; rows whose layout entry is negative are zeros."""
+    return _done("dg_swiglu_backward", _ops().swiglu_backward(z, grad_h, layout, grad_z, _raw_stream(z)))
+
+
+def dg_int8_gemm_nt(A, sa, B, sb, D):
+    """Dense int8 product: D[M][N] = bf16(sa[m] * sb[n] * (A @ B^T)), A[M][K] and
+    B[N][K] int8, sa[M] and sb[N] fp32, the sums exact.  No gradient is recorded in D."""
+    ops = _ops()
+    if ops.wants_grad(sa, sb):
+        _warn_no_grad("dg_int8_gemm_nt", "in D")
+    return _done("dg_int8_gemm_nt", ops.int8_gemm(A, sa, B, sb, D, None, _raw_stream(A)))
+
+
+def dg_int8_gemm_grouped_contiguous(A, sa, B, sb, D, grouped_layout):
+    """Contiguous-grouped int8 product: row r of D uses B[grouped_layout[r]]
+    ([G][N][K] int8) and sb[G][N]; rows whose id is outside [0, G) are not
+    written.  No gradient is recorded in D."""
+    ops = _ops()
+    if ops.wants_grad(sa, sb):
+        _warn_no_grad("dg_int8_gemm_grouped_contiguous", "in D")
+    if grouped_layout is None:
+        raise TypeError("grouped_layout must be a torch.Tensor")
+    return _done("dg_int8_gemm_grouped_contiguous", ops.int8_gemm(A, sa, B, sb, D, grouped_layout, _raw_stream(A)))
+
+
+def dg_quantize_int8_per_row(x, q=None, s=None):
+    """x[M][K] fp32 or bf16 -> (q[M][K] int8, s[M] fp32): per token for the
+    activations, per output channel for the weights."""
+    return _no_grad_rows("dg_quantize_int8_per_row", lambda: _ops().quantize_int8(x, q, s, _raw_stream(x)), x, q, s)

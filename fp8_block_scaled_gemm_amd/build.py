@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdgfp8.so")
 BINDING = os.path.join(HERE, "_binding.so")
-SOURCES = ["api.hip", "gemm.hip", "quantize.hip", "api_ops.hip", "router.hip", "moe.hip", "lora.hip"]
+SOURCES = ["api.hip", "gemm.hip", "quantize.hip", "api_ops.hip", "router.hip", "moe.hip", "lora.hip",
+           "api_experts.hip", "experts.hip", "int8.hip"]
 ARCH = "gfx950"
 
 

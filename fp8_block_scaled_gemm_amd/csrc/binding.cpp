@@ -1,4 +1,5 @@
-// Python entry to the operators of include/dg_ops.h: checks torch tensors,
+// Python entry to the operators of include/dg_ops.h, dg_experts.h and
+// dg_int8.h: checks torch tensors,
 // allocates outputs and workspaces that the caller did not give from torch's
 // caching allocator, and calls the C ABI.  These calls run a few microseconds
 // on the GPU, and checking ten tensors in Python took as long; here it takes
@@ -17,7 +18,10 @@
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
+#include "dg_experts.h"
+#include "dg_int8.h"
 #include "dg_ops.h"
 #include "on_device.h"
 
@@ -296,6 +300,293 @@ PyObject* gemm_lora(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// The tensor that a caller gave, or the new one.
+PyObject* returned(PyObject* given, const at::Tensor& t) {
+    return given == Py_None ? THPVariable_Wrap(t) : Py_NewRef(given);
+}
+
+// A tuple of the calls' outputs; `given` are the arguments they came as.
+PyObject* returned(std::initializer_list<std::pair<PyObject*, const at::Tensor*>> outs) {
+    PyObject* const tuple = PyTuple_New((Py_ssize_t)outs.size());
+    if (tuple == nullptr) return nullptr;
+    Py_ssize_t i = 0;
+    for (const auto& o : outs) PyTuple_SET_ITEM(tuple, i++, returned(o.first, *o.second));
+    return tuple;
+}
+
+// A pointer that may be left out: None.
+void* pointer_or_null(PyObject* o, const char* what, std::initializer_list<at::ScalarType> types,
+                      std::initializer_list<int64_t> shape, at::Device dev) {
+    return o == Py_None ? nullptr : pointer(o, what, types, shape, dev);
+}
+
+// The plan of a sort: sizes, outputs that were given or are new, workspace.
+struct Plan {
+    int64_t T, k, E, M;
+    at::Tensor rows, layout, offsets, ws;
+    const int32_t* ids;
+    int32_t *prows, *playout, *poffsets;
+    dg_status status;
+
+    // `held`: the buffer for the sorted rows, or None
+    Plan(PyObject* o, PyObject* experts, PyObject* rows_, PyObject* layout_, PyObject* offsets_, PyObject* held,
+         PyObject* workspace_) {
+        const at::Tensor& t = sized(o, "ids", 2);
+        const at::Device dev = t.device();
+        T = t.size(0), k = t.size(1), E = integer(experts), M = 0;
+        int64_t bytes = 0;
+        if ((status = dg_moe_sort_rows(T, k, E, &M)) != DG_OK) return;
+        if ((status = dg_moe_sort_workspace(T, k, E, &bytes)) != DG_OK) return;
+        if (layout_ != Py_None)
+            M = sized(layout_, "layout", 1).size(0);
+        else if (held != Py_None)
+            M = sized(held, "the rows' buffer", 2).size(0);
+        ids = (const int32_t*)pointer(t, "ids", {at::kInt}, {T, k}, dev);
+        rows = given_or_new(rows_, "rows", {T, k}, at::kInt, dev);
+        layout = given_or_new(layout_, "layout", {M}, at::kInt, dev);
+        offsets = given_or_new(offsets_, "offsets", {E + 1}, at::kInt, dev);
+        prows = (int32_t*)pointer(rows, "rows", {at::kInt}, {T, k}, dev);
+        playout = (int32_t*)pointer(layout, "layout", {at::kInt}, {M}, dev);
+        poffsets = (int32_t*)pointer(offsets, "offsets", {at::kInt}, {E + 1}, dev);
+        ws = workspace(workspace_, bytes, dev);
+    }
+};
+
+// ids, E, rows, layout, offsets, workspace, stream
+PyObject* moe_sort(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded<7>(args, n, [](PyObject* const* a) -> PyObject* {
+        const Plan p(a[0], a[1], a[2], a[3], a[4], Py_None, a[5]);
+        if (p.status != DG_OK) return PyLong_FromLong(p.status);
+        void* const stream = stream_of(a[6]);
+        void* const pws = p.ws.data_ptr();
+        const OnDevice on(p.rows.device().index());
+        const dg_status s = unlocked([&] {
+            return dg_moe_sort(p.ids, p.prows, p.playout, p.poffsets, p.T, p.k, p.E, p.M, pws, p.ws.numel(), stream);
+        });
+        if (s != DG_OK) return PyLong_FromLong(s);
+        return returned({{a[2], &p.rows}, {a[3], &p.layout}, {a[4], &p.offsets}});
+    });
+}
+
+// How the rows of a dispatch or gate call are held, as __init__.py numbers them.
+enum Held { kBf16 = 0, kFp8 = 1, kFp8E8 = 2, kInt8 = 3 };
+
+// The codes or rows [M][width] and the scales of a call, given or new.
+struct Rows {
+    at::Tensor q, s;
+    void *pq, *ps;
+
+    Rows(int held, PyObject* q_, PyObject* s_, const char* name, int64_t M, int64_t width, at::Device dev) : ps(nullptr) {
+        const int64_t kb = width / 128;
+        const at::ScalarType qt = held == kBf16 ? at::kBFloat16 : held == kInt8 ? at::kChar : at::kByte;
+        q = given_or_new(q_, name, {M, width}, qt, dev);
+        if (held == kBf16) {
+            pq = pointer(q, name, DG_BITS, {M, width}, dev);
+            return;
+        }
+        pq = held == kInt8 ? pointer(q, name, {at::kChar}, {M, width}, dev) : pointer(q, name, DG_CODES, {M, width}, dev);
+        if (held == kInt8) {
+            s = given_or_new(s_, "s", {M}, at::kFloat, dev);
+            ps = pointer(s, "s", {at::kFloat}, {M}, dev);
+        } else if (held == kFp8) {
+            s = given_or_new(s_, "s", {M, kb}, at::kFloat, dev);
+            ps = pointer(s, "s", {at::kFloat}, {M, kb}, dev);
+        } else {
+            const int64_t pitch = e8m0_pitch(kb);
+            s = given_or_new(s_, "s", {M, pitch}, at::kByte, dev);
+            if (s_ == Py_None && pitch != kb) s.zero_();  // the padding bytes, which no kernel writes
+            ps = pointer(s, "s", {at::kByte}, {M, pitch}, dev);
+        }
+    }
+};
+
+// held, x, ids, E, q, s, rows, layout, offsets, workspace, stream
+PyObject* moe_dispatch(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded<11>(args, n, [](PyObject* const* a) -> PyObject* {
+        const int held = (int)integer(a[0]);
+        const at::Tensor& x = sized(a[1], "x", 2);
+        const int64_t H = x.size(1);
+        const at::Device dev = x.device();
+        const Plan p(a[2], a[3], a[6], a[7], a[8], a[4], a[9]);
+        if (p.status != DG_OK) return PyLong_FromLong(p.status);
+        const auto* px = (const uint16_t*)pointer(x, "x", {at::kBFloat16}, {p.T, H}, dev);
+        pointer(a[2], "ids", {at::kInt}, {p.T, p.k}, dev);  // on x's device
+        const OnDevice on(dev.index());
+        const Rows r(held, a[4], a[5], held == kBf16 ? "out" : "q", p.M, H, dev);
+        void* const stream = stream_of(a[10]);
+        void* const pws = p.ws.data_ptr();
+        const dg_status s = unlocked([&] {
+            switch (held) {
+                case kBf16:
+                    return dg_moe_dispatch(px, p.ids, (uint16_t*)r.pq, p.prows, p.playout, p.poffsets, p.T, p.k, p.E, H, p.M,
+                                           pws, p.ws.numel(), stream);
+                case kFp8:
+                    return dg_moe_dispatch_fp8(px, p.ids, (uint8_t*)r.pq, (float*)r.ps, p.prows, p.playout, p.poffsets, p.T,
+                                               p.k, p.E, H, p.M, pws, p.ws.numel(), stream);
+                case kFp8E8:
+                    return dg_moe_dispatch_fp8_e8m0(px, p.ids, (uint8_t*)r.pq, (uint8_t*)r.ps, p.prows, p.playout,
+                                                    p.poffsets, p.T, p.k, p.E, H, p.M, pws, p.ws.numel(), stream);
+                default:
+                    return dg_moe_dispatch_int8(px, p.ids, (int8_t*)r.pq, (float*)r.ps, p.prows, p.playout, p.poffsets, p.T,
+                                                p.k, p.E, H, p.M, pws, p.ws.numel(), stream);
+            }
+        });
+        if (s != DG_OK) return PyLong_FromLong(s);
+        if (held == kBf16) return returned({{a[4], &r.q}, {a[6], &p.rows}, {a[7], &p.layout}, {a[8], &p.offsets}});
+        return returned({{a[4], &r.q}, {a[5], &r.s}, {a[6], &p.rows}, {a[7], &p.layout}, {a[8], &p.offsets}});
+    });
+}
+
+// y, rows, weights, out, stream
+PyObject* moe_unpermute(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded<5>(args, n, [](PyObject* const* a) -> PyObject* {
+        const at::Tensor& y = sized(a[0], "y", 2);
+        const at::Tensor& rows = sized(a[1], "rows", 2);
+        const int64_t M = y.size(0), H = y.size(1), T = rows.size(0), k = rows.size(1);
+        const at::Device dev = y.device();
+        const auto* py = (const uint16_t*)pointer(y, "y", {at::kBFloat16}, {M, H}, dev);
+        const auto* pr = (const int32_t*)pointer(rows, "rows", {at::kInt}, {T, k}, dev);
+        const auto* pw = (const float*)pointer_or_null(a[2], "weights", {at::kFloat}, {T, k}, dev);
+        const at::Tensor out = given_or_new(a[3], "out", {T, H}, at::kBFloat16, dev);
+        auto* po = (uint16_t*)pointer(out, "out", DG_BITS, {T, H}, dev);
+        void* const stream = stream_of(a[4]);
+        const OnDevice on(dev.index());
+        const dg_status s = unlocked([&] { return dg_moe_unpermute(py, pr, pw, po, T, k, H, M, stream); });
+        if (s != DG_OK) return PyLong_FromLong(s);
+        return returned(a[3], out);
+    });
+}
+
+// grad, y, rows, weights, layout, grad_y, grad_weights, want_y, want_weights, stream
+PyObject* moe_unpermute_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded<10>(args, n, [](PyObject* const* a) -> PyObject* {
+        const at::Tensor& g = sized(a[0], "grad", 2);
+        const at::Tensor& y = sized(a[1], "y", 2);
+        const at::Tensor& rows = sized(a[2], "rows", 2);
+        const int64_t T = g.size(0), H = g.size(1), M = y.size(0), k = rows.size(1);
+        const at::Device dev = g.device();
+        const bool want_y = a[7] == Py_True, want_w = a[8] == Py_True;
+        const auto* pg = (const uint16_t*)pointer(g, "grad", {at::kBFloat16}, {T, H}, dev);
+        const auto* py = (const uint16_t*)pointer(y, "y", {at::kBFloat16}, {M, H}, dev);
+        const auto* pr = (const int32_t*)pointer(rows, "rows", {at::kInt}, {T, k}, dev);
+        const auto* pw = (const float*)pointer_or_null(a[3], "weights", {at::kFloat}, {T, k}, dev);
+        const auto* pl = (const int32_t*)pointer_or_null(a[4], "layout", {at::kInt}, {M}, dev);
+        const OnDevice on(dev.index());
+        at::Tensor gy, gw;
+        uint16_t* pgy = nullptr;
+        float* pgw = nullptr;
+        if (want_y) {
+            gy = given_or_new(a[5], "grad_y", {M, H}, at::kBFloat16, dev);
+            pgy = (uint16_t*)pointer(gy, "grad_y", DG_BITS, {M, H}, dev);
+            if (a[5] == Py_None && pl == nullptr) gy.zero_();  // which rows are padding is not known
+        }
+        if (want_w) {
+            gw = given_or_new(a[6], "grad_weights", {T, k}, at::kFloat, dev);
+            pgw = (float*)pointer(gw, "grad_weights", {at::kFloat}, {T, k}, dev);
+        }
+        void* const stream = stream_of(a[9]);
+        const dg_status s = unlocked([&] { return dg_moe_unpermute_backward(pg, py, pr, pw, pl, pgy, pgw, T, k, H, M, stream); });
+        if (s != DG_OK) return PyLong_FromLong(s);
+        PyObject* const out = PyTuple_New(2);
+        if (out == nullptr) return nullptr;
+        PyTuple_SET_ITEM(out, 0, want_y ? returned(a[5], gy) : Py_NewRef(Py_None));
+        PyTuple_SET_ITEM(out, 1, want_w ? returned(a[6], gw) : Py_NewRef(Py_None));
+        return out;
+    });
+}
+
+// held, z, layout, q, s, stream
+PyObject* swiglu(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded<6>(args, n, [](PyObject* const* a) -> PyObject* {
+        const int held = (int)integer(a[0]);
+        const at::Tensor& z = sized(a[1], "z", 2);
+        const int64_t M = z.size(0), I = z.size(1) / 2;
+        const at::Device dev = z.device();
+        const auto* pz = (const uint16_t*)pointer(z, "z", {at::kBFloat16}, {M, 2 * I}, dev);
+        const auto* pl = (const int32_t*)pointer_or_null(a[2], "layout", {at::kInt}, {M}, dev);
+        const OnDevice on(dev.index());
+        const Rows r(held, a[3], a[4], held == kBf16 ? "h" : "q", M, I, dev);
+        void* const stream = stream_of(a[5]);
+        const dg_status s = unlocked([&] {
+            switch (held) {
+                case kBf16: return dg_swiglu(pz, pl, (uint16_t*)r.pq, M, I, stream);
+                case kFp8: return dg_swiglu_quantize_fp8(pz, pl, (uint8_t*)r.pq, (float*)r.ps, M, I, stream);
+                case kFp8E8: return dg_swiglu_quantize_fp8_e8m0(pz, pl, (uint8_t*)r.pq, (uint8_t*)r.ps, M, I, stream);
+                default: return dg_swiglu_quantize_int8(pz, pl, (int8_t*)r.pq, (float*)r.ps, M, I, stream);
+            }
+        });
+        if (s != DG_OK) return PyLong_FromLong(s);
+        if (held == kBf16) return returned(a[3], r.q);
+        return returned({{a[3], &r.q}, {a[4], &r.s}});
+    });
+}
+
+// z, grad_h, layout, grad_z, stream
+PyObject* swiglu_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded<5>(args, n, [](PyObject* const* a) -> PyObject* {
+        const at::Tensor& z = sized(a[0], "z", 2);
+        const int64_t M = z.size(0), I = z.size(1) / 2;
+        const at::Device dev = z.device();
+        const auto* pz = (const uint16_t*)pointer(z, "z", {at::kBFloat16}, {M, 2 * I}, dev);
+        const auto* pg = (const uint16_t*)pointer(a[1], "grad_h", {at::kBFloat16}, {M, I}, dev);
+        const auto* pl = (const int32_t*)pointer_or_null(a[2], "layout", {at::kInt}, {M}, dev);
+        const at::Tensor out = given_or_new(a[3], "grad_z", {M, 2 * I}, at::kBFloat16, dev);
+        auto* po = (uint16_t*)pointer(out, "grad_z", DG_BITS, {M, 2 * I}, dev);
+        void* const stream = stream_of(a[4]);
+        const OnDevice on(dev.index());
+        const dg_status s = unlocked([&] { return dg_swiglu_backward(pz, pg, pl, po, M, I, stream); });
+        if (s != DG_OK) return PyLong_FromLong(s);
+        return returned(a[3], out);
+    });
+}
+
+// A, sa, B, sb, D, grouped_layout (None: dense), stream
+PyObject* int8_gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded<7>(args, n, [](PyObject* const* a) -> PyObject* {
+        const bool grouped = a[5] != Py_None;
+        const at::Tensor& A = sized(a[0], "A", 2);
+        const at::Tensor& B = sized(a[2], "B", grouped ? 3 : 2);
+        const int64_t M = A.size(0), K = A.size(1), G = grouped ? B.size(0) : 1, N = B.size(grouped ? 1 : 0);
+        const at::Device dev = A.device();
+        const auto* pA = (const int8_t*)pointer(A, "A", {at::kChar}, {M, K}, dev);
+        const auto* psa = (const float*)pointer(a[1], "sa", {at::kFloat}, {M}, dev);
+        const auto* pB = (const int8_t*)(grouped ? pointer(B, "B", {at::kChar}, {G, N, K}, dev)
+                                                 : pointer(B, "B", {at::kChar}, {N, K}, dev));
+        const auto* psb = (const float*)(grouped ? pointer(a[3], "sb", {at::kFloat}, {G, N}, dev)
+                                                 : pointer(a[3], "sb", {at::kFloat}, {N}, dev));
+        auto* pD = (uint16_t*)pointer(a[4], "D", DG_BITS, {M, N}, dev);
+        const auto* pl = (const int32_t*)pointer_or_null(a[5], "grouped_layout", {at::kInt}, {M}, dev);
+        void* const stream = stream_of(a[6]);
+        const OnDevice on(dev.index());
+        const dg_status s = unlocked([&] {
+            return grouped ? dg_int8_gemm_grouped_contiguous(pA, psa, pB, psb, pD, pl, M, N, K, G, stream)
+                           : dg_int8_gemm_nt(pA, psa, pB, psb, pD, M, N, K, stream);
+        });
+        if (s != DG_OK) return PyLong_FromLong(s);
+        return Py_NewRef(a[4]);
+    });
+}
+
+// x, q, s, stream
+PyObject* quantize_int8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded<4>(args, n, [](PyObject* const* a) -> PyObject* {
+        const at::Tensor& x = sized(a[0], "x", 2);
+        const int64_t M = x.size(0), K = x.size(1);
+        const at::Device dev = x.device();
+        const bool bf16 = x.scalar_type() == at::kBFloat16;
+        const void* const px = pointer(x, "x", {at::kFloat, at::kBFloat16}, {M, K}, dev);
+        const Rows r(kInt8, a[1], a[2], "q", M, K, dev);
+        void* const stream = stream_of(a[3]);
+        const OnDevice on(dev.index());
+        const dg_status s = unlocked([&] {
+            return bf16 ? dg_quantize_int8_per_row_bf16((const uint16_t*)px, M, K, (int8_t*)r.pq, (float*)r.ps, stream)
+                        : dg_quantize_int8_per_row((const float*)px, M, K, (int8_t*)r.pq, (float*)r.ps, stream);
+        });
+        if (s != DG_OK) return PyLong_FromLong(s);
+        return returned({{a[1], &r.q}, {a[2], &r.s}});
+    });
+}
+
 // Whether gradients are recorded and any of the arguments is a tensor that requires one.
 PyObject* wants_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (c10::GradMode::is_enabled())
@@ -306,7 +597,9 @@ PyObject* wants_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define DG_METHOD(name) {#name, (PyCFunction)(void (*)())name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {DG_METHOD(moe_topk), DG_METHOD(moe_topk_backward), DG_METHOD(moe_mlp), DG_METHOD(gemm_lora),
-                         DG_METHOD(wants_grad),
+                         DG_METHOD(wants_grad), DG_METHOD(moe_sort), DG_METHOD(moe_dispatch), DG_METHOD(moe_unpermute),
+                         DG_METHOD(moe_unpermute_backward), DG_METHOD(swiglu), DG_METHOD(swiglu_backward),
+                         DG_METHOD(int8_gemm), DG_METHOD(quantize_int8),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,611 @@
+// The steps of an expert layer for many tokens around the grouped products.
+// include/dg_experts.h has the definitions.
+#include "experts_launch.h"
+
+#include <algorithm>
+#include <type_traits>
+
+#include "rows_common.h"
+
+namespace dg {
+
+// ------------------------------------------------------------------ the sort
+//
+// A stable counting sort by expert, without atomics on memory: (1) each
+// workgroup counts its run of pairs per expert into a table [run][E]; (2) each
+// workgroup adds up the table's columns (all of it: the experts' sizes; the
+// runs before its own: where its pairs go on), turns the sizes into padded
+// offsets, and places its pairs 1024 at a time.  Within a wave a pair's rank is
+// the number of lanes below it with the same expert, from one ballot per bit of
+// the expert's number; across the 16 waves of a tile each wave leaves its count
+// in a byte per expert, so that a pair's rank in the tile is a sum of at most 16
+// bytes.  One run alone needs no table and one launch.
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSortOnePairs = 8192;  // pairs that one workgroup sorts by itself
+constexpr int kSortMaxRuns = 256;
+
+// Pairs in a run, a multiple of the tile.
+static int64_t sort_run(int64_t P) {
+    if (P <= kSortOnePairs) return kSortOnePairs;
+    return std::max<int64_t>(1024, ((P + kSortMaxRuns - 1) / kSortMaxRuns + 1023) / 1024 * 1024);
+}
+static int sort_runs(int64_t P) { return (int)std::max<int64_t>(1, (P + sort_run(P) - 1) / sort_run(P)); }
+
+int64_t sort_workspace(int64_t T, int64_t k, int64_t E) {
+    const int runs = sort_runs(T * k);
+    return runs == 1 ? 0 : (int64_t)runs * E * 4;
+}
+
+// The number of pairs of each expert among ids [begin, end), added to count[E]
+// in LDS by n threads.
+__device__ __forceinline__ void count_pairs(const int32_t* __restrict__ ids, int64_t begin, int64_t end, int E,
+                                            int* count, int tid, int n) {
+    for (int64_t p = begin + tid; p < end; p += n) {
+        const int e = ids[p];
+        if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+    }
+}
+
+__global__ __launch_bounds__(kSortThreads) void moe_sort_count_kernel(const int32_t* __restrict__ ids, int64_t P, int E,
+                                                                      int64_t run, int* __restrict__ table) {
+    extern __shared__ int count[];
+    const int tid = threadIdx.x;
+    for (int e = tid; e < E; e += kSortThreads) count[e] = 0;
+    __syncthreads();
+    const int64_t begin = blockIdx.x * run;
+    count_pairs(ids, begin, min(begin + run, P), E, count, tid, kSortThreads);
+    __syncthreads();
+    for (int e = tid; e < E; e += kSortThreads) table[(int64_t)blockIdx.x * E + e] = count[e];
+}
+
+// offsets[0 .. E] in LDS from the experts' sizes: each padded to 128, summed
+// exclusively.  `part` holds a wave's sum each; all threads of the workgroup.
+template <int kThreads>
+__device__ __forceinline__ void padded_offsets(const int* size, int* offsets, int* part, int E, int tid) {
+    const int each = (E + kThreads - 1) / kThreads, first = tid * each;
+    int own = 0;
+    for (int i = 0; i < each; ++i)
+        if (first + i < E) own += (size[first + i] + 127) & ~127;
+    int upto = own;  // over the wave's lanes up to this one
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int below = __shfl_up(upto, d, 64);
+        if ((tid & 63) >= d) upto += below;
+    }
+    if ((tid & 63) == 63) part[tid >> 6] = upto;
+    __syncthreads();
+    int at = upto - own;
+    for (int w = 0; w < (tid >> 6); ++w) at += part[w];
+    for (int i = 0; i < each; ++i)
+        if (first + i < E) {
+            offsets[first + i] = at;
+            at += (size[first + i] + 127) & ~127;
+            if (first + i == E - 1) offsets[E] = at;
+        }
+    __syncthreads();
+}
+
+// layout of the 128-row blocks first, first + step, ... of M rows, one wave
+// per block, from the experts' offsets and sizes (LDS).
+__device__ __forceinline__ void write_layout(const int* offsets, const int* size, int E, int64_t M, int64_t first,
+                                             int64_t step, int32_t* __restrict__ layout, int lane) {
+    for (int64_t b = first; b < M / 128; b += step) {
+        const int64_t r0 = b * 128;
+        int2 v = {-1, -1};
+        if (r0 < offsets[E]) {
+            int lo = 0, hi = E - 1;  // the last expert that starts at or before the block has rows
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (offsets[mid] <= r0)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int r = (int)r0 + 2 * lane - offsets[lo];
+            v.x = r < size[lo] ? lo : -1;
+            v.y = r + 1 < size[lo] ? lo : -1;
+        }
+        *reinterpret_cast<int2*>(layout + r0 + 2 * lane) = v;
+    }
+}
+
+// Sum over 16 byte counts of one expert: those of the waves before `wave`, and
+// of all of them.
+__device__ __forceinline__ void sum_counts(const v4u& c, int wave, int& before, int& all) {
+    uint32_t b = 0, s = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int bytes = min(max(wave - 4 * w, 0), 4);
+        const uint32_t mask = bytes == 4 ? 0xffffffffu : (1u << (8 * bytes)) - 1u;
+        b = __builtin_amdgcn_sad_u8(c[w] & mask, 0, b);
+        s = __builtin_amdgcn_sad_u8(c[w], 0, s);
+    }
+    before = (int)b;
+    all = (int)s;
+}
+
+static size_t sort_lds(int E) { return (size_t)E * 16 + (size_t)E * 4 * 2 + (size_t)(E + 1) * 4 + kSortWaves * 4 + 16; }
+
+__global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(const int32_t* __restrict__ ids, int64_t P, int E,
+                                                                      int64_t run, int runs,
+                                                                      const int* __restrict__ table,
+                                                                      int32_t* __restrict__ rows,
+                                                                      int32_t* __restrict__ layout,
+                                                                      int32_t* __restrict__ out_offsets, int64_t M) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    v4u* const counts = reinterpret_cast<v4u*>(lds);         // [E] a byte for each wave
+    int* const size = reinterpret_cast<int*>(counts + E);    // [E]
+    int* const next = size + E;                              // [E] row of the next pair
+    int* const offsets = next + E;                           // [E + 1]
+    int* const part = offsets + E + 1;                       // [kSortWaves]
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int me = blockIdx.x;
+    for (int e = tid; e < E; e += kSortThreads) {
+        counts[e] = v4u{0, 0, 0, 0};
+        size[e] = next[e] = 0;
+    }
+    __syncthreads();
+    if (runs == 1) {
+        count_pairs(ids, 0, P, E, size, tid, kSortThreads);
+    } else {
+        // the table's rows shared out over groups of threads where experts are few
+        int width = 64;
+        while (width < E && width < kSortThreads) width *= 2;
+        const int group = tid / width, groups = kSortThreads / width;
+        for (int e = tid % width; e < E; e += width) {
+            int all = 0, before = 0;
+            for (int r = group; r < runs; r += groups) {
+                const int n = table[(int64_t)r * E + e];
+                all += n;
+                before += r < me ? n : 0;
+            }
+            atomicAdd(&size[e], all);
+            atomicAdd(&next[e], before);
+        }
+    }
+    __syncthreads();
+    padded_offsets<kSortThreads>(size, offsets, part, E, tid);
+    for (int e = tid; e < E; e += kSortThreads) next[e] += offsets[e];
+    if (me == 0)
+        for (int e = tid; e <= E; e += kSortThreads) out_offsets[e] = offsets[e];
+    __syncthreads();
+    write_layout(offsets, size, E, M, (int64_t)me * kSortWaves + wave, (int64_t)runs * kSortWaves, layout, lane);
+
+    const int bits = 32 - __builtin_clz(max(E - 1, 1));
+    const int64_t begin = me * run, end = min(begin + run, P);
+    for (int64_t base = begin; base < end; base += kSortThreads) {
+        const int64_t p = base + tid;
+        const int e = p < end ? ids[p] : -1;
+        const bool here = e >= 0 && e < E;
+        uint64_t same = __ballot(here);
+        for (int b = 0; b < bits; ++b) {
+            const bool bit = (e >> b) & 1;
+            const uint64_t set = __ballot(bit);
+            same &= bit ? set : ~set;
+        }
+        const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+        if (here && rank == 0) reinterpret_cast<uint8_t*>(counts + e)[wave] = (uint8_t)__popcll(same);
+        __syncthreads();
+        int before = 0, all = 0;
+        if (here) {
+            sum_counts(counts[e], wave, before, all);
+            rows[p] = next[e] + before + rank;
+        } else if (p < end) {
+            rows[p] = -1;
+        }
+        if (base + kSortThreads < end) {
+            __syncthreads();
+            if (here && before == 0 && rank == 0) {  // one pair of each expert in the tile
+                next[e] += all;
+                counts[e] = v4u{0, 0, 0, 0};
+            }
+            __syncthreads();
+        }
+    }
+}
+
+dg_status launch_sort(const SortArgs& a, hipStream_t stream) {
+    const int64_t P = a.T * a.k, run = sort_run(P);
+    const int runs = sort_runs(P);
+    int* const table = static_cast<int*>(a.workspace);
+    if (runs > 1) {
+        hipLaunchKernelGGL(moe_sort_count_kernel, dim3(runs), dim3(kSortThreads), a.E * 4, stream, a.ids, P, a.E, run,
+                           table);
+        if (launched() != DG_OK) return DG_ERR_HIP;
+    }
+    hipLaunchKernelGGL(moe_sort_place_kernel, dim3(runs), dim3(kSortThreads), sort_lds(a.E), stream, a.ids, P, a.E, run,
+                       runs, table, a.rows, a.layout, a.offsets, a.M);
+    return launched();
+}
+
+// --------------------------------------------------------------- the copies
+
+constexpr int kZeroRows = 16;  // rows that one workgroup sets to zero where they are padding
+
+// Sets those of kZeroRows rows to zero whose layout entry is negative.
+__device__ __forceinline__ void zero_padding(uint16_t* __restrict__ out, const int32_t* __restrict__ layout, int64_t M,
+                                             int64_t H, int64_t group, int tid) {
+    for (int64_t r = group * kZeroRows; r < min((group + 1) * kZeroRows, M); ++r) {
+        if (layout[r] >= 0) continue;
+        for (int64_t c = tid; c < H / 8; c += 256) *reinterpret_cast<v4u*>(out + r * H + c * 8) = v4u{0, 0, 0, 0};
+    }
+}
+
+// bf16 rows: a thread copies 8 columns of a token into each of its rows; the
+// workgroups behind the copies clear padding.
+__global__ __launch_bounds__(256) void moe_copy_bf16_kernel(const uint16_t* __restrict__ x,
+                                                            const int32_t* __restrict__ rows,
+                                                            const int32_t* __restrict__ layout,
+                                                            uint16_t* __restrict__ out, int64_t T, int k, int64_t H,
+                                                            int64_t M, unsigned copies) {
+    if (blockIdx.x >= copies) return zero_padding(out, layout, M, H, blockIdx.x - copies, threadIdx.x);
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, width = H / 8;
+    if (i >= T * width) return;
+    const int64_t t = i / width, c = i - t * width;
+    const v4u v = *reinterpret_cast<const v4u*>(x + i * 8);
+    for (int j = 0; j < k; ++j) {
+        const int r = rows[t * k + j];
+        if (r >= 0) *reinterpret_cast<v4u*>(out + r * H + c * 8) = v;
+    }
+}
+
+// FP8 rows: eight lanes own one 128-column block of a token, as in the
+// quantizer, and store its line of codes into each of the token's rows.
+template <bool kE8>
+__global__ __launch_bounds__(256) void moe_copy_fp8_kernel(const uint16_t* __restrict__ x,
+                                                           const int32_t* __restrict__ rows, uint8_t* __restrict__ q,
+                                                           void* __restrict__ s, int64_t T, int k, int64_t H) {
+    __shared__ __align__(16) uint8_t lines[32][128];
+    const int64_t KB = H >> 7;
+    const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;
+    const int64_t blk = (int64_t)blockIdx.x * 32 + group;
+    if (blk >= T * KB) return;  // uniform over each 8-lane group
+    const int64_t t = blk / KB, kb = blk - t * KB;
+    float f[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) unpack_bf16(*reinterpret_cast<const v4u*>(x + blk * 128 + 64 * h + 8 * lane), f[h]);
+    const auto scale = block_codes<kE8>(f, lines[group], lane);
+    const v4u codes = *reinterpret_cast<const v4u*>(&lines[group][16 * lane]);
+    for (int j = 0; j < k; ++j) {
+        const int64_t r = rows[t * k + j];
+        if (r < 0) continue;
+        *reinterpret_cast<v4u*>(q + r * H + kb * 128 + 16 * lane) = codes;
+        if (lane == 0) {
+            if constexpr (kE8)
+                static_cast<uint8_t*>(s)[r * ((KB + 3) & ~int64_t(3)) + kb] = (uint8_t)scale;
+            else
+                static_cast<float*>(s)[r * KB + kb] = scale;
+        }
+    }
+}
+
+// int8 rows: one workgroup per token, which reads the row twice (the second
+// time from its cache): the scale needs all of it.
+__global__ __launch_bounds__(256) void moe_copy_int8_kernel(const uint16_t* __restrict__ x,
+                                                            const int32_t* __restrict__ rows, uint8_t* __restrict__ q,
+                                                            float* __restrict__ s, int k, int64_t H) {
+    __shared__ uint32_t tops[4];
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x;
+    uint32_t top = 0;
+    for (int64_t c = tid; c < H / 8; c += 256) {
+        float f[8];
+        unpack_bf16(*reinterpret_cast<const v4u*>(x + t * H + c * 8), f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, magnitude_bits(f[e]));
+    }
+    const Int8Row row(block_max<4>(top, tops, tid));
+    for (int64_t c = tid; c < H / 8; c += 256) {
+        float f[8];
+        unpack_bf16(*reinterpret_cast<const v4u*>(x + t * H + c * 8), f);
+        const v2u codes = row.codes(f);
+        for (int j = 0; j < k; ++j) {
+            const int64_t r = rows[t * k + j];
+            if (r >= 0) *reinterpret_cast<v2u*>(q + r * H + c * 8) = codes;
+        }
+    }
+    for (int j = tid; j < k; j += 256) {
+        const int r = rows[t * k + j];
+        if (r >= 0) s[r] = row.scale;
+    }
+}
+
+static int64_t copy_grid(int64_t T, int64_t H, Held held) {
+    switch (held) {
+        case Held::Bf16: return (T * (H / 8) + 255) / 256;
+        case Held::Int8: return T;
+        default: return (T * (H >> 7) + 31) / 32;
+    }
+}
+
+dg_status dispatch_limits(int64_t T, int64_t H, int64_t M, Held held) {
+    const int64_t zero = held == Held::Bf16 ? (M + kZeroRows - 1) / kZeroRows : 0;
+    return grid_fits(copy_grid(T, H, held) + zero, 256) ? DG_OK : DG_ERR_SHAPE;
+}
+
+dg_status launch_dispatch(const DispatchArgs& a, Held held, hipStream_t stream) {
+    const SortArgs& p = a.sort;
+    const dg_status st = launch_sort(p, stream);
+    if (st != DG_OK) return st;
+    const int64_t copies = copy_grid(p.T, a.H, held);
+    const int64_t zero = held == Held::Bf16 ? (p.M + kZeroRows - 1) / kZeroRows : 0;
+    if (copies + zero == 0) return DG_OK;
+    const dim3 grid((unsigned)(copies + zero)), block(256);
+    uint8_t* const q = static_cast<uint8_t*>(a.out);
+    switch (held) {
+        case Held::Bf16:
+            hipLaunchKernelGGL(moe_copy_bf16_kernel, grid, block, 0, stream, a.x, p.rows, p.layout,
+                               static_cast<uint16_t*>(a.out), p.T, p.k, a.H, p.M, (unsigned)copies);
+            break;
+        case Held::Fp8:
+            hipLaunchKernelGGL(moe_copy_fp8_kernel<false>, grid, block, 0, stream, a.x, p.rows, q, a.s, p.T, p.k, a.H);
+            break;
+        case Held::Fp8E8:
+            hipLaunchKernelGGL(moe_copy_fp8_kernel<true>, grid, block, 0, stream, a.x, p.rows, q, a.s, p.T, p.k, a.H);
+            break;
+        case Held::Int8:
+            hipLaunchKernelGGL(moe_copy_int8_kernel, grid, block, 0, stream, a.x, p.rows, q, static_cast<float*>(a.s),
+                               p.k, a.H);
+            break;
+    }
+    return launched();
+}
+
+// ------------------------------------------------------- the weighted sum back
+
+// A thread adds up 8 columns of a token, eight of its rows in flight at once.
+__global__ __launch_bounds__(256) void moe_unpermute_kernel(const uint16_t* __restrict__ y,
+                                                            const int32_t* __restrict__ rows,
+                                                            const float* __restrict__ weights,
+                                                            uint16_t* __restrict__ out, int64_t T, int k, int64_t H,
+                                                            int64_t M) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, width = H / 8;
+    if (i >= T * width) return;
+    const int64_t t = i / width, c = i - t * width;
+    float sum[8] = {};
+    for (int j0 = 0; j0 < k; j0 += 8) {
+        v4u v[8];
+        float w[8];
+        bool on[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = j0 + j < k ? rows[t * k + j0 + j] : -1;
+            on[j] = r >= 0 && r < M;
+            w[j] = on[j] && weights != nullptr ? weights[t * k + j0 + j] : 1.0f;
+            v[j] = on[j] ? *reinterpret_cast<const v4u*>(y + r * H + c * 8) : v4u{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (!on[j]) continue;
+            float f[8];
+            unpack_bf16(v[j], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(w[j], f[e], sum[e]);
+        }
+    }
+    *reinterpret_cast<v4u*>(out + i * 8) = pack_bf16(sum);
+}
+
+dg_status launch_unpermute(const UnpermuteArgs& a, hipStream_t stream) {
+    const int64_t grid = (a.T * (a.H / 8) + 255) / 256;
+    if (!grid_fits(grid, 256)) return DG_ERR_SHAPE;
+    hipLaunchKernelGGL(moe_unpermute_kernel, dim3((unsigned)grid), dim3(256), 0, stream, a.y, a.rows, a.weights, a.out,
+                       a.T, a.k, a.H, a.M);
+    return launched();
+}
+
+// One workgroup per token and eight of its choices at a time: a thread holds
+// its columns of the gradient, scales them into each row's gradient and keeps
+// the eight dot products.  The workgroups behind the tokens clear padding.
+__global__ __launch_bounds__(256) void moe_unpermute_backward_kernel(
+    const uint16_t* __restrict__ grad, const uint16_t* __restrict__ y, const int32_t* __restrict__ rows,
+    const float* __restrict__ weights, const int32_t* __restrict__ layout, uint16_t* __restrict__ grad_y,
+    float* __restrict__ grad_weights, int64_t T, int k, int64_t H, int64_t M) {
+    __shared__ float parts[4][8];
+    const int tid = threadIdx.x;
+    if (blockIdx.x >= T) return zero_padding(grad_y, layout, M, H, blockIdx.x - T, tid);
+    const int64_t t = blockIdx.x;
+    for (int j0 = 0; j0 < k; j0 += 8) {
+        int64_t r[8];
+        float w[8], dot[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            r[j] = j0 + j < k ? rows[t * k + j0 + j] : -1;
+            if (r[j] >= M) r[j] = -1;
+            w[j] = r[j] >= 0 && weights != nullptr ? weights[t * k + j0 + j] : 1.0f;
+            dot[j] = 0.0f;
+        }
+        for (int64_t c = tid; c < H / 8; c += 256) {
+            float g[8];
+            unpack_bf16(*reinterpret_cast<const v4u*>(grad + t * H + c * 8), g);
+            v4u v[8];
+            if (grad_weights != nullptr) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (r[j] >= 0) v[j] = *reinterpret_cast<const v4u*>(y + r[j] * H + c * 8);
+            }
+            if (grad_y != nullptr) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (r[j] < 0) continue;
+                    float d[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d[e] = w[j] * g[e];
+                    *reinterpret_cast<v4u*>(grad_y + r[j] * H + c * 8) = pack_bf16(d);
+                }
+            }
+            if (grad_weights != nullptr) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (r[j] < 0) continue;
+                    float f[8];
+                    unpack_bf16(v[j], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dot[j] = __builtin_fmaf(g[e], f[e], dot[j]);
+                }
+            }
+        }
+        if (grad_weights != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float sum = wave_sum(dot[j]);
+                if ((tid & 63) == 0) parts[tid >> 6][j] = sum;
+            }
+            __syncthreads();
+            if (tid < 8 && j0 + tid < k)
+                grad_weights[t * k + j0 + tid] = (parts[0][tid] + parts[1][tid]) + (parts[2][tid] + parts[3][tid]);
+            __syncthreads();
+        }
+    }
+}
+
+dg_status launch_unpermute_backward(const UnpermuteBackwardArgs& a, hipStream_t stream) {
+    const int64_t zero = a.grad_y != nullptr && a.layout != nullptr ? (a.M + kZeroRows - 1) / kZeroRows : 0;
+    if (a.T + zero == 0) return DG_OK;
+    if (!grid_fits(a.T + zero, 256)) return DG_ERR_SHAPE;
+    hipLaunchKernelGGL(moe_unpermute_backward_kernel, dim3((unsigned)(a.T + zero)), dim3(256), 0, stream, a.grad, a.y,
+                       a.rows, a.weights, a.layout, a.grad_y, a.grad_weights, a.T, a.k, a.H, a.M);
+    return launched();
+}
+
+// ------------------------------------------------------------------ the gate
+
+// silu(gate) * up of eight columns.
+__device__ __forceinline__ void gate8(const uint16_t* __restrict__ z, int64_t I, float (&h)[8]) {
+    float g[8], u[8];
+    unpack_bf16(*reinterpret_cast<const v4u*>(z), g);
+    unpack_bf16(*reinterpret_cast<const v4u*>(z + I), u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = g[e] / (1.0f + expf(-g[e])) * u[e];
+}
+
+__global__ __launch_bounds__(256) void swiglu_bf16_kernel(const uint16_t* __restrict__ z,
+                                                          const int32_t* __restrict__ layout,
+                                                          uint16_t* __restrict__ h, int64_t M, int64_t I) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, width = I / 8;
+    if (i >= M * width) return;
+    const int64_t r = i / width, c = i - r * width;
+    v4u v = {0, 0, 0, 0};
+    if (layout == nullptr || layout[r] >= 0) {
+        float f[8];
+        gate8(z + r * 2 * I + c * 8, I, f);
+        v = pack_bf16(f);
+    }
+    *reinterpret_cast<v4u*>(h + i * 8) = v;
+}
+
+// Eight lanes per 128-column block of a row, as in the quantizer.
+template <bool kE8>
+__global__ __launch_bounds__(256) void swiglu_fp8_kernel(const uint16_t* __restrict__ z,
+                                                         const int32_t* __restrict__ layout, uint8_t* __restrict__ q,
+                                                         void* __restrict__ s, int64_t M, int64_t I) {
+    __shared__ __align__(16) uint8_t lines[32][128];
+    const int64_t KB = I >> 7;
+    const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;
+    const int64_t blk = (int64_t)blockIdx.x * 32 + group;
+    if (blk >= M * KB) return;  // uniform over each 8-lane group, as is the next
+    const int64_t r = blk / KB, kb = blk - r * KB;
+    if (layout != nullptr && layout[r] < 0) return;
+    float f[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) gate8(z + r * 2 * I + kb * 128 + 64 * h + 8 * lane, I, f[h]);
+    const auto scale = block_codes<kE8>(f, lines[group], lane);
+    *reinterpret_cast<v4u*>(q + blk * 128 + 16 * lane) = *reinterpret_cast<const v4u*>(&lines[group][16 * lane]);
+    if (lane == 0) {
+        if constexpr (kE8)
+            static_cast<uint8_t*>(s)[r * ((KB + 3) & ~int64_t(3)) + kb] = (uint8_t)scale;
+        else
+            static_cast<float*>(s)[blk] = scale;
+    }
+}
+
+// One workgroup per row: the scale needs all of it, so the gate is computed
+// twice, the second time from the cache.
+__global__ __launch_bounds__(256) void swiglu_int8_kernel(const uint16_t* __restrict__ z,
+                                                          const int32_t* __restrict__ layout, uint8_t* __restrict__ q,
+                                                          float* __restrict__ s, int64_t I) {
+    __shared__ uint32_t tops[4];
+    const int64_t r = blockIdx.x;
+    if (layout != nullptr && layout[r] < 0) return;
+    const int tid = threadIdx.x;
+    uint32_t top = 0;
+    for (int64_t c = tid; c < I / 8; c += 256) {
+        float f[8];
+        gate8(z + r * 2 * I + c * 8, I, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, magnitude_bits(f[e]));
+    }
+    const Int8Row row(block_max<4>(top, tops, tid));
+    for (int64_t c = tid; c < I / 8; c += 256) {
+        float f[8];
+        gate8(z + r * 2 * I + c * 8, I, f);
+        *reinterpret_cast<v2u*>(q + r * I + c * 8) = row.codes(f);
+    }
+    if (tid == 0) s[r] = row.scale;
+}
+
+dg_status launch_swiglu(const SwigluArgs& a, Held held, hipStream_t stream) {
+    const int64_t grid = held == Held::Bf16   ? (a.M * (a.I / 8) + 255) / 256
+                         : held == Held::Int8 ? a.M
+                                              : (a.M * (a.I >> 7) + 31) / 32;
+    if (!grid_fits(grid, 256)) return DG_ERR_SHAPE;
+    const dim3 blocks((unsigned)grid), threads(256);
+    uint8_t* const q = static_cast<uint8_t*>(a.out);
+    switch (held) {
+        case Held::Bf16:
+            hipLaunchKernelGGL(swiglu_bf16_kernel, blocks, threads, 0, stream, a.z, a.layout,
+                               static_cast<uint16_t*>(a.out), a.M, a.I);
+            break;
+        case Held::Fp8:
+            hipLaunchKernelGGL(swiglu_fp8_kernel<false>, blocks, threads, 0, stream, a.z, a.layout, q, a.s, a.M, a.I);
+            break;
+        case Held::Fp8E8:
+            hipLaunchKernelGGL(swiglu_fp8_kernel<true>, blocks, threads, 0, stream, a.z, a.layout, q, a.s, a.M, a.I);
+            break;
+        case Held::Int8:
+            hipLaunchKernelGGL(swiglu_int8_kernel, blocks, threads, 0, stream, a.z, a.layout, q,
+                               static_cast<float*>(a.s), a.I);
+            break;
+    }
+    return launched();
+}
+
+// Both gradients of eight columns, from the gate recomputed.
+__global__ __launch_bounds__(256) void swiglu_backward_kernel(const uint16_t* __restrict__ z,
+                                                              const uint16_t* __restrict__ grad_h,
+                                                              const int32_t* __restrict__ layout,
+                                                              uint16_t* __restrict__ grad_z, int64_t M, int64_t I) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, width = I / 8;
+    if (i >= M * width) return;
+    const int64_t r = i / width, c = i - r * width, at = r * 2 * I + c * 8;
+    v4u to_g = {0, 0, 0, 0}, to_u = {0, 0, 0, 0};
+    if (layout == nullptr || layout[r] >= 0) {
+        float g[8], u[8], d[8];
+        unpack_bf16(*reinterpret_cast<const v4u*>(z + at), g);
+        unpack_bf16(*reinterpret_cast<const v4u*>(z + at + I), u);
+        unpack_bf16(*reinterpret_cast<const v4u*>(grad_h + i * 8), d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float p = 1.0f / (1.0f + expf(-g[e])), silu = g[e] * p;
+            const float slope = p * (1.0f + g[e] * (1.0f - p));
+            g[e] = d[e] * u[e] * slope;
+            u[e] = d[e] * silu;
+        }
+        to_g = pack_bf16(g);
+        to_u = pack_bf16(u);
+    }
+    *reinterpret_cast<v4u*>(grad_z + at) = to_g;
+    *reinterpret_cast<v4u*>(grad_z + at + I) = to_u;
+}
+
+dg_status launch_swiglu_backward(const SwigluBackwardArgs& a, hipStream_t stream) {
+    const int64_t grid = (a.M * (a.I / 8) + 255) / 256;
+    if (!grid_fits(grid, 256)) return DG_ERR_SHAPE;
+    hipLaunchKernelGGL(swiglu_backward_kernel, dim3((unsigned)grid), dim3(256), 0, stream, a.z, a.grad_h, a.layout,
+                       a.grad_z, a.M, a.I);
+    return launched();
+}
+
+}  // namespace dg

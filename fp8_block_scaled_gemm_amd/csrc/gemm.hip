@@ -33,66 +33,15 @@
 //     time, so that concurrent tiles on one XCD share A and B slabs in its L2.
 #include "device_common.h"
 #include "launch.h"
+#include "tiles.h"
 #include "wave_ops.h"
 
 #include <algorithm>
-#include <atomic>
 #include <cstdlib>
 #include <cstring>
 #include <type_traits>
 
 namespace dg {
-
-constexpr int kNumXcds = 8;
-
-
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int GROUP_M_>
-struct TileConfig {
-    static constexpr int BM = BM_, BN = BN_;
-    static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
-    static constexpr int kWaves = WAVES_M * WAVES_N;
-    static constexpr int kThreads = 64 * kWaves;
-    static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;  // rows / cols per wave
-    static constexpr int TM = WM / 16, TN = WN / 16;            // 16x16 sub-tiles per wave
-    static constexpr int kGroupM = GROUP_M_;                    // m-blocks per raster group
-    // one wave-wide direct load fills 1 KiB (8 rows) of a stage; waves take
-    // the 8-row groups round-robin (the B slab may end part way round)
-    static constexpr int kLoadsA = BM / 8 / kWaves;
-    static constexpr int kLoadsB = (BN / 8 + kWaves - 1) / kWaves;
-    static constexpr int kLoadsBMin = BN / 8 / kWaves;  // loads of the wave with the fewest
-    static constexpr int kStageA = BM * 128;
-    static constexpr int kStageB = BN * 128;
-    // every wave's columns lie in one 128-column scale block
-    static constexpr bool kOneScaleB = BN % 128 == 0 && 128 % WN == 0;
-    // LDS row pitch of the bf16 output tile: a power of two of 16-byte
-    // chunks, at least 16, so the chunk swizzle c ^ (row & 15) stays in the row
-    static constexpr int kPitchChunks = BN <= 128 ? 16 : 32;
-    // the bf16 output tile reuses the stage memory on its way out
-    static constexpr int kSmem = (2 * (kStageA + kStageB) > BM * kPitchChunks * 16)
-                                     ? 2 * (kStageA + kStageB)
-                                     : BM * kPitchChunks * 16;
-    static_assert(WM % 16 == 0 && WN % 16 == 0, "wave tile must be a multiple of 16x16");
-    static_assert(BM % (8 * kWaves) == 0 && BN % 8 == 0, "slabs are staged 8 rows at a time");
-    static_assert(BN <= 256, "output tile pitch");
-    static_assert(BM % 64 == 0 && kWaves % (BM / 64) == 0, "waves stage the A scales 64 rows each");
-};
-
-// Logical tile of workgroup `b` among `tiles`: XCD x (= b % 8) receives the
-// contiguous range [x*per, (x+1)*per); -1 for the padding slots.
-__device__ __forceinline__ int xcd_tile(int b, int tiles) {
-    const int per = (tiles + kNumXcds - 1) / kNumXcds;
-    const int t = (b % kNumXcds) * per + b / kNumXcds;
-    return t < tiles ? t : -1;
-}
-
-// Where one output tile lives.  Every field is wave-uniform.
-struct TileInfo {
-    int g;              // group (0 for dense)
-    int m0, n0;         // first row within the group's row space, first column
-    int valid;          // tile rows [0, valid) exist and may be routed
-    int64_t arow0;      // A / sa / D row of tile row 0
-    uint64_t ok0, ok1;  // contiguous form: routed-row masks, tile rows 0-63 / 64-127
-};
 
 // Masked form: work units are (group, m-block) pairs times n-blocks; a
 // pair's cost is the number of 64-row chunks of its m-block that hold valid
@@ -145,24 +94,6 @@ __device__ __forceinline__ bool masked_slot(int b, int m_blocks, int n_blocks, i
         pos -= n;
     }
     return false;
-}
-
-// Contiguous form: the largest valid group id below `below` among the rows
-// of the 128-row block at ti.m0 and the masks of the rows carrying it; false
-// when there is none.  Every wave computes this from the layout itself.
-__device__ __forceinline__ bool block_group(const int32_t* __restrict__ layout, int64_t G, int below,
-                                            int lane, TileInfo& ti) {
-    const int id0 = layout[ti.m0 + lane], id1 = layout[ti.m0 + 64 + lane];
-    auto usable = [&](int id) { return id >= 0 && id < G && id < below; };
-    int gid = max(usable(id0) ? id0 : -1, usable(id1) ? id1 : -1);
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) gid = max(gid, __shfl_xor(gid, d, 64));
-    gid = __builtin_amdgcn_readfirstlane(gid);
-    if (gid < 0) return false;
-    ti.g = gid;
-    ti.ok0 = __ballot(id0 == gid);
-    ti.ok1 = __ballot(id1 == gid);
-    return true;
 }
 
 // Decode workgroup `b`'s tile; false when it is a padding slot or the tile
@@ -406,44 +337,15 @@ __device__ __forceinline__ void store_tile(v4f (&acc)[T::TM][T::TN], uint8_t* sm
                 for (int j = 0; j < T::TN; ++j) acc[h * kH + ii][j] += c[ii][j];
         }
     }
-    // Round to bf16 (v_cvt_pk_bf16_f32: nearest even), stage the whole tile
-    // in LDS, then write it back in full 16-byte chunks, consecutive lanes on
-    // consecutive chunks of a row.  In LDS (row pitch kPitchChunks chunks),
-    // 16-byte chunk c of row r sits at c ^ (r & 15): the 16 rows a fragment
-    // store touches land in distinct banks.
-    constexpr int kRowBytes = T::kPitchChunks * 16;
-    constexpr int kChunks = T::BN / 8;  // 16-byte chunks of an output row
-    uint8_t* const sD = smem;
+    // Round to bf16 (v_cvt_pk_bf16_f32: nearest even) and stage the whole tile
 #pragma unroll
     for (int i = 0; i < T::TM; ++i) {
         const int row = 16 * (T::WAVES_M * i + wm) + lr;
 #pragma unroll
-        for (int j = 0; j < T::TN; ++j) {
-            const int col = wcol + 16 * j + 4 * lg;
-            const v2f lo = {acc[i][j][0], acc[i][j][1]};
-            const v2f hi = {acc[i][j][2], acc[i][j][3]};
-            v2u packed;
-            packed[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector(lo, v2bf));
-            packed[1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, v2bf));
-            *reinterpret_cast<v2u*>(sD + row * kRowBytes + (((col >> 3) ^ (row & 15)) << 4) +
-                                    ((col >> 2) & 1) * 8) = packed;
-        }
+        for (int j = 0; j < T::TN; ++j) stage_bf16<T>(smem, row, wcol + 16 * j + 4 * lg, acc[i][j]);
     }
     __syncthreads();
-    static_assert((T::BM * kChunks) % T::kThreads == 0, "whole passes over the output tile");
-    // fully unrolled (the accumulators are dead by now): every pass's LDS
-    // read can be in flight before the first store waits for its data
-#pragma unroll
-    for (int q = tid; q < T::BM * kChunks; q += T::kThreads) {
-        const int row = q / kChunks, c = q % kChunks;
-        const int64_t col = ti.n0 + c * 8;
-        bool ok = row < ti.valid && col < N;
-        if (kForm == Form::Contiguous) ok = ok && (((row < 64 ? ti.ok0 : ti.ok1) >> (row & 63)) & 1);
-        const v4u v = *reinterpret_cast<const v4u*>(sD + row * kRowBytes + ((c ^ (row & 15)) << 4));
-        // D is written once and not read back here: non-temporal stores keep
-        // it from evicting operand slabs that later tiles still read
-        if (ok) __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(D + (ti.arow0 + row) * N + col));
-    }
+    store_staged<T, kForm == Form::Contiguous>(smem, tid, ti, D, N);
 }
 
 // Operands are separate __restrict__ arguments so the compiler knows they
@@ -803,25 +705,6 @@ using TileNarrow32 = TileConfig<128, 32, 2, 2, 8>;
 // short groups finish early and stop drawing on HBM while the full slabs
 // still stream; full tiles run the branch-free loop.
 using TileMasked = TileConfig<256, 256, 2, 4, 4>;
-
-// Compute units of the current device, cached per device.  Host threads may
-// launch concurrently: each slot only ever receives its device's one value,
-// so relaxed atomics suffice.
-static int device_cus() {
-    static std::atomic<int> cached[64] = {};
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess) dev = 0;
-    const bool slot = dev >= 0 && dev < 64;
-    if (slot) {
-        const int c = cached[dev].load(std::memory_order_relaxed);
-        if (c > 0) return c;
-    }
-    int n = 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
-        n = 256;
-    if (slot) cached[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
 
 // DG_FP8_DENSE_TILE=256x256|256x224|256x192|256x160|128x256|128x128|128x64|128x32|256x256t pins the dense tile
 // shape (for tests and tuning; read at every call); -1 when unset or not

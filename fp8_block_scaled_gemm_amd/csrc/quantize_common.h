@@ -2,6 +2,8 @@
 // the way: correctly rounded x / scale and the power-of-two exponent.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 
 namespace dg {
@@ -28,5 +30,36 @@ __device__ __forceinline__ int e8m0_exponent(float amax) {
 
 // 2^-e as an fp32 bit pattern (a normal number for e in [-127, 126]).
 __device__ __forceinline__ float exp2_neg(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
+
+// Codes of four hidden values in a block whose largest magnitude has the bits
+// `top` (a NaN's are the largest), and the block's scale or exponent byte: the
+// per-token quantizer's recipe, with a NaN scale for a block that is not finite.
+template <bool kE8>
+__device__ __forceinline__ typename std::conditional<kE8, int, float>::type quantize_hidden(
+    uint32_t top, const v4f& v, uint32_t& codes) {
+    const float a = __uint_as_float(top);
+    const bool finite = top < 0x7f800000u;
+    float d[4];
+    if constexpr (kE8) {
+        const int ex = e8m0_exponent(a);
+        const float y = exp2_neg(finite ? ex : 0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) d[q] = v[q] * y;
+        codes = e4m3x4_hw(d[0], d[1], d[2], d[3]);
+        return finite ? ex + 127 : 255;
+    } else {
+        const float scale = a / 448.0f, y = 1.0f / scale;
+        const bool fast = scale >= 1.17549435e-38f && y <= 3.40282347e38f;
+        if (fast) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[q] = quotient_rn(v[q], scale, y);
+        } else {  // a scale below the normal range; a branch, not four divisions everywhere
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[q] = v[q] / scale;
+        }
+        codes = top != 0 ? e4m3x4_hw(d[0], d[1], d[2], d[3]) : 0u;
+        return finite ? scale : __builtin_nanf("");
+    }
+}
 
 }  // namespace dg

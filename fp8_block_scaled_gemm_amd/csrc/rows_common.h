@@ -1,0 +1,94 @@
+// Rows of bf16 activations in registers, and the int8 recipe of a row, shared
+// by the kernels that quantize rows on the way.
+#pragma once
+
+#include "quantize_common.h"
+#include "wave_ops.h"
+
+namespace dg {
+
+// Eight bf16 in four words, the lower half of a word first, and back, rounded
+// to nearest even.  A bf16 is the upper half of its fp32.
+__device__ __forceinline__ void unpack_bf16(const v4u& raw, float (&f)[8]) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        f[2 * w] = __uint_as_float(raw[w] << 16);
+        f[2 * w + 1] = __uint_as_float(raw[w] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ v4u pack_bf16(const float (&f)[8]) {
+    v4u r;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+        r[w] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{f[2 * w], f[2 * w + 1]}), v2bf));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// The scale of an int8 row whose largest magnitude has the bits `top` (a NaN's
+// are the largest), and its codes, four to a word.
+struct Int8Row {
+    float scale, inverse;
+    bool fast, zero;
+    __device__ __forceinline__ explicit Int8Row(uint32_t top) {
+        scale = __uint_as_float(top) / 127.0f;
+        inverse = 1.0f / scale;
+        fast = scale >= 1.17549435e-38f && inverse <= 3.40282347e38f;
+        zero = scale == 0.0f || top >= 0x7f800000u;
+        if (top >= 0x7f800000u) scale = __builtin_nanf("");
+    }
+    __device__ __forceinline__ uint32_t code(float v) const {
+        // correctly rounded quotient, then the nearest integer, ties to even; a
+        // scale below the normal range is coarse, and a quotient may pass 127
+        const float d = fast ? quotient_rn(v, scale, inverse) : v / scale;
+        const int q = zero ? 0 : (int)__builtin_rintf(__builtin_amdgcn_fmed3f(d, -127.0f, 127.0f));
+        return (uint32_t)q & 0xffu;
+    }
+    __device__ __forceinline__ v2u codes(const float (&f)[8]) const {
+        v2u r;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+            r[w] = code(f[4 * w]) | code(f[4 * w + 1]) << 8 | code(f[4 * w + 2]) << 16 | code(f[4 * w + 3]) << 24;
+        return r;
+    }
+};
+
+// The largest of a workgroup's values, in every thread.
+template <int kWaves>
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* lds, int tid) {
+    v = wave_max(v);
+    if ((tid & 63) == 0) lds[tid >> 6] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v = max(v, lds[w]);
+    __syncthreads();
+    return v;
+}
+
+// Codes of a 128-column block that eight lanes hold, lane l its columns 8l ..
+// 8l+7 and 64+8l .. 64+8l+7: the block's scale (kE8: exponent byte, in every
+// lane) and, in `line` (LDS, the group's own 128 bytes), the codes in order.
+// The lanes are in one wave, whose LDS accesses are ordered: no barrier.
+template <bool kE8>
+__device__ __forceinline__ auto block_codes(const float (&f)[2][8], uint8_t* line, int lane) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, magnitude_bits(f[h][e]));
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 8));
+    typename std::conditional<kE8, int, float>::type scale;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t lo, hi;
+        scale = quantize_hidden<kE8>(top, v4f{f[h][0], f[h][1], f[h][2], f[h][3]}, lo);
+        quantize_hidden<kE8>(top, v4f{f[h][4], f[h][5], f[h][6], f[h][7]}, hi);
+        *reinterpret_cast<v2u*>(line + 64 * h + 8 * lane) = v2u{lo, hi};
+    }
+    wave_sync();
+    return scale;
+}
+
+}  // namespace dg
