@@ -10,6 +10,7 @@ import numpy as np
 from tests.ops_ref import BF16, FP32, e4m3_step, e4m3_value
 
 BF16_TINY = 2.0 ** -134  # half a step of the smallest bf16
+SILU_TINY = 1.05e-36     # see swiglu
 
 
 def bf16_error(v):
@@ -77,12 +78,14 @@ def sigmoid(g):
 
 def swiglu(z):
     """(h, bound on fp32 arithmetic): the exponential's own error, a sum, a
-    quotient and a product, each a rounding or two; where the exponential
-    overflows fp32 (gate below -88) the kernel's 0 is off by silu itself."""
+    quotient and a product, each a rounding or two.  A sigmoid below the smallest
+    normal fp32, 2^-126, may come as 0: there the gate is below -87.3, and where it
+    is below -88.8 silu itself is smaller than what that gives, so that the error
+    is at most 88.8 * 2^-126 = 1.05e-36 times |up|."""
     I = z.shape[1] // 2
     g, u = z[:, :I], z[:, I:]
     h = g * sigmoid(g) * u
-    return h, 8 * FP32 * np.abs(h) + 3e-37 * np.abs(u) + 2.0 ** -149
+    return h, 8 * FP32 * np.abs(h) + SILU_TINY * np.abs(u) + 2.0 ** -149
 
 
 def swiglu_backward(z, d):
@@ -91,7 +94,7 @@ def swiglu_backward(z, d):
     g, u, p = z[:, :I], z[:, I:], sigmoid(z[:, :I])
     out = np.concatenate((d * u * p * (1 + g * (1 - p)), d * g * p), 1)
     off = np.concatenate((np.abs(d * u) * (p * (8 * np.abs(g) + 16) * FP32 + 1e-35),
-                          np.abs(d) * (12 * FP32 * np.abs(g * p) + 3e-37)), 1) + 2.0 ** -149
+                          np.abs(d) * (12 * FP32 * np.abs(g * p) + SILU_TINY)), 1) + 2.0 ** -149
     return out, off + bf16_error(np.abs(out) + off)
 
 

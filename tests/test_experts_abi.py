@@ -106,6 +106,8 @@ def test_dispatch_refusals(lib, name):
         assert call(**{n: FAKE + 4}) == DG_ERR_ALIGN, n
     # copies past the work-items of one grid: refused before the sort is enqueued
     assert call(T=1 << 24, k=64, H=(1 << 24) - 128, E=1) == DG_ERR_SHAPE
+    if name == "dg_moe_dispatch":
+        assert call(T=4096, k=1, H=(1 << 24) - 128, E=1) == DG_ERR_SHAPE
 
 
 def test_unpermute_refusals(lib):
@@ -163,12 +165,13 @@ def test_int8_refusals(lib):
         return lib.dg_int8_gemm_grouped_contiguous(*[at.get(n, FAKE) for n in names + ("layout",)], M, N, K, G, None)
     for call in (dense, grouped):
         for bad in (dict(M=-1), dict(M=1 << 31), dict(N=0), dict(N=12), dict(N=1 << 31), dict(K=0), dict(K=100),
-                    dict(K=1 << 17), dict(M=(1 << 31) - 128, N=1 << 30)):
+                    dict(K=1 << 17)):
             assert call(**bad) == DG_ERR_SHAPE, bad
         for n in names:
             assert call(**{n: None}) == DG_ERR_NULL, n
             assert call(**{n: FAKE + 4}) == DG_ERR_ALIGN, n
         assert call(M=0, **{n: None for n in names}) == DG_OK
+    assert dense(M=(1 << 31) - 128, N=1 << 30) == DG_ERR_SHAPE  # more tiles than a grid holds
     for bad in (dict(M=130), dict(G=0), dict(G=1 << 31)):
         assert grouped(**bad) == DG_ERR_SHAPE, bad
     assert grouped(layout=None) == DG_ERR_NULL and grouped(layout=FAKE + 8) == DG_ERR_ALIGN
