@@ -17,21 +17,29 @@ namespace dg {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 
-// The tile kernel.  Four waves, one to a SIMD, as 2 x 2 over a BM x BN tile, so
-// that a wave may hold 512 registers: 128 x 128 sums of a 256 x 256 tile, and
-// two sets of fragments.  A K block is 128 bytes a row, loaded straight from
-// memory into one of S stages of LDS, 16-byte chunk c of row r at c ^ (r & 7).
-// Lane (lr, lg) of a fragment read takes chunk lg (the block's first half) or
-// lg + 4 (its second) of row lr, which is one operand of
-// v_mfma_i32_16x16x64_i8: which 64 of the block's 128 values an instruction
-// takes is free, as A and B agree.  B goes first, so that a lane owns one
-// output row and four consecutive columns of a sub-tile.
+// A tile.  A K block is 128 bytes a row, loaded straight from memory into one
+// of S stages of LDS, 16-byte chunk c of row r at c ^ (r & 7).  Lane (lr, lg) of
+// a fragment read takes chunk lg (the block's first half) or lg + 4 (its second)
+// of row lr, which is one operand of v_mfma_i32_16x16x64_i8: which 64 of the
+// block's 128 values an instruction takes is free, as A and B agree.  B goes
+// first, so that a lane owns one output row and four consecutive columns of a
+// sub-tile.
 //
 // A block takes two phases of TM TN products each.  The first multiplies the
 // first halves, while the second halves' fragments are read; it ends with the
 // block's only barrier, behind which its stage is free and the next block's has
 // landed.  The second multiplies those, while the next block's first halves are
 // read and the block S ahead is loaded.
+//
+// 256 x 256 in 8 waves: 1.38 us a K block where the products alone (no loads, no
+// reads) take 1.05, and 11 us for a tile's beginning, its end and the launch, of
+// which the stores of one round of tiles, 34 MB, are 5.  4096 x 7168 x 2048:
+// 55 us, 2190 TOPS; 8192^3: 374 us, 2940 (the library's int8 product: 73 and 530
+// us on this card).  Tried: the FP8 kernel's two barriers a block (59.7 us);
+// four waves of 128 x 128 with 512 registers each, whose sums the compiler moves
+// about (78); 32 x 32 x 32 products (64); the loads at the second phase's
+// beginning instead of spread over it (59-60); a barrier in the middle of the
+// first phase for earlier loads (62).
 template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int S_, int GROUP_M_>
 struct Int8Tile {
     static constexpr int BM = BM_, BN = BN_, S = S_;
@@ -50,191 +58,272 @@ struct Int8Tile {
     static_assert(kSmem <= 160 * 1024 && kLoads * (S - 1) < 64, "LDS, vmcnt range");
 };
 
-template <class T, bool kGrouped>
-__global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_gemm_kernel(
-    const uint8_t* __restrict__ A, const float* __restrict__ sa, const uint8_t* __restrict__ B,
-    const float* __restrict__ sb, uint16_t* __restrict__ D, const int32_t* __restrict__ layout, int64_t rows, int64_t N,
-    int64_t K, int64_t G, int m_blocks, int n_blocks) {
-    extern __shared__ __align__(1024) uint8_t smem[];
-    const int tid = threadIdx.x;
+struct Int8Operands {
+    const uint8_t* A;
+    const float* sa;
+    const uint8_t* B;
+    const float* sb;
+    uint16_t* D;
+    int64_t N, K;
+};
+
+// The tile at ti, all threads of the workgroup; kRouted: only the rows of ti's
+// masks are stored.  LDS is free again when every wave has come back.
+template <class T, bool kRouted>
+__device__ __forceinline__ void int8_tile(const Int8Operands& p, const TileInfo& ti, uint8_t* smem, int tid) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lane = tid & 63;
+    const uint32_t K = (uint32_t)p.K;  // below 2^17: a tile's rows are addressed with 32-bit offsets
     const int KB = (int)(K >> 7);
     const int lr = lane & 15, lg = lane >> 4;
     const int wrow = wave / T::WAVES_N * T::WM, wcol = wave % T::WAVES_N * T::WN;
     const int sub = lane >> 3, lchunk = (lane & 7) ^ sub;
-    const uint32_t offRow = (uint32_t)(wave * 8 + sub) * (uint32_t)K + lchunk * 16;
+    const uint32_t offRow = (uint32_t)(wave * 8 + sub) * K + lchunk * 16;
     const int chunk_lo = (lg ^ (lr & 7)) << 4, chunk_hi = chunk_lo ^ 64;
     const int fragA = (wrow + lr) * 128, fragB = T::BM * 128 + (wcol + lr) * 128;
-
-    TileInfo ti;
-    ti.ok0 = ti.ok1 = 0;
-    ti.g = 0;
-    auto compute = [&]() __attribute__((always_inline)) {
-        const int vn = (int)min<int64_t>(T::BN, N - ti.n0);
-        const uint8_t* tileA = A + ti.arow0 * K;
-        const uint8_t* tileB = B + ((int64_t)ti.g * N + ti.n0) * K;
-        // a wave's load q of block kb: rows [8 (wave + kWaves q), +8) of A, then of B;
-        // blocks past the last one get an empty buffer, and so count like the others
-        auto issue = [&](int kb, int st, int q0, int q1) __attribute__((always_inline)) {
-            const v4u ra = buffer_rsrc(tileA + kb * 128, kb < KB ? (uint32_t)ti.valid * (uint32_t)K - kb * 128 : 0u);
-            const v4u rb = buffer_rsrc(tileB + kb * 128, kb < KB ? (uint32_t)vn * (uint32_t)K - kb * 128 : 0u);
-            uint8_t* const to = smem + st * T::kStage + wave * 1024;
-            constexpr int kRows = 8 * T::kWaves;  // of a load of every wave
+    const int vn = (int)min<int64_t>(T::BN, p.N - ti.n0);
+    const uint8_t* const tileA = p.A + ti.arow0 * p.K;
+    const uint8_t* const tileB = p.B + ((int64_t)ti.g * p.N + ti.n0) * p.K;
+    // a wave's loads [q0, q1) of block kb: rows [8 (wave + kWaves q), +8) of A,
+    // then of B; blocks past the last one get an empty buffer, and so count like
+    // the others
+    auto issue = [&](int kb, int st, int q0, int q1) __attribute__((always_inline)) {
+        const v4u ra = buffer_rsrc(tileA + kb * 128, kb < KB ? (uint32_t)ti.valid * K - kb * 128 : 0u);
+        const v4u rb = buffer_rsrc(tileB + kb * 128, kb < KB ? (uint32_t)vn * K - kb * 128 : 0u);
+        uint8_t* const to = smem + st * T::kStage + wave * 1024;
+        constexpr int kRows = 8 * T::kWaves;  // of a load of every wave
 #pragma unroll
-            for (int q = q0; q < q1; ++q) {
-                if (q < T::kLoadsA)
-                    load_lds_16(ra, offRow + (uint32_t)(q * kRows) * (uint32_t)K, to + q * kRows * 128);
-                else if (!T::kUneven || wave + (q - T::kLoadsA) * T::kWaves < T::BN / 8)
-                    load_lds_16(rb, offRow + (uint32_t)((q - T::kLoadsA) * kRows) * (uint32_t)K, to + q * kRows * 128);
-            }
-        };
-        v4i acc[T::TM][T::TN];
-#pragma unroll
-        for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-            for (int j = 0; j < T::TN; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-        v4i a[2][T::TM], b[2][T::TN];
-        auto read_b = [&](const uint8_t* st, int chunk, int set, int j) __attribute__((always_inline)) {
-            b[set][j] = *reinterpret_cast<const v4i*>(st + fragB + j * 2048 + chunk);
-        };
-        auto read_a = [&](const uint8_t* st, int chunk, int set, int i) __attribute__((always_inline)) {
-            a[set][i] = *reinterpret_cast<const v4i*>(st + fragA + i * 2048 + chunk);
-        };
-        // the products of one set, a row of sub-tiles at a time, with the next
-        // set's reads (and, kLoad, the loads of a block) between them
-        auto phase = [&](auto which, const uint8_t* next, int chunk, auto load, int kb, int st) __attribute__((always_inline)) {
-            constexpr int set = decltype(which)::value;
-            constexpr bool kLoad = decltype(load)::value;
-            constexpr int kRead = (T::TN + T::TM + T::TM - 1) / T::TM;  // reads a row
-            constexpr int kEach = (T::kLoads + T::TM - 1) / T::TM;
-#pragma unroll
-            for (int i = 0; i < T::TM; ++i) {
-#pragma unroll
-                for (int r = i * kRead; r < (i + 1) * kRead; ++r) {
-                    if (r < T::TN)
-                        read_b(next, chunk, set ^ 1, r);
-                    else if (r < T::TN + T::TM)
-                        read_a(next, chunk, set ^ 1, r - T::TN);
-                }
-                if constexpr (kLoad) issue(kb, st, i * kEach, min((i + 1) * kEach, T::kLoads));
-#pragma unroll
-                for (int j = 0; j < T::TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[set][j], a[set][i], acc[i][j], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        };
-        using std::integral_constant;
-        using First = integral_constant<int, 0>;
-        using Second = integral_constant<int, 1>;
-
-#pragma unroll
-        for (int s = 0; s < T::S; ++s) issue(s, s, 0, T::kLoads);
-        wait_vmcnt<T::kUneven ? 0 : T::kLoads*(T::S - 1)>();
-        lds_barrier();
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) read_b(smem, chunk_lo, 0, j);
-#pragma unroll
-        for (int i = 0; i < T::TM; ++i) read_a(smem, chunk_lo, 0, i);
-        int st = 0;
-        for (int kb = 0; kb < KB; ++kb) {
-            const int nx = st + 1 == T::S ? 0 : st + 1;
-            phase(First{}, smem + st * T::kStage, chunk_hi, std::false_type{}, 0, 0);
-            wait_vmcnt_lgkm0<T::kLoads*(T::S - 2)>();  // the stage has been read, the next block's has landed
-            lds_barrier();
-            phase(Second{}, smem + nx * T::kStage, chunk_lo, std::true_type{}, kb + T::S, st);
-            st = nx;
+        for (int q = q0; q < q1; ++q) {
+            if (q < T::kLoadsA)
+                load_lds_16(ra, offRow + (uint32_t)(q * kRows) * K, to + q * kRows * 128);
+            else if (!T::kUneven || wave + (q - T::kLoadsA) * T::kWaves < T::BN / 8)
+                load_lds_16(rb, offRow + (uint32_t)((q - T::kLoadsA) * kRows) * K, to + q * kRows * 128);
         }
-        wait_vmcnt_lgkm0<0>();  // the empty loads of the last blocks have retired
-        lds_barrier();
-
-        // epilogue: scales by row and column, rounding, and out through LDS
-        v4f col_scale[T::TN];
+    };
+    v4i acc[T::TM][T::TN];
 #pragma unroll
-        for (int j = 0; j < T::TN; ++j) {
-            const int64_t col = min<int64_t>(ti.n0 + wcol + 16 * j + 4 * lg, N - 4);
-            col_scale[j] = *reinterpret_cast<const v4f*>(sb + (int64_t)ti.g * N + col);
-        }
+    for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+    v4i a[2][T::TM], b[2][T::TN];
+    auto read_b = [&](const uint8_t* st, int chunk, int set, int j) __attribute__((always_inline)) {
+        b[set][j] = *reinterpret_cast<const v4i*>(st + fragB + j * 2048 + chunk);
+    };
+    auto read_a = [&](const uint8_t* st, int chunk, int set, int i) __attribute__((always_inline)) {
+        a[set][i] = *reinterpret_cast<const v4i*>(st + fragA + i * 2048 + chunk);
+    };
+    // the products of one set, a row of sub-tiles at a time, with the next
+    // set's reads (and, kLoad, the loads of a block) between them
+    auto phase = [&](auto which, const uint8_t* next, int chunk, auto load, int kb, int st) __attribute__((always_inline)) {
+        constexpr int set = decltype(which)::value;
+        constexpr bool kLoad = decltype(load)::value;
+        constexpr int kRead = (T::TN + T::TM + T::TM - 1) / T::TM;  // reads a row
+        constexpr int kEach = (T::kLoads + T::TM - 1) / T::TM;
 #pragma unroll
         for (int i = 0; i < T::TM; ++i) {
-            const int row = wrow + 16 * i + lr;
-            const float row_scale = sa[ti.arow0 + min(row, ti.valid - 1)];
 #pragma unroll
-            for (int j = 0; j < T::TN; ++j) {
-                v4f v;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = (row_scale * col_scale[j][q]) * (float)acc[i][j][q];
-                stage_bf16<T>(smem, row, wcol + 16 * j + 4 * lg, v);
+            for (int r = i * kRead; r < (i + 1) * kRead; ++r) {
+                if (r < T::TN)
+                    read_b(next, chunk, set ^ 1, r);
+                else if (r < T::TN + T::TM)
+                    read_a(next, chunk, set ^ 1, r - T::TN);
             }
+            if constexpr (kLoad) issue(kb, st, min(i * kEach, T::kLoads), min((i + 1) * kEach, T::kLoads));
+#pragma unroll
+            for (int j = 0; j < T::TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[set][j], a[set][i], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __syncthreads();
-        store_staged<T, kGrouped>(smem, tid, ti, D, N);
     };
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, 1>;
 
-    if constexpr (!kGrouped) {
-        const int tile = xcd_tile(blockIdx.x, m_blocks * n_blocks);
-        if (tile < 0) return;
-        const int span = T::kGroupM * n_blocks;
-        const int first_m = (tile / span) * T::kGroupM;
-        const int gm = min(m_blocks - first_m, T::kGroupM);
-        const int in_span = tile % span;
-        ti.m0 = (first_m + in_span % gm) * T::BM;
-        ti.n0 = (in_span / gm) * T::BN;
-        ti.arow0 = ti.m0;
-        ti.valid = (int)min<int64_t>(T::BM, rows - ti.m0);
-        compute();
-    } else {
-        // A buffer of the most rows that any choice of experts needs is mostly
-        // padding behind the last expert's: a workgroup walks the tiles (the
-        // columns of a block first), looking at as many blocks at once as it has waves.
-        static_assert(T::BM == 128, "one group per 128-row block");
-        int* const ahead = reinterpret_cast<int*>(smem + T::kSmem);
-        const int64_t tiles = (int64_t)m_blocks * n_blocks;
-        for (int64_t t0 = blockIdx.x; t0 < tiles; t0 += T::kWaves * (int64_t)gridDim.x) {
-            const int64_t mine = t0 + wave * (int64_t)gridDim.x;
-            int any = 0;
-            if (mine < tiles) {
-                const int32_t* const ids = layout + mine / n_blocks * 128;
-                const int id0 = ids[lane], id1 = ids[64 + lane];
-                any = __ballot((id0 >= 0 && id0 < G) || (id1 >= 0 && id1 < G)) != 0;
-            }
-            if (lane == 0) ahead[wave] = any;
-            __syncthreads();
-            int todo = 0;
 #pragma unroll
-            for (int w = 0; w < T::kWaves; ++w) todo |= ahead[w] << w;
-            todo = __builtin_amdgcn_readfirstlane(todo);
-            __syncthreads();
-            while (todo != 0) {
-                const int w = __builtin_ctz(todo);
-                todo &= todo - 1;
-                const int64_t t = t0 + w * (int64_t)gridDim.x;
-                ti.m0 = (int)(t / n_blocks) * T::BM;
-                ti.n0 = (int)(t % n_blocks) * T::BN;
-                ti.arow0 = ti.m0;
-                ti.valid = T::BM;
-                // once per id among the block's rows, the largest first
-                int below = (int)min<int64_t>(G, 0x7fffffff);
-                while (block_group(layout, G, below, lane, ti)) {
-                    compute();
-                    below = ti.g;
-                    __syncthreads();  // the staged tile has been stored before the next loads
-                }
-            }
+    for (int s = 0; s < T::S; ++s) issue(s, s, 0, T::kLoads);
+    wait_vmcnt<T::kUneven ? 0 : T::kLoads*(T::S - 1)>();
+    lds_barrier();
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) read_b(smem, chunk_lo, 0, j);
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) read_a(smem, chunk_lo, 0, i);
+    int st = 0;
+    for (int kb = 0; kb < KB; ++kb) {
+        const int nx = st + 1 == T::S ? 0 : st + 1;
+        phase(First{}, smem + st * T::kStage, chunk_hi, std::false_type{}, 0, 0);
+        wait_vmcnt_lgkm0<T::kLoads*(T::S - 2)>();  // the stage has been read, the next block's has landed
+        lds_barrier();
+        phase(Second{}, smem + nx * T::kStage, chunk_lo, std::true_type{}, kb + T::S, st);
+        st = nx;
+    }
+    wait_vmcnt_lgkm0<0>();  // the empty loads of the last blocks have retired
+    lds_barrier();
+
+    // epilogue: scales by row and column, rounding, and out through LDS
+    v4f col_scale[T::TN];
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) {
+        const int64_t col = min<int64_t>(ti.n0 + wcol + 16 * j + 4 * lg, p.N - 4);
+        col_scale[j] = *reinterpret_cast<const v4f*>(p.sb + (int64_t)ti.g * p.N + col);
+    }
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) {
+        const int row = wrow + 16 * i + lr;
+        const float row_scale = p.sa[ti.arow0 + min(row, ti.valid - 1)];
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j) {
+            v4f v;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = (row_scale * col_scale[j][q]) * (float)acc[i][j][q];
+            stage_bf16<T>(smem, row, wcol + 16 * j + 4 * lg, v);
         }
+    }
+    __syncthreads();
+    store_staged<T, kRouted>(smem, tid, ti, p.D, p.N);
+}
+
+// The dense form: tiles of shape T over columns [0, split), of shape U behind
+// them, whose workgroups (from `first` on) come last.  Two shapes may leave less
+// of the last round idle than one.
+template <class T, class U>
+__global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_gemm_kernel(Int8Operands p, int64_t rows, int64_t split,
+                                                                               unsigned first) {
+    static_assert(T::kThreads == U::kThreads, "one workgroup size");
+    extern __shared__ __align__(1024) uint8_t smem[];
+    auto run = [&](auto shape, int block, int64_t from, int64_t to) __attribute__((always_inline)) {
+        using X = decltype(shape);
+        const int m_blocks = (int)((rows + X::BM - 1) / X::BM), n_blocks = (int)((to - from + X::BN - 1) / X::BN);
+        const int tile = xcd_tile(block, m_blocks * n_blocks);
+        if (tile < 0) return;
+        TileInfo ti;
+        ti.ok0 = ti.ok1 = 0;
+        ti.g = 0;
+        const int span = X::kGroupM * n_blocks;
+        const int first_m = (tile / span) * X::kGroupM;
+        const int gm = min(m_blocks - first_m, X::kGroupM);
+        const int in_span = tile % span;
+        ti.m0 = (first_m + in_span % gm) * X::BM;
+        ti.n0 = (int)from + (in_span / gm) * X::BN;
+        ti.arow0 = ti.m0;
+        ti.valid = (int)min<int64_t>(X::BM, rows - ti.m0);
+        int8_tile<X, false>(p, ti, smem, threadIdx.x);
+    };
+    if constexpr (std::is_same<T, U>::value) {
+        run(T{}, blockIdx.x, 0, p.N);
+    } else {
+        if (blockIdx.x < first)
+            run(T{}, blockIdx.x, 0, split);
+        else
+            run(U{}, blockIdx.x - first, split, p.N);
     }
 }
 
-template <class T, bool kGrouped>
-static dg_status launch_tiled(const Int8Args& a, hipStream_t stream) {
-    const int64_t m_blocks = (a.rows + T::BM - 1) / T::BM, n_blocks = (a.N + T::BN - 1) / T::BN;
-    int64_t grid = (m_blocks * n_blocks + kNumXcds - 1) / kNumXcds * kNumXcds;
-    if (kGrouped) grid = std::min<int64_t>(grid, device_cus());
+// The contiguous-grouped form.  A buffer of the most rows that any choice of
+// experts needs is mostly padding behind the last expert's, so the 128-row
+// blocks that hold rows are found first, by every workgroup for itself (in
+// windows of kWindow blocks), and their tiles, the columns of a block first,
+// are shared out evenly: with one workgroup per tile of the buffer, in order,
+// 4096 rows in a buffer of 33664 were left to one of the 8 XCDs (829 us for 8
+// experts of 4096 x 7168).  Tiles that are left over behind the whole rounds are
+// cut in two (T2) or four (T4) where that takes less than a round of whole ones.
+template <class T, class T2, class T4>
+__global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_grouped_kernel(Int8Operands p,
+                                                                                  const int32_t* __restrict__ layout,
+                                                                                  int64_t rows, int64_t G) {
+    static_assert(T::BM == 128 && T2::BM == 128 && T4::BM == 128, "one group per 128-row block");
+    static_assert(T2::BN * 2 == T::BN && T4::BN * 4 == T::BN, "halves and quarters");
+    static_assert(T::kThreads == T2::kThreads && T::kThreads == T4::kThreads, "one workgroup size");
+    constexpr int kWindow = 4096;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint16_t used[kWindow / 16];  // a bit per block: whether it holds a row
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t m_blocks = rows / 128;
+    const int n_blocks = (int)((p.N + T::BN - 1) / T::BN);
+    const int grid = (int)gridDim.x;
+    for (int64_t w0 = 0; w0 < m_blocks; w0 += kWindow) {
+        const int blocks = (int)min<int64_t>(kWindow, m_blocks - w0), words = (blocks + 63) / 64;
+        // a load covers two blocks, 32 lanes of four ids each; eight loads at once,
+        // those past the last block of its own ids again
+        for (int b0 = wave * 16; b0 < words * 64; b0 += T::kWaves * 16) {
+            int4 id[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int b = min(b0 + 2 * i + (lane >> 5), blocks - 1);
+                id[i] = *reinterpret_cast<const int4*>(layout + (w0 + b) * 128 + (lane & 31) * 4);
+            }
+            uint32_t bits = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                auto valid = [&](int e) { return (uint32_t)e < (uint32_t)G; };
+                const uint64_t any = __ballot(valid(id[i].x) || valid(id[i].y) || valid(id[i].z) || valid(id[i].w));
+                bits |= (((uint32_t)any != 0 ? 1u : 0u) | ((any >> 32) != 0 ? 2u : 0u)) << (2 * i);
+            }
+            bits &= b0 >= blocks ? 0u : blocks - b0 >= 16 ? 0xffffu : (1u << (blocks - b0)) - 1u;
+            if (lane == 0) used[b0 / 16] = (uint16_t)bits;
+        }
+        __syncthreads();
+        // lane l holds word l of the window's blocks, and how many are used up to its end
+        const uint64_t word = lane < words ? reinterpret_cast<const uint64_t*>(used)[lane] : 0;
+        int upto = __popcll(word);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int below = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += below;
+        }
+        const int before = upto - __popcll(word);
+        const int64_t tiles = (int64_t)__builtin_amdgcn_readlane(upto, 63) * n_blocks;
+        const int left = (int)(tiles % grid);
+        // us a K block and round: 0.95 whole, 0.6 halves, 0.43 quarters
+        const int cost2 = (2 * left + grid - 1) / grid * 60, cost4 = (4 * left + grid - 1) / grid * 43;
+        const int cut = left == 0 || min(cost2, cost4) >= 95 ? 1 : cost2 <= cost4 ? 2 : 4;
+        const int64_t whole = cut > 1 ? tiles - left : tiles;
+        auto run = [&](auto shape, int64_t t, int part) __attribute__((always_inline)) {
+            using X = decltype(shape);
+            // the block: which word holds the k-th used one, then which bit
+            const int k = (int)(t / n_blocks);
+            const int at = __builtin_ctzll(__ballot(before <= k && k < upto));
+            uint64_t bits = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)word, at) |
+                            (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(word >> 32), at) << 32;
+            for (int skip = k - __builtin_amdgcn_readlane(before, at); skip > 0; --skip) bits &= bits - 1;
+            TileInfo ti;
+            ti.m0 = (int)(w0 + at * 64 + __builtin_ctzll(bits)) * 128;
+            ti.n0 = (int)(t % n_blocks) * T::BN + part * X::BN;
+            if (ti.n0 >= p.N) return;
+            ti.arow0 = ti.m0;
+            ti.valid = 128;
+            // once per id among the block's rows, the largest first
+            const int id0 = layout[ti.m0 + lane], id1 = layout[ti.m0 + 64 + lane];
+            for (int64_t below = G;;) {
+                auto usable = [&](int id) { return id >= 0 && id < below; };
+                const int largest = max(usable(id0) ? id0 : -1, usable(id1) ? id1 : -1);
+                ti.g = (int)wave_max((uint32_t)(largest + 1)) - 1;
+                if (ti.g < 0) break;
+                ti.ok0 = __ballot(id0 == ti.g);
+                ti.ok1 = __ballot(id1 == ti.g);
+                int8_tile<X, true>(p, ti, smem, tid);
+                __syncthreads();  // the staged tile has been stored before the next loads
+                below = ti.g;
+            }
+        };
+        for (int64_t t = blockIdx.x; t < whole; t += grid) run(T{}, t, 0);
+        if (cut == 2)
+            for (int i = blockIdx.x; i < left * 2; i += grid) run(T2{}, whole + i / 2, i % 2);
+        else if (cut == 4)
+            for (int i = blockIdx.x; i < left * 4; i += grid) run(T4{}, whole + i / 4, i % 4);
+        __syncthreads();  // the bits have been read
+    }
+}
+
+template <class T, class U>
+static dg_status launch_tiled(const Int8Args& a, int64_t split, hipStream_t stream) {
+    auto tiles = [&](int64_t bm, int64_t bn, int64_t columns) {
+        return ((a.rows + bm - 1) / bm * ((columns + bn - 1) / bn) + kNumXcds - 1) / kNumXcds * kNumXcds;
+    };
+    const int64_t first = tiles(T::BM, T::BN, split), grid = first + tiles(U::BM, U::BN, a.N - split);
     if (!grid_fits(grid, T::kThreads)) return DG_ERR_SHAPE;
-    // per-lane 32-bit offsets into a tile's rows of K bytes: K < 2^17
-    hipLaunchKernelGGL((int8_gemm_kernel<T, kGrouped>), dim3((unsigned)grid), dim3(T::kThreads), T::kSmem + 64, stream,
-                       reinterpret_cast<const uint8_t*>(a.A), a.sa, reinterpret_cast<const uint8_t*>(a.B), a.sb, a.D,
-                       a.layout, a.rows, a.N, a.K, a.G, (int)m_blocks, (int)n_blocks);
+    const Int8Operands p{reinterpret_cast<const uint8_t*>(a.A), a.sa, reinterpret_cast<const uint8_t*>(a.B), a.sb, a.D,
+                         a.N, a.K};
+    hipLaunchKernelGGL((int8_gemm_kernel<T, U>), dim3((unsigned)grid), dim3(T::kThreads),
+                       T::kSmem > U::kSmem ? T::kSmem : U::kSmem, stream, p, a.rows, split, (unsigned)first);
     return launched();
 }
 
@@ -327,9 +416,20 @@ using Int8Square128 = Int8Tile<128, 128, 2, 4, 4, 8>;
 using Int8Tall64 = Int8Tile<128, 64, 2, 2, 4, 8>;
 using Int8Square64 = Int8Tile<64, 64, 2, 2, 4, 8>;
 using Int8Narrow = Int8Tile<64, 32, 2, 2, 4, 8>;
+using Int8Quarter = Int8Tile<128, 64, 4, 2, 4, 8>;  // of Int8Rows128; Int8Square128 is half of it
+
+static dg_status launch_grouped(const Int8Args& a, hipStream_t stream) {
+    using T = Int8Rows128;
+    const int64_t tiles = a.rows / 128 * ((a.N + T::BN - 1) / T::BN) * 4;
+    const Int8Operands p{reinterpret_cast<const uint8_t*>(a.A), a.sa, reinterpret_cast<const uint8_t*>(a.B), a.sb, a.D,
+                         a.N, a.K};
+    hipLaunchKernelGGL((int8_grouped_kernel<T, Int8Square128, Int8Quarter>), dim3((unsigned)std::min<int64_t>(tiles, device_cus())),
+                       dim3(T::kThreads), T::kSmem, stream, p, a.layout, a.rows, a.G);
+    return launched();
+}
 
 dg_status launch_int8_gemm(const Int8Args& a, hipStream_t stream) {
-    if (a.layout != nullptr) return launch_tiled<Int8Rows128, true>(a, stream);
+    if (a.layout != nullptr) return launch_grouped(a, stream);
     const int64_t cus = device_cus();
     // 32 columns a workgroup where they are enough for the CUs (1 x 7168 x 2048:
     // 5.7 us, 6.3 with 16), else 16 (8 x 4096 x 7168: 7.8, 10.7 with 32)
@@ -341,26 +441,42 @@ dg_status launch_int8_gemm(const Int8Args& a, hipStream_t stream) {
     struct Shape { int bm, bn, ns; };
     static const Shape kShapes[] = {{256, 256, 1580}, {256, 192, 1250}, {256, 160, 1070}, {128, 256, 890},
                                     {128, 128, 530},  {128, 64, 320},   {64, 64, 200},    {64, 32, 155}};
+    auto rounds = [&](const Shape& sh, int64_t columns) {
+        return ((a.rows + sh.bm - 1) / sh.bm * ((columns + sh.bn - 1) / sh.bn) + cus - 1) / cus;
+    };
     int best = 0;
-    int64_t least = INT64_MAX;
+    int64_t least = INT64_MAX, split = a.N;
     for (int i = 0; i < 8; ++i) {
-        const Shape& sh = kShapes[i];
-        const int64_t tiles = ((a.rows + sh.bm - 1) / sh.bm) * ((a.N + sh.bn - 1) / sh.bn);
-        const int64_t cost = (tiles + cus - 1) / cus * sh.ns;
+        const int64_t cost = rounds(kShapes[i], a.N) * kShapes[i].ns;
         if (cost < least) {
             least = cost;
             best = i;
         }
     }
+    // or as many rounds of 256 x 256 tiles as are whole, and 192 or 160 columns
+    // behind them
+    const int64_t whole = rounds(kShapes[0], a.N) - 1, m_blocks = (a.rows + 255) / 256;
+    for (int i = 1; i <= 2 && whole > 0 && m_blocks <= whole * cus; ++i) {
+        const int64_t at = whole * cus / m_blocks * 256;
+        if (at >= a.N) continue;
+        const int64_t cost = whole * kShapes[0].ns + rounds(kShapes[i], a.N - at) * kShapes[i].ns;
+        if (cost < least) {
+            least = cost;
+            best = 7 + i;
+            split = at;
+        }
+    }
     switch (best) {
-        case 0: return launch_tiled<Int8Large, false>(a, stream);
-        case 1: return launch_tiled<Int8Wide192, false>(a, stream);
-        case 2: return launch_tiled<Int8Wide160, false>(a, stream);
-        case 3: return launch_tiled<Int8Rows128, false>(a, stream);
-        case 4: return launch_tiled<Int8Square128, false>(a, stream);
-        case 5: return launch_tiled<Int8Tall64, false>(a, stream);
-        case 6: return launch_tiled<Int8Square64, false>(a, stream);
-        default: return launch_tiled<Int8Narrow, false>(a, stream);
+        case 0: return launch_tiled<Int8Large, Int8Large>(a, split, stream);
+        case 1: return launch_tiled<Int8Wide192, Int8Wide192>(a, split, stream);
+        case 2: return launch_tiled<Int8Wide160, Int8Wide160>(a, split, stream);
+        case 3: return launch_tiled<Int8Rows128, Int8Rows128>(a, split, stream);
+        case 4: return launch_tiled<Int8Square128, Int8Square128>(a, split, stream);
+        case 5: return launch_tiled<Int8Tall64, Int8Tall64>(a, split, stream);
+        case 6: return launch_tiled<Int8Square64, Int8Square64>(a, split, stream);
+        case 7: return launch_tiled<Int8Narrow, Int8Narrow>(a, split, stream);
+        case 8: return launch_tiled<Int8Large, Int8Wide192>(a, split, stream);
+        default: return launch_tiled<Int8Large, Int8Wide160>(a, split, stream);
     }
 }
 

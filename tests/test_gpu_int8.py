@@ -79,7 +79,9 @@ def test_scales_that_are_not_finite_stay_in_their_rows_and_columns(M):
 
 
 GROUPED = [(3, 264, 384, [100, 0, 200]), (1, 8, 128, [1]), (5, 520, 256, [128, 1, 127, 0, 130]), (8, 4096, 256, [3] * 8),
-           (16, 1032, 640, [5, 0, 300, 17, 128, 64, 0, 0, 90, 33, 12, 1, 2, 16, 31, 257]), (2, 2048, 2048, [700, 900])]
+           (16, 1032, 640, [5, 0, 300, 17, 128, 64, 0, 0, 90, 33, 12, 1, 2, 16, 31, 257]), (2, 2048, 2048, [700, 900]),
+           # left-over tiles as they are, and behind a whole round in halves and in quarters (256 CUs)
+           (2, 2048, 256, [1300, 1250]), (3, 2056, 128, [2000, 1500, 1700]), (2, 2048, 128, [2500, 2400])]
 
 
 def grouped_case(G, N, K, counts, seed):
@@ -119,6 +121,32 @@ def test_grouped_blocks_that_mix_ids(N):
     D = torch.full((layout.size, N), SENTINEL, dtype=torch.int16, device="cuda")
     dg.dg_int8_gemm_grouped_contiguous(to_dev(A), to_dev(sa), to_dev(B), to_dev(sb), D, to_dev(layout))
     check_grouped(D, A, sa, B, sb, layout)
+
+
+def test_grouped_blocks_far_apart_in_a_long_buffer():
+    """Few blocks that hold rows, the others empty, over more of them than a workgroup lists at once."""
+    rng = np.random.default_rng(3)
+    M, N, K, G = 9000 * 128, 264, 128, 3
+    layout = np.full(M, -1, np.int32)
+    for b in (0, 63, 64, 1000, 4095, 4096, 4097, 8191, 8192, 8999):
+        layout[b * 128 + rng.integers(0, 128, 40)] = rng.integers(0, G)
+    layout[5000 * 128 + 127], layout[6000 * 128:6001 * 128] = 2, G  # one row alone; ids that are none
+    rows = np.nonzero((layout >= 0) & (layout < G))[0]
+    A = torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda")
+    B = torch.randint(-128, 128, (G, N, K), dtype=torch.int8, device="cuda")
+    sa, sb = torch.rand(M, device="cuda"), torch.rand(G, N, device="cuda")
+    D = torch.full((M, N), SENTINEL, dtype=torch.int16, device="cuda")
+    dg.dg_int8_gemm_grouped_contiguous(A, sa, B, sb, D, to_dev(layout))
+    at = torch.from_numpy(rows).cuda()
+    want = exact_rows(A[at], sa[at], B, sb, torch.from_numpy(layout[rows].astype(np.int64)).cuda())
+    assert torch.equal(D[at].view(torch.bfloat16), want)
+    D[at] = SENTINEL
+    assert bool((D == SENTINEL).all())
+
+
+def exact_rows(A, sa, B, sb, e):
+    sums = (B[e].double() * A.double().unsqueeze(1)).sum(2).float()
+    return ((sa.unsqueeze(1) * sb[e]) * sums).to(torch.bfloat16)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
