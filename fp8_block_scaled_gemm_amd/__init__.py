@@ -608,21 +608,21 @@ def dg_moe_dispatch(x, ids, E, out=None, rows=None, layout=None, offsets=None, w
                                                      _raw_stream(x)))
 
 
-def _no_grad_rows(name, call, x, *given):
-    """A quantizing call: new outputs refuse to pass a gradient back, given ones warn."""
-    def done():
-        return _done(name, call())
-    if not _ops().wants_grad(x):
-        return done()
-    if all(g is None for g in given):
-        return _NoGradient.apply(name, done, x)
-    _warn_no_grad(name, "in outputs that are given", 4)
-    return done()
+def _no_grad_rows(name, call, x, q, s):
+    """A quantizing call whose input requires a gradient: new outputs refuse to
+    pass one back, given ones warn."""
+    if q is None and s is None:
+        return _NoGradient.apply(name, call, x)
+    _warn_no_grad(name, "in outputs that are given", 5)
+    return call()
 
 
-def _dispatch_codes(name, held, x, ids, E, q, s, rows, layout, offsets, workspace):
-    return _no_grad_rows(name, lambda: _ops().moe_dispatch(held, x, ids, E, q, s, rows, layout, offsets, workspace,
-                                                           _raw_stream(x)), x, q, s)
+def _dispatch_codes(name, held, x, ids, E, q, s, *plan):
+    ops = _ops()
+    if ops.wants_grad(x):
+        return _no_grad_rows(name, lambda: _done(name, ops.moe_dispatch(held, x, ids, E, q, s, *plan, _raw_stream(x))),
+                             x, q, s)
+    return _done(name, ops.moe_dispatch(held, x, ids, E, q, s, *plan, _raw_stream(x)))
 
 
 def dg_moe_dispatch_fp8(x, ids, E, q=None, s=None, rows=None, layout=None, offsets=None, workspace=None):
@@ -713,7 +713,10 @@ def dg_swiglu(z, layout=None, h=None):
 
 
 def _swiglu_codes(name, held, z, layout, q, s):
-    return _no_grad_rows(name, lambda: _ops().swiglu(held, z, layout, q, s, _raw_stream(z)), z, q, s)
+    ops = _ops()
+    if ops.wants_grad(z):
+        return _no_grad_rows(name, lambda: _done(name, ops.swiglu(held, z, layout, q, s, _raw_stream(z))), z, q, s)
+    return _done(name, ops.swiglu(held, z, layout, q, s, _raw_stream(z)))
 
 
 def dg_swiglu_quantize_fp8(z, layout=None, q=None, s=None):
@@ -762,4 +765,7 @@ def dg_int8_gemm_grouped_contiguous(A, sa, B, sb, D, grouped_layout):
 def dg_quantize_int8_per_row(x, q=None, s=None):
     """x[M][K] fp32 or bf16 -> (q[M][K] int8, s[M] fp32): per token for the
     activations, per output channel for the weights."""
-    return _no_grad_rows("dg_quantize_int8_per_row", lambda: _ops().quantize_int8(x, q, s, _raw_stream(x)), x, q, s)
+    name, ops = "dg_quantize_int8_per_row", _ops()
+    if ops.wants_grad(x):
+        return _no_grad_rows(name, lambda: _done(name, ops.quantize_int8(x, q, s, _raw_stream(x))), x, q, s)
+    return _done(name, ops.quantize_int8(x, q, s, _raw_stream(x)))

@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/LegacyTypeDispatch.h>
 #include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -342,14 +343,27 @@ struct Plan {
         else if (held != Py_None)
             M = sized(held, "the rows' buffer", 2).size(0);
         ids = (const int32_t*)pointer(t, "ids", {at::kInt}, {T, k}, dev);
-        rows = given_or_new(rows_, "rows", {T, k}, at::kInt, dev);
-        layout = given_or_new(layout_, "layout", {M}, at::kInt, dev);
-        offsets = given_or_new(offsets_, "offsets", {E + 1}, at::kInt, dev);
+        if (rows_ == Py_None && layout_ == Py_None && offsets_ == Py_None) {
+            // one allocation for the three: each takes longer than a kernel for
+            // few tokens can spare (one token: 8.8 -> 6.2 us of host time)
+            const int64_t at_rows = M, at_offsets = M + (T * k + 3) / 4 * 4;
+            const at::Tensor all = at::empty({at_offsets + E + 1}, at::TensorOptions().dtype(at::kInt).device(dev));
+            const at::AutoDispatchBelowADInplaceOrView plain;
+            layout = all.as_strided({M}, {1}, 0);
+            rows = all.as_strided({T, k}, {k, 1}, at_rows);
+            offsets = all.as_strided({E + 1}, {1}, at_offsets);
+        } else {
+            rows = given_or_new(rows_, "rows", {T, k}, at::kInt, dev);
+            layout = given_or_new(layout_, "layout", {M}, at::kInt, dev);
+            offsets = given_or_new(offsets_, "offsets", {E + 1}, at::kInt, dev);
+        }
         prows = (int32_t*)pointer(rows, "rows", {at::kInt}, {T, k}, dev);
         playout = (int32_t*)pointer(layout, "layout", {at::kInt}, {M}, dev);
         poffsets = (int32_t*)pointer(offsets, "offsets", {at::kInt}, {E + 1}, dev);
-        ws = workspace(workspace_, bytes, dev);
+        if (bytes > 0 || workspace_ != Py_None) ws = workspace(workspace_, bytes, dev);
     }
+    void* scratch() const { return ws.defined() ? ws.data_ptr() : nullptr; }
+    int64_t scratch_bytes() const { return ws.defined() ? ws.numel() : 0; }
 };
 
 // ids, E, rows, layout, offsets, workspace, stream
@@ -358,10 +372,10 @@ PyObject* moe_sort(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const Plan p(a[0], a[1], a[2], a[3], a[4], Py_None, a[5]);
         if (p.status != DG_OK) return PyLong_FromLong(p.status);
         void* const stream = stream_of(a[6]);
-        void* const pws = p.ws.data_ptr();
+        void* const pws = p.scratch();
         const OnDevice on(p.rows.device().index());
         const dg_status s = unlocked([&] {
-            return dg_moe_sort(p.ids, p.prows, p.playout, p.poffsets, p.T, p.k, p.E, p.M, pws, p.ws.numel(), stream);
+            return dg_moe_sort(p.ids, p.prows, p.playout, p.poffsets, p.T, p.k, p.E, p.M, pws, p.scratch_bytes(), stream);
         });
         if (s != DG_OK) return PyLong_FromLong(s);
         return returned({{a[2], &p.rows}, {a[3], &p.layout}, {a[4], &p.offsets}});
@@ -414,21 +428,21 @@ PyObject* moe_dispatch(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const OnDevice on(dev.index());
         const Rows r(held, a[4], a[5], held == kBf16 ? "out" : "q", p.M, H, dev);
         void* const stream = stream_of(a[10]);
-        void* const pws = p.ws.data_ptr();
+        void* const pws = p.scratch();
         const dg_status s = unlocked([&] {
             switch (held) {
                 case kBf16:
                     return dg_moe_dispatch(px, p.ids, (uint16_t*)r.pq, p.prows, p.playout, p.poffsets, p.T, p.k, p.E, H, p.M,
-                                           pws, p.ws.numel(), stream);
+                                           pws, p.scratch_bytes(), stream);
                 case kFp8:
                     return dg_moe_dispatch_fp8(px, p.ids, (uint8_t*)r.pq, (float*)r.ps, p.prows, p.playout, p.poffsets, p.T,
-                                               p.k, p.E, H, p.M, pws, p.ws.numel(), stream);
+                                               p.k, p.E, H, p.M, pws, p.scratch_bytes(), stream);
                 case kFp8E8:
                     return dg_moe_dispatch_fp8_e8m0(px, p.ids, (uint8_t*)r.pq, (uint8_t*)r.ps, p.prows, p.playout,
-                                                    p.poffsets, p.T, p.k, p.E, H, p.M, pws, p.ws.numel(), stream);
+                                                    p.poffsets, p.T, p.k, p.E, H, p.M, pws, p.scratch_bytes(), stream);
                 default:
                     return dg_moe_dispatch_int8(px, p.ids, (int8_t*)r.pq, (float*)r.ps, p.prows, p.playout, p.poffsets, p.T,
-                                                p.k, p.E, H, p.M, pws, p.ws.numel(), stream);
+                                                p.k, p.E, H, p.M, pws, p.scratch_bytes(), stream);
             }
         });
         if (s != DG_OK) return PyLong_FromLong(s);

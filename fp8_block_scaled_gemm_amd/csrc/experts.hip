@@ -160,6 +160,8 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(const int3
     int* const part = offsets + E + 1;                       // [kSortWaves]
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int me = blockIdx.x;
+    const int64_t begin = me * run, end = min(begin + run, P);
+    int id = begin + tid < end ? ids[begin + tid] : -1;  // of the tile that is placed next
     for (int e = tid; e < E; e += kSortThreads) {
         counts[e] = v4u{0, 0, 0, 0};
         size[e] = next[e] = 0;
@@ -174,10 +176,15 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(const int3
         const int group = tid / width, groups = kSortThreads / width;
         for (int e = tid % width; e < E; e += width) {
             int all = 0, before = 0;
-            for (int r = group; r < runs; r += groups) {
-                const int n = table[(int64_t)r * E + e];
-                all += n;
-                before += r < me ? n : 0;
+            for (int r0 = group; r0 < runs; r0 += 8 * groups) {
+                int n[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) n[i] = table[(int64_t)min(r0 + i * groups, runs - 1) * E + e];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (r0 + i * groups < runs) all += n[i];
+                    if (r0 + i * groups < me) before += n[i];
+                }
             }
             atomicAdd(&size[e], all);
             atomicAdd(&next[e], before);
@@ -189,13 +196,12 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(const int3
     if (me == 0)
         for (int e = tid; e <= E; e += kSortThreads) out_offsets[e] = offsets[e];
     __syncthreads();
-    write_layout(offsets, size, E, M, (int64_t)me * kSortWaves + wave, (int64_t)runs * kSortWaves, layout, lane);
 
     const int bits = 32 - __builtin_clz(max(E - 1, 1));
-    const int64_t begin = me * run, end = min(begin + run, P);
     for (int64_t base = begin; base < end; base += kSortThreads) {
         const int64_t p = base + tid;
-        const int e = p < end ? ids[p] : -1;
+        const int e = id;
+        id = p + kSortThreads < end ? ids[p + kSortThreads] : -1;
         const bool here = e >= 0 && e < E;
         uint64_t same = __ballot(here);
         for (int b = 0; b < bits; ++b) {
@@ -222,6 +228,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(const int3
             __syncthreads();
         }
     }
+    write_layout(offsets, size, E, M, (int64_t)me * kSortWaves + wave, (int64_t)runs * kSortWaves, layout, lane);
 }
 
 dg_status launch_sort(const SortArgs& a, hipStream_t stream) {
@@ -281,17 +288,15 @@ __device__ __forceinline__ void sort_token(const SmallSort& p, int64_t t, int* l
     for (int e = tid; e < 2 * p.E; e += 256) size[e] = 0;
     __syncthreads();
     const int first = (int)(t * p.k);
+    const int own = tid < p.k && first + tid < p.P ? p.ids[first + tid] : -1;
     count_pairs<true>(p.ids, 0, p.P, p.E, size, tid, 256, before, first);
     __syncthreads();
     padded_offsets<256>(size, offsets, part, p.E, tid);
-    if (tid < p.k && first + tid < p.P) {
-        const int e = p.ids[first + tid];
-        int r = -1;
-        if (e >= 0 && e < p.E) {
-            r = offsets[e] + before[e];
-            for (int j = 0; j < tid; ++j) r += p.ids[first + j] == e;
-        }
-        row[tid] = r;
+    if (tid < 64) {  // the first wave, a lane for each choice
+        const bool here = own >= 0 && own < p.E;
+        int r = here ? offsets[own] + before[own] : -1;
+        for (int j = 0; j < p.k; ++j) r += here && j < tid && __builtin_amdgcn_readlane(own, j) == own;
+        if (tid < p.k) row[tid] = r;
     }
     __syncthreads();
 }
@@ -325,8 +330,8 @@ __global__ __launch_bounds__(256) void moe_copy_bf16_kernel(const uint16_t* __re
         __shared__ int part[4], row[kMaxChoices];
         const int64_t t = blockIdx.x < copies ? blockIdx.x / parts : T;  // T: none, all pairs lie before it
         sort_token(plan, t, plan_lds, part, row, tid);
-        write_plan(plan, t, t < T && blockIdx.x % parts == 0, plan_lds, row, tid);
         if (t == T) {
+            write_plan(plan, t, false, plan_lds, row, tid);
             const int* const size = plan_lds;
             const int* const offsets = size + 2 * plan.E;
             const int64_t r0 = (int64_t)(blockIdx.x - copies) * kZeroRows;
@@ -339,10 +344,12 @@ __global__ __launch_bounds__(256) void moe_copy_bf16_kernel(const uint16_t* __re
             return zero_rows(out, r0, __ballot(pad), H, tid);
         }
         const int64_t c = blockIdx.x % parts * 256 + tid;
-        if (c >= width) return;
-        const v4u v = *reinterpret_cast<const v4u*>(x + t * H + c * 8);
-        for (int j = 0; j < k; ++j)
-            if (row[j] >= 0) *reinterpret_cast<v4u*>(out + row[j] * H + c * 8) = v;
+        if (c < width) {
+            const v4u v = *reinterpret_cast<const v4u*>(x + t * H + c * 8);
+            for (int j = 0; j < k; ++j)
+                if (row[j] >= 0) *reinterpret_cast<v4u*>(out + row[j] * H + c * 8) = v;
+        }
+        write_plan(plan, t, blockIdx.x % parts == 0, plan_lds, row, tid);
     } else {
         if (blockIdx.x >= copies) return zero_padding(out, layout, M, H, blockIdx.x - copies, tid);
         const int64_t i = (int64_t)blockIdx.x * 256 + tid;
@@ -407,10 +414,7 @@ __global__ __launch_bounds__(256) void moe_copy_fp8_kernel(const uint16_t* __res
 #pragma unroll
         for (int h = 0; h < 2; ++h) raw[h] = *reinterpret_cast<const v4u*>(x + t * H + kb * 128 + 64 * h + 8 * lane);
     }
-    if constexpr (kSmall) {
-        sort_token(plan, t, plan_lds, part, row, tid);
-        write_plan(plan, t, blockIdx.y == 0, plan_lds, row, tid);
-    }
+    if constexpr (kSmall) sort_token(plan, t, plan_lds, part, row, tid);
     if (here) {
         float f[2][8];
 #pragma unroll
@@ -429,6 +433,7 @@ __global__ __launch_bounds__(256) void moe_copy_fp8_kernel(const uint16_t* __res
             const int64_t r = target(t, j);
             if (r >= 0) static_cast<S*>(s)[r * pitch + kb] = scales[tid & 31];
         }
+    if constexpr (kSmall) write_plan(plan, blockIdx.x, blockIdx.y == 0, plan_lds, row, tid);
 }
 
 // int8 rows: one workgroup per token, which reads the row twice (the second
@@ -444,7 +449,6 @@ __global__ __launch_bounds__(256) void moe_copy_int8_kernel(const uint16_t* __re
     const int tid = threadIdx.x;
     if constexpr (kSmall) {
         sort_token(plan, t, plan_lds, part, row, tid);
-        write_plan(plan, t, true, plan_lds, row, tid);
     } else {
         if (tid < k) row[tid] = rows[t * k + tid];
     }
@@ -464,6 +468,7 @@ __global__ __launch_bounds__(256) void moe_copy_int8_kernel(const uint16_t* __re
             if (row[j] >= 0) *reinterpret_cast<v2u*>(q + row[j] * H + c * 8) = codes;
     }
     if (tid < k && row[tid] >= 0) s[row[tid]] = held.scale;
+    if constexpr (kSmall) write_plan(plan, t, true, plan_lds, row, tid);
 }
 
 static bool small_sort(int64_t T, int k) { return T > 0 && T * k <= kSmallPairs; }
