@@ -648,7 +648,9 @@ class _Unpermute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, rows, weights, layout):
         out = _done("dg_moe_unpermute", _ops().moe_unpermute(y, rows, weights, None, _raw_stream(y)))
-        ctx.save_for_backward(y, rows, weights, layout)
+        # the rows themselves are kept only where the weights' gradient needs them
+        ctx.rows = y.shape[0]
+        ctx.save_for_backward(y if weights is not None and weights.requires_grad else None, rows, weights, layout)
         return out
 
     @staticmethod
@@ -657,7 +659,8 @@ class _Unpermute(torch.autograd.Function):
         y, rows, weights, layout = ctx.saved_tensors
         want_y, _, want_weights, _ = ctx.needs_input_grad
         gy, gw = _done("dg_moe_unpermute_backward", _ops().moe_unpermute_backward(
-            grad.contiguous(), y, rows, weights, layout, None, None, want_y, want_weights, _raw_stream(y)))
+            grad.contiguous(), ctx.rows if y is None else y, rows, weights, layout, None, None, want_y, want_weights,
+            _raw_stream(grad)))
         return gy, None, gw, None
 
 

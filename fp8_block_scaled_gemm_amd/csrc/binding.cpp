@@ -471,17 +471,20 @@ PyObject* moe_unpermute(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
-// grad, y, rows, weights, layout, grad_y, grad_weights, want_y, want_weights, stream
+// grad, y (an int: its rows, where the weights' gradient is not wanted), rows, weights, layout, grad_y,
+// grad_weights, want_y, want_weights, stream
 PyObject* moe_unpermute_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded<10>(args, n, [](PyObject* const* a) -> PyObject* {
         const at::Tensor& g = sized(a[0], "grad", 2);
-        const at::Tensor& y = sized(a[1], "y", 2);
+        const bool rows_only = PyLong_Check(a[1]);
         const at::Tensor& rows = sized(a[2], "rows", 2);
-        const int64_t T = g.size(0), H = g.size(1), M = y.size(0), k = rows.size(1);
+        const int64_t T = g.size(0), H = g.size(1), k = rows.size(1);
+        const int64_t M = rows_only ? integer(a[1]) : sized(a[1], "y", 2).size(0);
         const at::Device dev = g.device();
         const bool want_y = a[7] == Py_True, want_w = a[8] == Py_True;
         const auto* pg = (const uint16_t*)pointer(g, "grad", {at::kBFloat16}, {T, H}, dev);
-        const auto* py = (const uint16_t*)pointer(y, "y", {at::kBFloat16}, {M, H}, dev);
+        const auto* py =
+            rows_only ? nullptr : (const uint16_t*)pointer(a[1], "y", {at::kBFloat16}, {M, H}, dev);
         const auto* pr = (const int32_t*)pointer(rows, "rows", {at::kInt}, {T, k}, dev);
         const auto* pw = (const float*)pointer_or_null(a[3], "weights", {at::kFloat}, {T, k}, dev);
         const auto* pl = (const int32_t*)pointer_or_null(a[4], "layout", {at::kInt}, {M}, dev);

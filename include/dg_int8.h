@@ -1,7 +1,8 @@
 /*
  * dg_int8.h - C ABI of the 8-bit integer products: operands in int8 with one
  * fp32 scale per row on either side (per token for the activations, per output
- * channel for the weights).  Same library, same conventions as dg_fp8.h.
+ * channel for the weights).  Same library, same conventions as dg_fp8.h;
+ * outputs overlap no input.
  *
  *   D[m,n] = bf16( (sa[m] * sb[n]) * sum_k A[m,k] * B[n,k] )
  *

@@ -214,6 +214,22 @@ def test_unpermute_takes_rows_outside_the_buffer_as_none():
     assert gy.float().sum(1).nonzero().flatten().tolist() == [0, 127] and float(gy.max()) == 2.0
 
 
+def test_sums_without_sorted_rows_or_without_tokens():
+    none = torch.empty(0, 16, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([[-1, 0], [5, -1]], dtype=torch.int32, device="cuda")
+    w = torch.ones(2, 2, device="cuda")
+    g = torch.ones(2, 16, dtype=torch.bfloat16, device="cuda")
+    assert float(dg.dg_moe_unpermute(none, rows, w).abs().max()) == 0.0
+    gy, gw = dg.dg_moe_unpermute_backward(g, none, rows, w)
+    assert gy.shape == (0, 16) and float(gw.abs().max()) == 0.0
+    y = torch.full((256, 16), 3.0, dtype=torch.bfloat16, device="cuda")
+    assert dg.dg_moe_unpermute(y, rows[:0], w[:0]).shape == (0, 16)
+    layout = torch.full((256,), -1, dtype=torch.int32, device="cuda")
+    layout[7] = 0
+    gy, gw = dg.dg_moe_unpermute_backward(g[:0], y, rows[:0], w[:0], layout, y.clone())
+    assert gw.shape == (0, 2) and gy.float().sum(1).nonzero().flatten().tolist() == [7]
+
+
 @pytest.mark.parametrize("value", [INF, NAN])
 def test_unpermute_keeps_values_that_are_not_finite_in_their_rows(value):
     rows, layout, y, w, g = sum_case(9, 2, 3, "own", 64)
