@@ -30,7 +30,8 @@
 //     (scattered 8-byte fragment stores reach half the write bandwidth).
 //   - Workgroups are dispatched round-robin over the 8 XCDs; the tile order
 //     gives each XCD a contiguous range of tiles, grouped a few m-blocks at a
-//     time, so that concurrent tiles on one XCD share A and B slabs in its L2.
+//     time (the contiguous form: every eighth column tile), so that concurrent
+//     tiles on one XCD share A and B slabs in its L2.
 #include "device_common.h"
 #include "launch.h"
 #include "tiles.h"
@@ -117,6 +118,21 @@ __device__ __forceinline__ bool decode_tile(int b, int m_blocks, int n_blocks, i
         ti.arow0 = (int64_t)ti.g * rows + ti.m0;
         return true;
     }
+    if constexpr (kForm == Form::Contiguous) {
+        // Tiles in plain order, the columns of a block first: each XCD takes every
+        // eighth column tile of all blocks.  A buffer of the most rows that any
+        // choice of experts needs holds them at its beginning, and with a run of
+        // blocks for each XCD one of the eight did all of the work (4128 rows in a
+        // buffer of 33664, 8 groups of 4096 x 7168: 884 us, 185 in this order;
+        // full buffers 1036 -> 1008 at 4096 x 7168, 545 -> 551 at 7168 x 2048).
+        static_assert(T::BM == 128, "one group per 128-row block");
+        if (b >= m_blocks * n_blocks) return false;
+        ti.m0 = b / n_blocks * T::BM;
+        ti.n0 = b % n_blocks * T::BN;
+        ti.valid = T::BM;
+        ti.arow0 = ti.m0;
+        return block_group(aux, G, (int)G, lane, ti);
+    }
     int tile = xcd_tile(b, m_blocks * n_blocks);
     if (tile < 0) return false;
     ti.g = 0;
@@ -127,15 +143,8 @@ __device__ __forceinline__ bool decode_tile(int b, int m_blocks, int n_blocks, i
     const int in_span = tile % span;
     ti.m0 = (first_m + in_span % gm) * T::BM;
     ti.n0 = (in_span / gm) * T::BN;
-    if (kForm == Form::Dense || kForm == Form::DenseAcc || kForm == Form::DenseLora) {
-        ti.valid = (int)min<int64_t>(T::BM, rows - ti.m0);
-        ti.arow0 = ti.m0;
-    } else {
-        static_assert(kForm != Form::Contiguous || T::BM == 128, "one group per 128-row block");
-        if (!block_group(aux, G, (int)G, lane, ti)) return false;
-        ti.valid = T::BM;
-        ti.arow0 = ti.m0;
-    }
+    ti.valid = (int)min<int64_t>(T::BM, rows - ti.m0);
+    ti.arow0 = ti.m0;
     return true;
 }
 
