@@ -23,7 +23,10 @@ namespace dg {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kSortOnePairs = 8192;  // pairs that one workgroup sorts by itself
+// Pairs that one workgroup sorts by itself: one tile (256 experts: 1024 pairs
+// 8.3 us; 2048 pairs 9.5 in one workgroup, 9.0 in two and two launches, 8192
+// pairs 17.0 and 8.5).
+constexpr int kSortOnePairs = 1024;
 constexpr int kSortMaxRuns = 256;
 
 // Pairs in a run, a multiple of the tile.
@@ -113,20 +116,37 @@ __device__ __forceinline__ int expert_of(const int* offsets, int E, int r) {
     return lo;
 }
 
-// layout of the 128-row blocks first, first + step, ... of M rows, one wave
-// per block, from the experts' offsets and sizes (LDS).
-__device__ __forceinline__ void write_layout(const int* offsets, const int* size, int E, int64_t M, int64_t first,
-                                             int64_t step, int32_t* __restrict__ layout, int lane) {
-    for (int64_t b = first; b < M / 128; b += step) {
-        const int64_t r0 = b * 128;
-        int2 v = {-1, -1};
-        if (r0 < offsets[E]) {
-            const int e = expert_of(offsets, E, (int)r0), r = (int)r0 + 2 * lane - offsets[e];
-            v.x = r < size[e] ? e : -1;
-            v.y = r + 1 < size[e] ? e : -1;
+// layout of M rows, by `waves` waves of which this is the `wave`-th, from the
+// experts' offsets and sizes (LDS): the experts that have pairs are dealt out to
+// the waves, several to an expert's blocks where there are more waves than
+// experts, and then the rows behind the last expert's.  (A search for each
+// block's expert took 10 of 15 us where one workgroup sorts 512 pairs of 256
+// experts.)
+__device__ __forceinline__ void write_layout(const int* offsets, const int* size, int E, int64_t M, int wave, int waves,
+                                             int32_t* __restrict__ layout, int lane) {
+    auto blocks = [&](int e, int begin, int step) {
+        const int first = offsets[e], n = size[e];
+        for (int r = begin * 128; r < n; r += step * 128) {
+            const int at = r + 2 * lane;
+            *reinterpret_cast<int2*>(layout + first + at) = int2{at < n ? e : -1, at + 1 < n ? e : -1};
         }
-        *reinterpret_cast<int2*>(layout + r0 + 2 * lane) = v;
+    };
+    if (waves > E) {
+        blocks(wave % E, wave / E, (waves - 1 - wave % E) / E + 1);
+    } else {
+        int turn = wave;  // used experts until this wave's next one
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            uint64_t used = __ballot(e0 + lane < E && size[min(e0 + lane, E - 1)] > 0);
+            for (; turn < __popcll(used); turn += waves) {
+                uint64_t rest = used;
+                for (int i = 0; i < turn; ++i) rest &= rest - 1;
+                blocks(e0 + __builtin_ctzll(rest), 0, 1);
+            }
+            turn -= __popcll(used);
+        }
     }
+    for (int64_t r = offsets[E] + (int64_t)(wave * 64 + lane) * 4; r < M; r += (int64_t)waves * 256)
+        *reinterpret_cast<int4*>(layout + r) = int4{-1, -1, -1, -1};
 }
 
 // Sum over 16 byte counts of one expert: those of the waves before `wave`, and
@@ -228,7 +248,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(const int3
             __syncthreads();
         }
     }
-    write_layout(offsets, size, E, M, (int64_t)me * kSortWaves + wave, (int64_t)runs * kSortWaves, layout, lane);
+    write_layout(offsets, size, E, M, me * kSortWaves + wave, runs * kSortWaves, layout, lane);
 }
 
 dg_status launch_sort(const SortArgs& a, hipStream_t stream) {
@@ -274,7 +294,10 @@ struct SmallSort {
     int64_t M;
     int P, k, E;
 };
-constexpr int kSmallPairs = 4096;  // as many ids as a workgroup looks through
+// As many ids as a workgroup looks through (512 tokens of 7168 to 8 of 256: 13.3
+// us against 18.7 behind a sort; 2048 tokens of 2048 to 4 of 64, 8192 ids: 19.2
+// and 16.0).
+constexpr int kSmallPairs = 4096;
 constexpr int kMaxChoices = 64;
 
 static size_t small_lds(int E) { return (size_t)(3 * E + 1) * 4; }
@@ -309,8 +332,8 @@ __device__ __forceinline__ void write_plan(const SmallSort& p, int64_t t, bool f
     if (first_part && tid < p.k && t * p.k + tid < p.P) p.rows[t * p.k + tid] = row[tid];
     if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int e = tid; e <= p.E; e += 256) p.offsets[e] = offsets[e];
-    const int64_t wg = blockIdx.y * (int64_t)gridDim.x + blockIdx.x;
-    write_layout(offsets, size, p.E, p.M, wg * 4 + (tid >> 6), (int64_t)gridDim.x * gridDim.y * 4, p.layout, tid & 63);
+    const int wg = blockIdx.y * gridDim.x + blockIdx.x;
+    write_layout(offsets, size, p.E, p.M, wg * 4 + (tid >> 6), gridDim.x * gridDim.y * 4, p.layout, tid & 63);
 }
 
 // bf16 rows: a thread copies 8 columns of a token into each of its rows.  The
