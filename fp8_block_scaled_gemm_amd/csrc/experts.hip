@@ -394,10 +394,12 @@ __device__ __forceinline__ int64_t xcd_run(unsigned b, unsigned grid) {
 }
 
 // FP8 rows: eight lanes own one 128-column block of a token, as in the
-// quantizer, and store its line of codes into each of the token's rows.  The
-// scales of the workgroup's 32 blocks go out together: stored by each group
-// for itself, four bytes a row, they cost 7 of 78 us (4096 tokens of 7168 into
-// 8 rows each).
+// quantizer, and store its line of codes into each of the token's rows.  Bound
+// by the stores: 4096 tokens of 7168 into 8 rows each, 243 MB, 64 us, 4.7 TB/s
+// with the reads.  The scales of the workgroup's 32 blocks go out together and
+// tokens in runs per XCD, so that rows beside each other meet in one L2 (76 us
+// with the sort, 78 before, 71 without scales); a wave for each whole row took
+// as long, stores past the caches too.
 template <bool kE8, bool kSmall>
 __global__ __launch_bounds__(256) void moe_copy_fp8_kernel(const uint16_t* __restrict__ x,
                                                            const int32_t* __restrict__ rows, uint8_t* __restrict__ q,
@@ -459,9 +461,9 @@ __global__ __launch_bounds__(256) void moe_copy_fp8_kernel(const uint16_t* __res
     if constexpr (kSmall) write_plan(plan, blockIdx.x, blockIdx.y == 0, plan_lds, row, tid);
 }
 
-// int8 rows: one workgroup per token, which reads the row twice (the second
-// time from its cache): the scale needs all of it.
-template <bool kSmall>
+// int8 rows: one workgroup per token, as the scale needs all of it.  4096 tokens
+// of 7168 into 8 rows each: 71 us with the sort, 4.1 TB/s.
+template <int C, bool kSmall>
 __global__ __launch_bounds__(256) void moe_copy_int8_kernel(const uint16_t* __restrict__ x,
                                                             const int32_t* __restrict__ rows, uint8_t* __restrict__ q,
                                                             float* __restrict__ s, int k, int64_t H, SmallSort plan) {
@@ -475,22 +477,15 @@ __global__ __launch_bounds__(256) void moe_copy_int8_kernel(const uint16_t* __re
     } else {
         if (tid < k) row[tid] = rows[t * k + tid];
     }
-    uint32_t top = 0;
-    for (int64_t c = tid; c < H / 8; c += 256) {
-        float f[8];
-        unpack_bf16(*reinterpret_cast<const v4u*>(x + t * H + c * 8), f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, magnitude_bits(f[e]));
-    }
-    const Int8Row held(block_max<4>(top, tops, tid));
-    for (int64_t c = tid; c < H / 8; c += 256) {
-        float f[8];
-        unpack_bf16(*reinterpret_cast<const v4u*>(x + t * H + c * 8), f);
-        const v2u codes = held.codes(f);
-        for (int j = 0; j < k; ++j)
-            if (row[j] >= 0) *reinterpret_cast<v2u*>(q + row[j] * H + c * 8) = codes;
-    }
-    if (tid < k && row[tid] >= 0) s[row[tid]] = held.scale;
+    // the barrier inside is in front of the first store
+    const float scale = int8_row<256, C>(
+        H / 8, tid, tops,
+        [&](int64_t c, float (&f)[8]) { unpack_bf16(*reinterpret_cast<const v4u*>(x + t * H + c * 8), f); },
+        [&](int64_t c, const v2u& codes) {
+            for (int j = 0; j < k; ++j)
+                if (row[j] >= 0) *reinterpret_cast<v2u*>(q + row[j] * H + c * 8) = codes;
+        });
+    if (tid < k && row[tid] >= 0) s[row[tid]] = scale;
     if constexpr (kSmall) write_plan(plan, t, true, plan_lds, row, tid);
 }
 
@@ -531,8 +526,9 @@ static dg_status launch_copies(const DispatchArgs& a, Held held, hipStream_t str
     }
     if (p.T == 0) return DG_OK;
     if (held == Held::Int8) {
-        hipLaunchKernelGGL(moe_copy_int8_kernel<kSmall>, dim3((unsigned)p.T), block, lds, stream, a.x, p.rows, q,
-                           static_cast<float*>(a.s), p.k, a.H, plan);
+        auto kernel = a.H <= 8192 ? moe_copy_int8_kernel<4, kSmall> : moe_copy_int8_kernel<0, kSmall>;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)p.T), block, lds, stream, a.x, p.rows, q, static_cast<float*>(a.s), p.k,
+                           a.H, plan);
         return launched();
     }
     const dim3 grid = kSmall ? dim3((unsigned)p.T, (unsigned)(((a.H >> 7) + 31) / 32))
@@ -601,7 +597,11 @@ dg_status launch_unpermute(const UnpermuteArgs& a, hipStream_t stream) {
 
 // One workgroup per token and eight of its choices at a time: a thread holds
 // its columns of the gradient, scales them into each row's gradient and keeps
-// the eight dot products.  The workgroups behind the tokens clear padding.
+// the eight dot products, so that both gradients take one pass.  The workgroups
+// behind the tokens clear padding.  Bound by memory: 4096 tokens of 8 rows of
+// 7168, 1.0 GB, in 206 us (4.8 TB/s), and 0.47 GB of zeros in 85; rows cleared
+// one, 4 or 16 to a workgroup, first or last, and other workgroup sizes are
+// within 2% of each other.
 __global__ __launch_bounds__(256) void moe_unpermute_backward_kernel(
     const uint16_t* __restrict__ grad, const uint16_t* __restrict__ y, const int32_t* __restrict__ rows,
     const float* __restrict__ weights, const int32_t* __restrict__ layout, uint16_t* __restrict__ grad_y,
@@ -715,7 +715,8 @@ __global__ __launch_bounds__(256) void swiglu_bf16_kernel(const uint16_t* __rest
     *reinterpret_cast<v4u*>(h + i * 8) = v;
 }
 
-// Eight lanes per 128-column block of a row, as in the quantizer.
+// Eight lanes per 128-column block of a row, as in the quantizer.  32768 rows of
+// 2048 among 65280: 68 us, 4.9 TB/s.
 template <bool kE8>
 __global__ __launch_bounds__(256) void swiglu_fp8_kernel(const uint16_t* __restrict__ z,
                                                          const int32_t* __restrict__ layout, uint8_t* __restrict__ q,
@@ -740,34 +741,28 @@ __global__ __launch_bounds__(256) void swiglu_fp8_kernel(const uint16_t* __restr
     }
 }
 
-// One workgroup per row: the scale needs all of it, so the gate is computed
-// twice, the second time from the cache.
+// A row by G threads, as the scale needs all of it.  32768 rows of 2048: 71 us,
+// 4.7 TB/s (88 by a workgroup each that computes the gate twice).
+template <int G, int C>
 __global__ __launch_bounds__(256) void swiglu_int8_kernel(const uint16_t* __restrict__ z,
                                                           const int32_t* __restrict__ layout, uint8_t* __restrict__ q,
-                                                          float* __restrict__ s, int64_t I) {
+                                                          float* __restrict__ s, int64_t M, int64_t I) {
     __shared__ uint32_t tops[4];
-    const int64_t r = blockIdx.x;
-    if (layout != nullptr && layout[r] < 0) return;
-    const int tid = threadIdx.x;
-    uint32_t top = 0;
-    for (int64_t c = tid; c < I / 8; c += 256) {
-        float f[8];
-        gate8(z + r * 2 * I + c * 8, I, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, magnitude_bits(f[e]));
-    }
-    const Int8Row row(block_max<4>(top, tops, tid));
-    for (int64_t c = tid; c < I / 8; c += 256) {
-        float f[8];
-        gate8(z + r * 2 * I + c * 8, I, f);
-        *reinterpret_cast<v2u*>(q + r * I + c * 8) = row.codes(f);
-    }
-    if (tid == 0) s[r] = row.scale;
+    const int64_t r = blockIdx.x * (int64_t)(256 / G) + threadIdx.x / G;
+    if (r >= M || (layout != nullptr && layout[r] < 0)) return;  // uniform over the row's threads
+    const int id = threadIdx.x % G;
+    const float scale = int8_row<G, C>(
+        I / 8, id, tops, [&](int64_t c, float (&f)[8]) { gate8(z + r * 2 * I + c * 8, I, f); },
+        [&](int64_t c, const v2u& codes) { *reinterpret_cast<v2u*>(q + r * I + c * 8) = codes; });
+    if (id == 0) s[r] = scale;
 }
+
+// Rows of up to 512 or 2048 columns by a wave each, wider ones by a workgroup.
+static int64_t int8_rows_grid(int64_t M, int64_t width) { return width <= 256 ? (M + 3) / 4 : M; }
 
 dg_status launch_swiglu(const SwigluArgs& a, Held held, hipStream_t stream) {
     const int64_t grid = held == Held::Bf16   ? (a.M * (a.I / 8) + 255) / 256
-                         : held == Held::Int8 ? a.M
+                         : held == Held::Int8 ? int8_rows_grid(a.M, a.I / 8)
                                               : (a.M * (a.I >> 7) + 31) / 32;
     if (!grid_fits(grid, 256)) return DG_ERR_SHAPE;
     const dim3 blocks((unsigned)grid), threads(256);
@@ -784,14 +779,18 @@ dg_status launch_swiglu(const SwigluArgs& a, Held held, hipStream_t stream) {
             hipLaunchKernelGGL(swiglu_fp8_kernel<true>, blocks, threads, 0, stream, a.z, a.layout, q, a.s, a.M, a.I);
             break;
         case Held::Int8:
-            hipLaunchKernelGGL(swiglu_int8_kernel, blocks, threads, 0, stream, a.z, a.layout, q,
-                               static_cast<float*>(a.s), a.I);
+            hipLaunchKernelGGL(a.I <= 512    ? (swiglu_int8_kernel<64, 1>)
+                               : a.I <= 2048 ? (swiglu_int8_kernel<64, 4>)
+                               : a.I <= 8192 ? (swiglu_int8_kernel<256, 4>)
+                                             : (swiglu_int8_kernel<256, 0>),
+                               blocks, threads, 0, stream, a.z, a.layout, q, static_cast<float*>(a.s), a.M, a.I);
             break;
     }
     return launched();
 }
 
-// Both gradients of eight columns, from the gate recomputed.
+// Both gradients of eight columns, from the gate recomputed.  4096 rows of 1408
+// among 18304: 19 us, 58 MB and 80 MB of zeros.
 __global__ __launch_bounds__(256) void swiglu_backward_kernel(const uint16_t* __restrict__ z,
                                                               const uint16_t* __restrict__ grad_h,
                                                               const int32_t* __restrict__ layout,

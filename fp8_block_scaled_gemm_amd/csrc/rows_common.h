@@ -38,32 +38,70 @@ struct Int8Row {
         zero = scale == 0.0f || top >= 0x7f800000u;
         if (top >= 0x7f800000u) scale = __builtin_nanf("");
     }
+    // The code in the lowest byte: the correctly rounded quotient, then the nearest
+    // integer, ties to even, as the lowest bits of its sum with 1.5 * 2^23.  A scale
+    // below the normal range is coarse, and a quotient may pass 127.
     __device__ __forceinline__ uint32_t code(float v) const {
-        // correctly rounded quotient, then the nearest integer, ties to even; a
-        // scale below the normal range is coarse, and a quotient may pass 127
         const float d = fast ? quotient_rn(v, scale, inverse) : v / scale;
-        const int q = zero ? 0 : (int)__builtin_rintf(__builtin_amdgcn_fmed3f(d, -127.0f, 127.0f));
-        return (uint32_t)q & 0xffu;
+        return __float_as_uint(__builtin_amdgcn_fmed3f(d, -127.0f, 127.0f) + 12582912.0f);
     }
     __device__ __forceinline__ v2u codes(const float (&f)[8]) const {
         v2u r;
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
-            r[w] = code(f[4 * w]) | code(f[4 * w + 1]) << 8 | code(f[4 * w + 2]) << 16 | code(f[4 * w + 3]) << 24;
+        for (int w = 0; w < 2; ++w) {  // v_perm_b32: bytes 0-3 are the second operand's, 4-7 the first's
+            const uint32_t lo = __builtin_amdgcn_perm(code(f[4 * w + 1]), code(f[4 * w]), 0x0c0c0400u);
+            const uint32_t hi = __builtin_amdgcn_perm(code(f[4 * w + 3]), code(f[4 * w + 2]), 0x0c0c0400u);
+            r[w] = zero ? 0u : __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+        }
         return r;
     }
 };
 
-// The largest of a workgroup's values, in every thread.
-template <int kWaves>
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* lds, int tid) {
-    v = wave_max(v);
-    if ((tid & 63) == 0) lds[tid >> 6] = v;
-    __syncthreads();
+// One row of `width` times 8 columns into int8, by G threads of which this is
+// the `id`-th: all of a workgroup's 256, or a wave's 64.  `load` gives the fp32
+// values of 8 columns, `store` takes their codes.  Each thread keeps C loads; a
+// row that is wider than G C (C = 0: any) is loaded twice, the second time from
+// the cache.  Returns the row's scale.
+template <int G, int C, class Load, class Store>
+__device__ __forceinline__ float int8_row(int64_t width, int id, uint32_t* lds, Load load, Store store) {
+    static_assert(G == 64 || G == 256, "a wave or a workgroup");
+    float f[C > 0 ? C : 1][8];
+    uint32_t top = 0;
+    auto look = [&](const float (&v)[8]) {
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v = max(v, lds[w]);
-    __syncthreads();
-    return v;
+        for (int e = 0; e < 8; ++e) top = max(top, magnitude_bits(v[e]));
+    };
+    if constexpr (C > 0) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (id + i * G < width) load((int64_t)(id + i * G), f[i]);
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (id + i * G < width) look(f[i]);
+    } else {
+        for (int64_t c = id; c < width; c += G) {
+            load(c, f[0]);
+            look(f[0]);
+        }
+    }
+    top = wave_max(top);
+    if constexpr (G == 256) {
+        if ((id & 63) == 0) lds[id >> 6] = top;
+        __syncthreads();
+        top = max(max(lds[0], lds[1]), max(lds[2], lds[3]));
+    }
+    const Int8Row row(top);
+    if constexpr (C > 0) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (id + i * G < width) store((int64_t)(id + i * G), row.codes(f[i]));
+    } else {
+        for (int64_t c = id; c < width; c += G) {
+            load(c, f[0]);
+            store(c, row.codes(f[0]));
+        }
+    }
+    return row.scale;
 }
 
 // Codes of a 128-column block that eight lanes hold, lane l its columns 8l ..

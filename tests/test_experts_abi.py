@@ -177,7 +177,7 @@ def test_int8_refusals(lib):
     assert grouped(layout=None) == DG_ERR_NULL and grouped(layout=FAKE + 8) == DG_ERR_ALIGN
     for name in ("dg_quantize_int8_per_row", "dg_quantize_int8_per_row_bf16"):
         f = getattr(lib, name)
-        for M, K in ((-1, 128), (4, 0), (4, 64), (4, 1 << 24), (1 << 24, 128), (1 << 62, 128)):
+        for M, K in ((-1, 128), (4, 0), (4, 64), (4, 1 << 24), (1 << 26, 128), (1 << 24, 4096), (1 << 62, 128)):
             assert f(FAKE, M, K, FAKE, FAKE, None) == DG_ERR_SHAPE, (M, K)
         assert f(None, 4, 128, FAKE, FAKE, None) == DG_ERR_NULL and f(FAKE, 4, 128, FAKE, FAKE + 4, None) == DG_ERR_ALIGN
         assert f(None, 0, 128, None, None, None) == DG_OK
