@@ -9,8 +9,9 @@
  * dg_ops.h: device pointers to caller-owned, contiguous, row-major memory
  * aligned to 16 bytes; work is enqueued on `stream` and no call synchronizes;
  * arguments are checked on the host, sizes first, then pointers, before
- * anything is enqueued; workspaces as there; outputs overlap no input.  Sums are taken in a fixed order
- * without atomics: the same inputs give the same bits.
+ * anything is enqueued; workspaces as there; outputs overlap no input.  Sums
+ * are taken in a fixed order without atomics: the same inputs give the same
+ * bits.
  */
 #ifndef DG_EXPERTS_H
 #define DG_EXPERTS_H

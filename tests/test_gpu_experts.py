@@ -71,6 +71,7 @@ def test_sort_into_larger_buffers_that_held_other_values():
 DISPATCHES = [  # T, k, E, kind, H
     (1, 8, 256, "own", 7168), (0, 3, 5, "own", 256), (5, 2, 4, "any", 128), (37, 3, 6, "any", 384), (333, 5, 31, "far", 640),
     (61, 20, 7, "any", 1152), (1030, 8, 40, "own", 256), (9, 1, 3, "none", 128),
+    (3, 2, 5, "any", 8320), (130, 33, 6, "any", 8320),
 ]
 
 
@@ -270,7 +271,7 @@ def test_swiglu_and_gradient_match_definition(M, I, with_layout):
 
 
 @pytest.mark.parametrize("kind", ["fp8", "e8m0", "int8"])
-@pytest.mark.parametrize("M,I", [(1, 128), (3, 384), (130, 640), (40, 2048), (33, 8320)])
+@pytest.mark.parametrize("M,I", [(1, 128), (3, 384), (130, 640), (7, 512), (40, 2048), (9, 2176), (5, 8192), (33, 8320)])
 def test_swiglu_quantized_matches_definition(M, I, kind):
     z, layout, _ = gate_case(M, I, M + I)
     zh, on = host(z), layout >= 0

@@ -152,7 +152,7 @@ def exact_rows(A, sa, B, sb, e):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("M,K", [(1, 128), (5, 384), (130, 2048), (3, 7168), (7, 16512)])
+@pytest.mark.parametrize("M,K", [(1, 128), (5, 384), (6, 512), (7, 640), (130, 2048), (9, 2176), (3, 7168), (5, 8192), (7, 16512)])
 def test_quantizer_matches_recipe(M, K, dtype):
     rng = np.random.default_rng(M + K)
     x = torch.from_numpy((rng.standard_normal((M, K)) * np.exp(5 * rng.standard_normal((M, 1)))).astype(np.float32))
