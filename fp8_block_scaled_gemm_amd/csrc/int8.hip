@@ -40,11 +40,18 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 // about (78); 32 x 32 x 32 products (64); the loads at the second phase's
 // beginning instead of spread over it (59-60); a barrier in the middle of the
 // first phase for earlier loads (62).
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int S_, int GROUP_M_>
+//
+// Where few tiles leave CUs without one, a K block's latency bounds a tile, and
+// PARTS groups of waves with stages of their own take every PARTS-th block each;
+// their sums, exact in any order, are added in LDS at the end.  64 x 512 x 7168:
+// 7.8 us in 32 x 32 by two groups of two waves (8.2 by four; a group of four
+// waves alone: 11.4 in 64 x 32, two 10.2).
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int S_, int GROUP_M_, int PARTS_ = 1>
 struct Int8Tile {
     static constexpr int BM = BM_, BN = BN_, S = S_;
     static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, kWaves = WAVES_M * WAVES_N;
-    static constexpr int kThreads = 64 * kWaves, kGroupM = GROUP_M_;
+    static constexpr int kThreads = 64 * kWaves, kGroupM = GROUP_M_;  // of a group
+    static constexpr int kParts = PARTS_, kAllThreads = kThreads * kParts;
     static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 16, TN = WN / 16;  // of a wave
     static constexpr int kStage = (BM + BN) * 128;
     static constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = (BN / 8 + kWaves - 1) / kWaves;
@@ -52,7 +59,10 @@ struct Int8Tile {
     static constexpr bool kUneven = BN / 8 % kWaves != 0;
     // the bf16 output tile on its way out: row pitch in 16-byte chunks
     static constexpr int kPitchChunks = BN <= 128 ? 16 : 32;
-    static constexpr int kSmem = S * kStage > BM * kPitchChunks * 16 ? S * kStage : BM * kPitchChunks * 16;
+    static constexpr int kOut = BM * kPitchChunks * 16;
+    static constexpr int kSums = (kParts - 1) * kThreads * TM * TN * 16;  // of the other groups, behind it
+    static constexpr int kStages = kParts * S * kStage;
+    static constexpr int kSmem = kStages > kOut + kSums ? kStages : kOut + kSums;
     static_assert(WM % 16 == 0 && WN % 16 == 0 && BN <= 256, "whole sub-tiles, output pitch");
     static_assert(BM % (8 * kWaves) == 0 && BN % 8 == 0 && (!kUneven || S == 2), "waits count every wave's loads");
     static_assert(kSmem <= 160 * 1024 && kLoads * (S - 1) < 64, "LDS, vmcnt range");
@@ -71,7 +81,9 @@ struct Int8Operands {
 // masks are stored.  LDS is free again when every wave has come back.
 template <class T, bool kRouted>
 __device__ __forceinline__ void int8_tile(const Int8Operands& p, const TileInfo& ti, uint8_t* smem, int tid) {
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % T::kWaves;
+    const int part = T::kParts > 1 ? __builtin_amdgcn_readfirstlane(tid >> 6) / T::kWaves : 0;
+    uint8_t* const own = smem + part * (T::S * T::kStage);
     const int lane = tid & 63;
     const uint32_t K = (uint32_t)p.K;  // below 2^17: a tile's rows are addressed with 32-bit offsets
     const int KB = (int)(K >> 7);
@@ -84,13 +96,14 @@ __device__ __forceinline__ void int8_tile(const Int8Operands& p, const TileInfo&
     const int vn = (int)min<int64_t>(T::BN, p.N - ti.n0);
     const uint8_t* const tileA = p.A + ti.arow0 * p.K;
     const uint8_t* const tileB = p.B + ((int64_t)ti.g * p.N + ti.n0) * p.K;
-    // a wave's loads [q0, q1) of block kb: rows [8 (wave + kWaves q), +8) of A,
+    // a wave's loads [q0, q1) of its group's block i: rows [8 (wave + kWaves q), +8) of A,
     // then of B; blocks past the last one get an empty buffer, and so count like
     // the others
-    auto issue = [&](int kb, int st, int q0, int q1) __attribute__((always_inline)) {
+    auto issue = [&](int i, int st, int q0, int q1) __attribute__((always_inline)) {
+        const int kb = i * T::kParts + part;
         const v4u ra = buffer_rsrc(tileA + kb * 128, kb < KB ? (uint32_t)ti.valid * K - kb * 128 : 0u);
         const v4u rb = buffer_rsrc(tileB + kb * 128, kb < KB ? (uint32_t)vn * K - kb * 128 : 0u);
-        uint8_t* const to = smem + st * T::kStage + wave * 1024;
+        uint8_t* const to = own + st * T::kStage + wave * 1024;
         constexpr int kRows = 8 * T::kWaves;  // of a load of every wave
 #pragma unroll
         for (int q = q0; q < q1; ++q) {
@@ -114,7 +127,7 @@ __device__ __forceinline__ void int8_tile(const Int8Operands& p, const TileInfo&
     };
     // the products of one set, a row of sub-tiles at a time, with the next
     // set's reads (and, kLoad, the loads of a block) between them
-    auto phase = [&](auto which, const uint8_t* next, int chunk, auto load, int kb, int st) __attribute__((always_inline)) {
+    auto phase = [&](auto which, const uint8_t* next, int chunk, auto load, int block, int st) __attribute__((always_inline)) {
         constexpr int set = decltype(which)::value;
         constexpr bool kLoad = decltype(load)::value;
         constexpr int kRead = (T::TN + T::TM + T::TM - 1) / T::TM;  // reads a row
@@ -128,7 +141,7 @@ __device__ __forceinline__ void int8_tile(const Int8Operands& p, const TileInfo&
                 else if (r < T::TN + T::TM)
                     read_a(next, chunk, set ^ 1, r - T::TN);
             }
-            if constexpr (kLoad) issue(kb, st, min(i * kEach, T::kLoads), min((i + 1) * kEach, T::kLoads));
+            if constexpr (kLoad) issue(block, st, min(i * kEach, T::kLoads), min((i + 1) * kEach, T::kLoads));
 #pragma unroll
             for (int j = 0; j < T::TN; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[set][j], a[set][i], acc[i][j], 0, 0, 0);
@@ -143,22 +156,38 @@ __device__ __forceinline__ void int8_tile(const Int8Operands& p, const TileInfo&
     wait_vmcnt<T::kUneven ? 0 : T::kLoads*(T::S - 1)>();
     lds_barrier();
 #pragma unroll
-    for (int j = 0; j < T::TN; ++j) read_b(smem, chunk_lo, 0, j);
+    for (int j = 0; j < T::TN; ++j) read_b(own, chunk_lo, 0, j);
 #pragma unroll
-    for (int i = 0; i < T::TM; ++i) read_a(smem, chunk_lo, 0, i);
+    for (int i = 0; i < T::TM; ++i) read_a(own, chunk_lo, 0, i);
     int st = 0;
-    for (int kb = 0; kb < KB; ++kb) {
+    for (int i = 0; i * T::kParts < KB; ++i) {
         const int nx = st + 1 == T::S ? 0 : st + 1;
-        phase(First{}, smem + st * T::kStage, chunk_hi, std::false_type{}, 0, 0);
+        phase(First{}, own + st * T::kStage, chunk_hi, std::false_type{}, 0, 0);
         wait_vmcnt_lgkm0<T::kLoads*(T::S - 2)>();  // the stage has been read, the next block's has landed
         lds_barrier();
-        phase(Second{}, smem + nx * T::kStage, chunk_lo, std::true_type{}, kb + T::S, st);
+        phase(Second{}, own + nx * T::kStage, chunk_lo, std::true_type{}, i + T::S, st);
         st = nx;
     }
     wait_vmcnt_lgkm0<0>();  // the empty loads of the last blocks have retired
     lds_barrier();
 
-    // epilogue: scales by row and column, rounding, and out through LDS
+    if constexpr (T::kParts > 1) {
+        v4i* const sums = reinterpret_cast<v4i*>(smem + T::kOut) + wave * 64 * T::TM * T::TN + lane;
+        auto at = [&](int p, int i, int j) { return (p - 1) * T::kThreads * T::TM * T::TN + (i * T::TN + j) * 64; };
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < T::TN; ++j)
+                if (part > 0) sums[at(part, i, j)] = acc[i][j];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < T::TN; ++j)
+                for (int p = 1; p < T::kParts && part == 0; ++p) acc[i][j] += sums[at(p, i, j)];
+    }
+
+    // epilogue, of the first group: scales by row and column, rounding, and out through LDS
     v4f col_scale[T::TN];
 #pragma unroll
     for (int j = 0; j < T::TN; ++j) {
@@ -166,7 +195,7 @@ __device__ __forceinline__ void int8_tile(const Int8Operands& p, const TileInfo&
         col_scale[j] = *reinterpret_cast<const v4f*>(p.sb + (int64_t)ti.g * p.N + col);
     }
 #pragma unroll
-    for (int i = 0; i < T::TM; ++i) {
+    for (int i = 0; i < T::TM && part == 0; ++i) {
         const int row = wrow + 16 * i + lr;
         const float row_scale = p.sa[ti.arow0 + min(row, ti.valid - 1)];
 #pragma unroll
@@ -178,16 +207,16 @@ __device__ __forceinline__ void int8_tile(const Int8Operands& p, const TileInfo&
         }
     }
     __syncthreads();
-    store_staged<T, kRouted>(smem, tid, ti, p.D, p.N);
+    if (part == 0) store_staged<T, kRouted>(smem, tid, ti, p.D, p.N);
 }
 
 // The dense form: tiles of shape T over columns [0, split), of shape U behind
 // them, whose workgroups (from `first` on) come last.  Two shapes may leave less
 // of the last round idle than one.
 template <class T, class U>
-__global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_gemm_kernel(Int8Operands p, int64_t rows, int64_t split,
-                                                                               unsigned first) {
-    static_assert(T::kThreads == U::kThreads, "one workgroup size");
+__global__ __launch_bounds__(T::kAllThreads, T::kAllThreads / 256) void int8_gemm_kernel(Int8Operands p, int64_t rows,
+                                                                                         int64_t split, unsigned first) {
+    static_assert(T::kAllThreads == U::kAllThreads, "one workgroup size");
     extern __shared__ __align__(1024) uint8_t smem[];
     auto run = [&](auto shape, int block, int64_t from, int64_t to) __attribute__((always_inline)) {
         using X = decltype(shape);
@@ -232,6 +261,7 @@ __global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_grouped_kerne
     static_assert(T::BM == 128 && T2::BM == 128 && T4::BM == 128, "one group per 128-row block");
     static_assert(T2::BN * 2 == T::BN && T4::BN * 4 == T::BN, "halves and quarters");
     static_assert(T::kThreads == T2::kThreads && T::kThreads == T4::kThreads, "one workgroup size");
+    static_assert(T::kParts == 1 && T2::kParts == 1 && T4::kParts == 1, "every thread takes part in a tile");
     constexpr int kWindow = 4096;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint16_t used[kWindow / 16];  // a bit per block: whether it holds a row
@@ -289,7 +319,6 @@ __global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_grouped_kerne
             ti.n0 = (int)(t % n_blocks) * T::BN + part * X::BN;
             if (ti.n0 >= p.N) return;
             ti.arow0 = ti.m0;
-            ti.valid = 128;
             // once per id among the block's rows, the largest first
             const int id0 = layout[ti.m0 + lane], id1 = layout[ti.m0 + 64 + lane];
             for (int64_t below = G;;) {
@@ -299,6 +328,8 @@ __global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_grouped_kerne
                 if (ti.g < 0) break;
                 ti.ok0 = __ballot(id0 == ti.g);
                 ti.ok1 = __ballot(id1 == ti.g);
+                // rows behind the id's last one are not loaded
+                ti.valid = ti.ok1 != 0 ? 128 - __builtin_clzll(ti.ok1) : 64 - __builtin_clzll(ti.ok0);
                 int8_tile<X, true>(p, ti, smem, tid);
                 __syncthreads();  // the staged tile has been stored before the next loads
                 below = ti.g;
@@ -319,10 +350,10 @@ static dg_status launch_tiled(const Int8Args& a, int64_t split, hipStream_t stre
         return ((a.rows + bm - 1) / bm * ((columns + bn - 1) / bn) + kNumXcds - 1) / kNumXcds * kNumXcds;
     };
     const int64_t first = tiles(T::BM, T::BN, split), grid = first + tiles(U::BM, U::BN, a.N - split);
-    if (!grid_fits(grid, T::kThreads)) return DG_ERR_SHAPE;
+    if (!grid_fits(grid, T::kAllThreads)) return DG_ERR_SHAPE;
     const Int8Operands p{reinterpret_cast<const uint8_t*>(a.A), a.sa, reinterpret_cast<const uint8_t*>(a.B), a.sb, a.D,
                          a.N, a.K};
-    hipLaunchKernelGGL((int8_gemm_kernel<T, U>), dim3((unsigned)grid), dim3(T::kThreads),
+    hipLaunchKernelGGL((int8_gemm_kernel<T, U>), dim3((unsigned)grid), dim3(T::kAllThreads),
                        T::kSmem > U::kSmem ? T::kSmem : U::kSmem, stream, p, a.rows, split, (unsigned)first);
     return launched();
 }
@@ -416,6 +447,7 @@ using Int8Square128 = Int8Tile<128, 128, 2, 4, 4, 8>;
 using Int8Tall64 = Int8Tile<128, 64, 2, 2, 4, 8>;
 using Int8Square64 = Int8Tile<64, 64, 2, 2, 4, 8>;
 using Int8Narrow = Int8Tile<64, 32, 2, 2, 4, 8>;
+using Int8Parted = Int8Tile<32, 32, 2, 1, 4, 8, 2>;
 using Int8Quarter = Int8Tile<128, 64, 4, 2, 4, 8>;  // of Int8Rows128; Int8Square128 is half of it
 
 static dg_status launch_grouped(const Int8Args& a, hipStream_t stream) {
@@ -440,13 +472,15 @@ dg_status launch_int8_gemm(const Int8Args& a, hipStream_t stream) {
     // several (4096 x 7168 x 2048, 8192^3).
     struct Shape { int bm, bn, ns; };
     static const Shape kShapes[] = {{256, 256, 1580}, {256, 192, 1250}, {256, 160, 1070}, {128, 256, 890},
-                                    {128, 128, 530},  {128, 64, 320},   {64, 64, 200},    {64, 32, 155}};
+                                    {128, 128, 530},  {128, 64, 320},   {64, 64, 200},    {64, 32, 155},
+                                    {32, 32, 88}};
     auto rounds = [&](const Shape& sh, int64_t columns) {
         return ((a.rows + sh.bm - 1) / sh.bm * ((columns + sh.bn - 1) / sh.bn) + cus - 1) / cus;
     };
     int best = 0;
     int64_t least = INT64_MAX, split = a.N;
-    for (int i = 0; i < 8; ++i) {
+    const int shapes = a.K < 640 ? 8 : 9;  // adding up parts takes 0.2 us, three K blocks' time
+    for (int i = 0; i < shapes; ++i) {
         const int64_t cost = rounds(kShapes[i], a.N) * kShapes[i].ns;
         if (cost < least) {
             least = cost;
@@ -462,7 +496,7 @@ dg_status launch_int8_gemm(const Int8Args& a, hipStream_t stream) {
         const int64_t cost = whole * kShapes[0].ns + rounds(kShapes[i], a.N - at) * kShapes[i].ns;
         if (cost < least) {
             least = cost;
-            best = 7 + i;
+            best = 8 + i;
             split = at;
         }
     }
@@ -475,7 +509,8 @@ dg_status launch_int8_gemm(const Int8Args& a, hipStream_t stream) {
         case 5: return launch_tiled<Int8Tall64, Int8Tall64>(a, split, stream);
         case 6: return launch_tiled<Int8Square64, Int8Square64>(a, split, stream);
         case 7: return launch_tiled<Int8Narrow, Int8Narrow>(a, split, stream);
-        case 8: return launch_tiled<Int8Large, Int8Wide192>(a, split, stream);
+        case 8: return launch_tiled<Int8Parted, Int8Parted>(a, split, stream);
+        case 9: return launch_tiled<Int8Large, Int8Wide192>(a, split, stream);
         default: return launch_tiled<Int8Large, Int8Wide160>(a, split, stream);
     }
 }

@@ -28,6 +28,7 @@ def operands(rng, M, N, K, G=None):
 
 DENSE = [(1, 8, 128), (1, 7168, 2048), (2, 40, 384), (3, 520, 1152), (5, 1032, 256), (7, 24, 5120), (8, 264, 640),
          (9, 264, 640), (15, 136, 256), (16, 72, 1024), (17, 1000, 384), (31, 8, 2176), (33, 328, 512), (64, 2112, 7168),
+         (32, 40, 128), (64, 512, 7168), (40, 8, 8320), (255, 1016, 640),
          (100, 264, 256), (127, 56, 128), (129, 520, 384), (256, 256, 128), (257, 264, 256), (300, 4104, 640),
          (512, 8192, 256), (1000, 2064, 384), (2049, 4088, 128), (4096, 2112, 256),
          # 192 and 160 columns behind a round of 256 (256 CUs)
