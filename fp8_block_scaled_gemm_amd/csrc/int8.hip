@@ -184,7 +184,9 @@ __device__ __forceinline__ void int8_tile(const Int8Operands& p, const TileInfo&
         for (int i = 0; i < T::TM; ++i)
 #pragma unroll
             for (int j = 0; j < T::TN; ++j)
-                for (int p = 1; p < T::kParts && part == 0; ++p) acc[i][j] += sums[at(p, i, j)];
+#pragma unroll
+                for (int p = 1; p < T::kParts; ++p)
+                    if (part == 0) acc[i][j] += sums[at(p, i, j)];
     }
 
     // epilogue, of the first group: scales by row and column, rounding, and out through LDS
@@ -195,7 +197,8 @@ __device__ __forceinline__ void int8_tile(const Int8Operands& p, const TileInfo&
         col_scale[j] = *reinterpret_cast<const v4f*>(p.sb + (int64_t)ti.g * p.N + col);
     }
 #pragma unroll
-    for (int i = 0; i < T::TM && part == 0; ++i) {
+    for (int i = 0; i < T::TM; ++i) {
+        if (part > 0) continue;
         const int row = wrow + 16 * i + lr;
         const float row_scale = p.sa[ti.arow0 + min(row, ti.valid - 1)];
 #pragma unroll
@@ -253,18 +256,24 @@ __global__ __launch_bounds__(T::kAllThreads, T::kAllThreads / 256) void int8_gem
 // are shared out evenly: with one workgroup per tile of the buffer, in order,
 // 4096 rows in a buffer of 33664 were left to one of the 8 XCDs (829 us for 8
 // experts of 4096 x 7168).  Tiles that are left over behind the whole rounds are
-// cut in two (T2) or four (T4) where that takes less than a round of whole ones.
-template <class T, class T2, class T4>
+// cut in two (T2) or four (T4) where that takes less than a round of whole ones,
+// and blocks of few rows in eight (T8: fewer rows, K in parts).  Rows behind an
+// id's last one in a block are not loaded (16 blocks of 8 rows, 1024 x 7168: 24.7
+// us, 39.6 with them).
+template <class T, class T2, class T4, class T8>
 __global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_grouped_kernel(Int8Operands p,
                                                                                   const int32_t* __restrict__ layout,
                                                                                   int64_t rows, int64_t G) {
-    static_assert(T::BM == 128 && T2::BM == 128 && T4::BM == 128, "one group per 128-row block");
-    static_assert(T2::BN * 2 == T::BN && T4::BN * 4 == T::BN, "halves and quarters");
-    static_assert(T::kThreads == T2::kThreads && T::kThreads == T4::kThreads, "one workgroup size");
-    static_assert(T::kParts == 1 && T2::kParts == 1 && T4::kParts == 1, "every thread takes part in a tile");
+    static_assert(T::BM == 128 && T2::BM == 128 && T4::BM == 128 && T8::BM < 128, "one group per 128-row block");
+    static_assert(T::kSmem >= T2::kSmem && T::kSmem >= T4::kSmem && T::kSmem >= T8::kSmem, "LDS of every shape");
+    static_assert(T2::BN * 2 == T::BN && T4::BN * 4 == T::BN && T8::BN * 8 == T::BN, "halves, quarters and eighths");
+    static_assert(T::kAllThreads == T2::kAllThreads && T::kAllThreads == T4::kAllThreads &&
+                      T::kAllThreads == T8::kAllThreads,
+                  "one workgroup size");
     constexpr int kWindow = 4096;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint16_t used[kWindow / 16];  // a bit per block: whether it holds a row
+    __shared__ int deep[T::kWaves];                       // of a wave's blocks: whether one holds a row from T8::BM on
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t m_blocks = rows / 128;
     const int n_blocks = (int)((p.N + T::BN - 1) / T::BN);
@@ -273,6 +282,7 @@ __global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_grouped_kerne
         const int blocks = (int)min<int64_t>(kWindow, m_blocks - w0), words = (blocks + 63) / 64;
         // a load covers two blocks, 32 lanes of four ids each; eight loads at once,
         // those past the last block of its own ids again
+        uint64_t lower = 0;
         for (int b0 = wave * 16; b0 < words * 64; b0 += T::kWaves * 16) {
             int4 id[8];
 #pragma unroll
@@ -285,12 +295,17 @@ __global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_grouped_kerne
             for (int i = 0; i < 8; ++i) {
                 auto valid = [&](int e) { return (uint32_t)e < (uint32_t)G; };
                 const uint64_t any = __ballot(valid(id[i].x) || valid(id[i].y) || valid(id[i].z) || valid(id[i].w));
+                lower |= any & ~(((uint64_t(1) << (T8::BM / 4)) - 1) * 0x100000001ull);
                 bits |= (((uint32_t)any != 0 ? 1u : 0u) | ((any >> 32) != 0 ? 2u : 0u)) << (2 * i);
             }
             bits &= b0 >= blocks ? 0u : blocks - b0 >= 16 ? 0xffffu : (1u << (blocks - b0)) - 1u;
             if (lane == 0) used[b0 / 16] = (uint16_t)bits;
         }
+        if (lane == 0) deep[wave] = lower != 0;
         __syncthreads();
+        int shallow = 1;
+#pragma unroll
+        for (int w = 0; w < T::kWaves; ++w) shallow &= deep[w] == 0;
         // lane l holds word l of the window's blocks, and how many are used up to its end
         const uint64_t word = lane < words ? reinterpret_cast<const uint64_t*>(used)[lane] : 0;
         int upto = __popcll(word);
@@ -304,7 +319,11 @@ __global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_grouped_kerne
         const int left = (int)(tiles % grid);
         // us a K block and round: 0.95 whole, 0.6 halves, 0.43 quarters
         const int cost2 = (2 * left + grid - 1) / grid * 60, cost4 = (4 * left + grid - 1) / grid * 43;
-        const int cut = left == 0 || min(cost2, cost4) >= 95 ? 1 : cost2 <= cost4 ? 2 : 4;
+        // eighths of the first 32 rows, if no block has more and they take one
+        // round (12 blocks of 512 x 7168: 13.4 us, 20.8 in quarters; more rounds
+        // gain nothing)
+        const bool eighths = __builtin_amdgcn_readfirstlane(shallow) != 0 && 8 * tiles <= grid;
+        const int cut = eighths ? 8 : left == 0 || min(cost2, cost4) >= 95 ? 1 : cost2 <= cost4 ? 2 : 4;
         const int64_t whole = cut > 1 ? tiles - left : tiles;
         auto run = [&](auto shape, int64_t t, int part) __attribute__((always_inline)) {
             using X = decltype(shape);
@@ -340,6 +359,8 @@ __global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void int8_grouped_kerne
             for (int i = blockIdx.x; i < left * 2; i += grid) run(T2{}, whole + i / 2, i % 2);
         else if (cut == 4)
             for (int i = blockIdx.x; i < left * 4; i += grid) run(T4{}, whole + i / 4, i % 4);
+        else if (cut == 8)
+            for (int i = blockIdx.x; i < left * 8; i += grid) run(T8{}, whole + i / 8, i % 8);
         __syncthreads();  // the bits have been read
     }
 }
@@ -448,15 +469,17 @@ using Int8Tall64 = Int8Tile<128, 64, 2, 2, 4, 8>;
 using Int8Square64 = Int8Tile<64, 64, 2, 2, 4, 8>;
 using Int8Narrow = Int8Tile<64, 32, 2, 2, 4, 8>;
 using Int8Parted = Int8Tile<32, 32, 2, 1, 4, 8, 2>;
-using Int8Quarter = Int8Tile<128, 64, 4, 2, 4, 8>;  // of Int8Rows128; Int8Square128 is half of it
+using Int8Quarter = Int8Tile<128, 64, 4, 2, 4, 8>;   // of Int8Rows128; Int8Square128 is half of it
+using Int8Eighth = Int8Tile<32, 32, 2, 1, 4, 8, 4>;  // of its first 32 rows
 
 static dg_status launch_grouped(const Int8Args& a, hipStream_t stream) {
     using T = Int8Rows128;
-    const int64_t tiles = a.rows / 128 * ((a.N + T::BN - 1) / T::BN) * 4;
+    const int64_t tiles = a.rows / 128 * ((a.N + T::BN - 1) / T::BN) * 8;
     const Int8Operands p{reinterpret_cast<const uint8_t*>(a.A), a.sa, reinterpret_cast<const uint8_t*>(a.B), a.sb, a.D,
                          a.N, a.K};
-    hipLaunchKernelGGL((int8_grouped_kernel<T, Int8Square128, Int8Quarter>), dim3((unsigned)std::min<int64_t>(tiles, device_cus())),
-                       dim3(T::kThreads), T::kSmem, stream, p, a.layout, a.rows, a.G);
+    hipLaunchKernelGGL((int8_grouped_kernel<T, Int8Square128, Int8Quarter, Int8Eighth>),
+                       dim3((unsigned)std::min<int64_t>(tiles, device_cus())), dim3(T::kThreads), T::kSmem, stream, p,
+                       a.layout, a.rows, a.G);
     return launched();
 }
 

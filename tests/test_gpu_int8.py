@@ -84,7 +84,9 @@ def test_scales_that_are_not_finite_stay_in_their_rows_and_columns(M):
 GROUPED = [(3, 264, 384, [100, 0, 200]), (1, 8, 128, [1]), (5, 520, 256, [128, 1, 127, 0, 130]), (8, 4096, 256, [3] * 8),
            (16, 1032, 640, [5, 0, 300, 17, 128, 64, 0, 0, 90, 33, 12, 1, 2, 16, 31, 257]), (2, 2048, 2048, [700, 900]),
            # left-over tiles as they are, and behind a whole round in halves and in quarters (256 CUs)
-           (2, 2048, 256, [1300, 1250]), (3, 2056, 128, [2000, 1500, 1700]), (2, 2048, 128, [2500, 2400])]
+           (2, 2048, 256, [1300, 1250]), (3, 2056, 128, [2000, 1500, 1700]), (2, 2048, 128, [2500, 2400]),
+           # at most 32 rows a block, and one more
+           (4, 264, 128, [32, 1, 0, 7]), (3, 520, 7168, [32, 31, 5]), (3, 1288, 640, [2, 33, 1]), (9, 1024, 384, [9] * 9)]
 
 
 def grouped_case(G, N, K, counts, seed):
@@ -122,6 +124,20 @@ def test_grouped_blocks_that_mix_ids(N):
     layout[128:256] = rng.integers(-3, 8, 128)  # several, and some that are none
     layout[300] = 4
     D = torch.full((layout.size, N), SENTINEL, dtype=torch.int16, device="cuda")
+    dg.dg_int8_gemm_grouped_contiguous(to_dev(A), to_dev(sa), to_dev(B), to_dev(sb), D, to_dev(layout))
+    check_grouped(D, A, sa, B, sb, layout)
+
+
+@pytest.mark.parametrize("rows", [32, 33])
+def test_grouped_blocks_that_mix_ids_in_their_first_rows(rows):
+    A, sa, B, sb, layout = grouped_case(5, 264, 384, [128, 100, 0, 256, 30], 9)
+    rng = np.random.default_rng(rows)
+    ids = np.full((layout.size // 128, 128), -1, np.int32)
+    ids[:4, :rows] = rng.integers(-3, 8, (4, rows))
+    ids[2, :rows] = 2 ** 31 - 1
+    ids[0, rows - 1] = 4
+    layout = ids.reshape(-1)
+    D = torch.full((layout.size, 264), SENTINEL, dtype=torch.int16, device="cuda")
     dg.dg_int8_gemm_grouped_contiguous(to_dev(A), to_dev(sa), to_dev(B), to_dev(sb), D, to_dev(layout))
     check_grouped(D, A, sa, B, sb, layout)
 
