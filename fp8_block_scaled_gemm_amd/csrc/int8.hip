@@ -384,10 +384,10 @@ static dg_status launch_tiled(const Int8Args& a, int64_t split, hipStream_t stre
 // each, straight from memory into fragments (a lane's two operands of a block
 // are 32 bytes of its row, so that a wave reads whole lines), without a barrier
 // before the shares of the sums, which are exact in any order, are added in LDS.
-// 1 x 7168 x 2048: 5.7 us, 5.9 in the narrowest tiles, of which a launch alone
-// takes 2.5 and 15 MB at a copy's rate 3; 1 x 2112 x 7168, where those tiles are
-// few and their K blocks follow each other: 6.4 against 11.4.  With 32 rows, two
-// fragments of A for one of B, it gained nothing (11.9 against 11.6).
+// 1 x 7168 x 2048: 5.1 us, of which a launch alone takes 2.5 and 15 MB at a
+// copy's rate 3 (17 rows in tiles: 5.5); 1 x 2112 x 7168 6.3, 8 x 4096 x 7168
+// 7.6 (20 and 32 rows in tiles: 7.8 and 8.5).  With two or four row tiles its
+// loads, 16 bytes of a row a lane, bound it (64 x 2112 x 7168: 15 and 22 us).
 template <int CN>
 __global__ __launch_bounds__(512) void int8_few_rows_kernel(const uint8_t* __restrict__ A, const float* __restrict__ sa,
                                                             const uint8_t* __restrict__ B, const float* __restrict__ sb,
