@@ -502,7 +502,9 @@ dg_status launch_int8_gemm(const Int8Args& a, hipStream_t stream) {
     };
     int best = 0;
     int64_t least = INT64_MAX, split = a.N;
-    const int shapes = a.K < 640 ? 8 : 9;  // adding up parts takes 0.2 us, three K blocks' time
+    // not the last one for short sums, as adding up its parts takes 0.2 us, three
+    // K blocks' time, nor in a second round (96 x 5000 x 2048: 7.0 us for 6.7)
+    const int shapes = a.K < 640 || rounds(kShapes[8], a.N) > 1 ? 8 : 9;
     for (int i = 0; i < shapes; ++i) {
         const int64_t cost = rounds(kShapes[i], a.N) * kShapes[i].ns;
         if (cost < least) {
