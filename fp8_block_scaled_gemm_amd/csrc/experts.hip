@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "layout_share.h"
 #include "rows_common.h"
 
 namespace dg {
@@ -116,23 +117,24 @@ __device__ __forceinline__ int expert_of(const int* offsets, int E, int r) {
     return lo;
 }
 
-// layout of M rows, by `waves` waves of which this is the `wave`-th, from the
-// experts' offsets and sizes (LDS): the experts that have pairs are dealt out to
-// the waves, several to an expert's blocks where there are more waves than
-// experts, and then the rows behind the last expert's.  (A search for each
-// block's expert took 10 of 15 us where one workgroup sorts 512 pairs of 256
-// experts.)
+// layout of M rows, by `waves` waves (at most kLayoutWaves) of which this is the
+// `wave`-th, from the experts' offsets and sizes (LDS): the experts that have
+// pairs are dealt out to the waves, several to an expert's blocks where there
+// are more waves than experts, and then the rows behind the last expert's.  (A
+// search for each block's expert took 10 of 15 us where one workgroup sorts 512
+// pairs of 256 experts.)
 __device__ __forceinline__ void write_layout(const int* offsets, const int* size, int E, int64_t M, int wave, int waves,
                                              int32_t* __restrict__ layout, int lane) {
     auto blocks = [&](int e, int begin, int step) {
         const int first = offsets[e], n = size[e];
-        for (int r = begin * 128; r < n; r += step * 128) {
+        each_block(n, begin, step, [&](int r) {
             const int at = r + 2 * lane;
             *reinterpret_cast<int2*>(layout + first + at) = int2{at < n ? e : -1, at + 1 < n ? e : -1};
-        }
+        });
     };
     if (waves > E) {
-        blocks(wave % E, wave / E, (waves - 1 - wave % E) / E + 1);
+        const BlockShare s = block_share(wave, waves, E);
+        blocks(s.expert, s.begin, s.step);
     } else {
         int turn = wave;  // used experts until this wave's next one
         for (int e0 = 0; e0 < E; e0 += 64) {
@@ -145,8 +147,8 @@ __device__ __forceinline__ void write_layout(const int* offsets, const int* size
             turn -= __popcll(used);
         }
     }
-    for (int64_t r = offsets[E] + (int64_t)(wave * 64 + lane) * 4; r < M; r += (int64_t)waves * 256)
-        *reinterpret_cast<int4*>(layout + r) = int4{-1, -1, -1, -1};
+    each_rest(offsets[E], M, wave, waves, lane,
+              [&](int64_t r) { *reinterpret_cast<int4*>(layout + r) = int4{-1, -1, -1, -1}; });
 }
 
 // Sum over 16 byte counts of one expert: those of the waves before `wave`, and
@@ -332,8 +334,9 @@ __device__ __forceinline__ void write_plan(const SmallSort& p, int64_t t, bool f
     if (first_part && tid < p.k && t * p.k + tid < p.P) p.rows[t * p.k + tid] = row[tid];
     if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int e = tid; e <= p.E; e += 256) p.offsets[e] = offsets[e];
-    const int wg = blockIdx.y * gridDim.x + blockIdx.x;
-    write_layout(offsets, size, p.E, p.M, wg * 4 + (tid >> 6), gridDim.x * gridDim.y * 4, p.layout, tid & 63);
+    const unsigned wg = blockIdx.y * gridDim.x + blockIdx.x;  // of at most 2^24
+    const int waves = layout_waves(gridDim.x * gridDim.y, 4), wave = (int)(wg * 4 + (tid >> 6));
+    if (wave < waves) write_layout(offsets, size, p.E, p.M, wave, waves, p.layout, tid & 63);
 }
 
 // bf16 rows: a thread copies 8 columns of a token into each of its rows.  The
