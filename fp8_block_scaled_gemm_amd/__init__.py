@@ -378,7 +378,8 @@ def dg_quantize_fp8_per_block_e8m0(x, q=None, s=None):
 
 # Argument checks, allocation and the call itself run in _binding.so
 # (csrc/binding.cpp): these operators take microseconds, and checking ten
-# tensors in Python took as long as they do.
+# tensors in Python took as long as they do.  None of them has a forward-mode
+# derivative: a dual tensor's tangent is refused where a new output would lose it.
 
 _SCORING = {"softmax": 0, "sigmoid": 1}
 _native = None
@@ -436,7 +437,7 @@ def _score_mode(scoring):
 
 
 def _warn_no_grad(name, where, depth=3):
-    warnings.warn(f"{name} records no gradient {where}, though an argument requires one", stacklevel=depth)
+    warnings.warn(f"{name} records no gradient {where}, though an argument requires one or has a tangent", stacklevel=depth)
 
 
 class _Topk(torch.autograd.Function):

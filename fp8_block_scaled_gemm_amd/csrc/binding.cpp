@@ -13,6 +13,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -604,11 +605,16 @@ PyObject* quantize_int8(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
-// Whether gradients are recorded and any of the arguments is a tensor that requires one.
+// Whether any of the arguments is a tensor that requires a gradient where those
+// are recorded, or carries a forward-mode tangent, which the calls' functions
+// refuse (a plain call would drop it).
 PyObject* wants_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (c10::GradMode::is_enabled())
-        for (Py_ssize_t i = 0; i < n; ++i)
-            if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad()) Py_RETURN_TRUE;
+    const bool backward = c10::GradMode::is_enabled(), forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (!THPVariable_Check(a[i])) continue;
+        const at::Tensor& t = THPVariable_Unpack(a[i]);
+        if ((backward && t.requires_grad()) || (forward && t._fw_grad(0).defined())) Py_RETURN_TRUE;
+    }
     Py_RETURN_FALSE;
 }
 
