@@ -611,9 +611,13 @@ def dg_moe_dispatch(x, ids, E, out=None, rows=None, layout=None, offsets=None, w
 
 def _no_grad_rows(name, call, x, q, s):
     """A quantizing call whose input requires a gradient: new outputs refuse to
-    pass one back, given ones warn."""
+    pass one back, given ones warn, and so do those that are all whole numbers
+    (E8M0), which cannot refuse."""
     if q is None and s is None:
-        return _NoGradient.apply(name, call, x)
+        out = _NoGradient.apply(name, call, x)
+        if not any(t.requires_grad for t in out):
+            _warn_no_grad(name, "in whole numbers", 5)
+        return out
     _warn_no_grad(name, "in outputs that are given", 5)
     return call()
 
