@@ -673,8 +673,12 @@ def dg_moe_unpermute(y, rows, weights=None, out=None, *, layout=None):
     """Sorted rows back to their tokens: out[T][H] bf16 = sum over j of
     weights[t][j] * y[rows[t][j]] (weights None: ones), entries of rows outside
     [0, M) add nothing.  Where y or the weights require a gradient and no out is
-    given, out carries it; layout is used by that gradient alone, which clears
-    only the rows of padding where it is given and all of them where it is not."""
+    given, out carries it, for rows that name no row twice; layout is used by
+    that gradient alone, which clears only the rows of padding where it is given
+    and all of them where it is not.  A given layout belongs to rows: every row
+    with an entry of 0 or more is named in rows.  Where pairs were dropped from
+    rows after the sort, leave layout out or write -1 into their rows' entries,
+    else those rows of y's gradient are not written."""
     ops = _ops()
     if ops.wants_grad(y, weights):
         if out is None:
@@ -687,7 +691,9 @@ def dg_moe_unpermute_backward(grad, y, rows, weights=None, layout=None, grad_y=N
     """Gradients of ``dg_moe_unpermute``: grad[T][H] bf16 -> (grad_y[M][H] bf16,
     grad_weights[T][k] fp32, or None where weights is None and none is given).
     Rows of padding are zeros in grad_y where layout is given or grad_y is new;
-    a given grad_y keeps them without layout."""
+    a given grad_y keeps them without layout.  No row may be named twice in rows,
+    and a given layout belongs to rows as in ``dg_moe_unpermute``: rows with an
+    entry of 0 or more that rows does not name are not written."""
     want_weights = weights is not None or grad_weights is not None
     return _done("dg_moe_unpermute_backward", _ops().moe_unpermute_backward(
         grad, y, rows, weights, layout, grad_y, grad_weights, True, want_weights, _raw_stream(y)))

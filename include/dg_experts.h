@@ -94,11 +94,15 @@ dg_status dg_moe_unpermute(const uint16_t* y, const int32_t* rows, const float* 
 
 /* Gradients of dg_moe_unpermute.
  *   grad         [T][H] bf16 bits: the gradient of out
- *   layout       [M] int32 as dg_moe_sort makes it, or NULL
+ *   layout       [M] int32 or NULL: as dg_moe_sort makes it together with rows, so
+ *                that an entry of rows names every row whose entry here is not
+ *                negative
  *   grad_y       [M][H] bf16 bits (output) or NULL when not wanted:
  *                grad_y[rows[t][j]] = bf16(weights[t][j] * grad[t]); with layout,
- *                rows whose entry is negative are set to zero, without it rows
- *                that no entry of `rows` names are left as they were
+ *                rows whose entry is negative are set to zero; other rows that no
+ *                entry of `rows` names are left as they were (a caller that drops
+ *                a pair by writing -1 into rows writes -1 into its row's layout
+ *                entry too, or clears grad_y itself and gives no layout)
  *   grad_weights [T][k] fp32 (output) or NULL when not wanted (y may then be
  *                NULL): the sum over H of grad[t] * y[rows[t][j]], 0 where
  *                rows[t][j] is outside [0, M)
