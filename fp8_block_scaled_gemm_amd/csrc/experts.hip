@@ -117,6 +117,11 @@ __device__ __forceinline__ int expert_of(const int* offsets, int E, int r) {
     return lo;
 }
 
+// The number of lanes below this one whose bit is set.
+__device__ __forceinline__ int lanes_below(uint64_t bits) {
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(bits >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)bits, 0));
+}
+
 // layout of M rows, by `waves` waves (at most kLayoutWaves) of which this is the
 // `wave`-th, from the experts' offsets and sizes (LDS): the experts that have
 // pairs are dealt out to the waves, several to an expert's blocks where there
@@ -136,15 +141,13 @@ __device__ __forceinline__ void write_layout(const int* offsets, const int* size
         const BlockShare s = block_share(wave, waves, E);
         blocks(s.expert, s.begin, s.step);
     } else {
-        int turn = wave;  // used experts until this wave's next one
+        int before = 0;  // used experts in front of e0
         for (int e0 = 0; e0 < E; e0 += 64) {
-            uint64_t used = __ballot(e0 + lane < E && size[min(e0 + lane, E - 1)] > 0);
-            for (; turn < __popcll(used); turn += waves) {
-                uint64_t rest = used;
-                for (int i = 0; i < turn; ++i) rest &= rest - 1;
-                blocks(e0 + __builtin_ctzll(rest), 0, 1);
-            }
-            turn -= __popcll(used);
+            const bool has = e0 + lane < E && size[min(e0 + lane, E - 1)] > 0;
+            const uint64_t used = __ballot(has);
+            uint64_t mine = __ballot(has && (before + lanes_below(used)) % waves == wave);
+            for (; mine != 0; mine &= mine - 1) blocks(e0 + __builtin_ctzll(mine), 0, 1);
+            before += __popcll(used);
         }
     }
     each_rest(offsets[E], M, wave, waves, lane,
@@ -231,7 +234,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(const int3
             const uint64_t set = __ballot(bit);
             same &= bit ? set : ~set;
         }
-        const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+        const int rank = lanes_below(same);
         if (here && rank == 0) reinterpret_cast<uint8_t*>(counts + e)[wave] = (uint8_t)__popcll(same);
         __syncthreads();
         int before = 0, all = 0;
