@@ -65,7 +65,7 @@ dg_status dispatch(const uint16_t* x, const int32_t* ids, void* out, void* scale
     if (s != DG_OK) return s;
     const int64_t unit = held == dg::Held::Bf16 ? 8 : 128;
     if (H <= 0 || H % unit != 0 || H >= (int64_t(1) << 24)) return DG_ERR_SHAPE;
-    if ((s = dg::dispatch_limits(T, k, H, M, held)) != DG_OK) return s;
+    if ((s = dg::dispatch_limits(T, k, E, H, M, held)) != DG_OK) return s;
     s = check_plan(ids, rows, layout, offsets, T, k, E, M, workspace, workspace_bytes, true);
     if (s == DG_OK && T > 0) s = check_ptrs({x});
     if (s == DG_OK && M > 0) s = held == dg::Held::Bf16 ? check_ptrs({out}) : check_ptrs({out, scales});

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "dispatch_form.h"
 #include "layout_share.h"
 #include "rows_common.h"
 
@@ -272,8 +273,6 @@ dg_status launch_sort(const SortArgs& a, hipStream_t stream) {
 
 // --------------------------------------------------------------- the copies
 
-constexpr int kZeroRows = 16;  // rows that one workgroup sets to zero where they are padding
-
 // Sets rows to zero: those of the kZeroRows from r0 on whose bit is set.
 __device__ __forceinline__ void zero_rows(uint16_t* __restrict__ out, int64_t r0, uint64_t which, int64_t H, int tid) {
     for (; which != 0; which &= which - 1) {
@@ -291,18 +290,14 @@ __device__ __forceinline__ void zero_padding(uint16_t* __restrict__ out, const i
 }
 
 // Where a copy finds its tokens' rows: in memory, behind a sort of its own
-// launches, or, for few pairs, from a sort that every workgroup does for
-// itself: it counts all pairs per expert, and those before its token's.
+// launches, or, for few pairs (dispatch_form.h), from a sort that every workgroup
+// does for itself: it counts all pairs per expert, and those before its token's.
 struct SmallSort {
     const int32_t* ids;
     int32_t *rows, *layout, *offsets;  // the plan's outputs
     int64_t M;
     int P, k, E;
 };
-// As many ids as a workgroup looks through (512 tokens of 7168 to 8 of 256: 13.3
-// us against 18.7 behind a sort; 2048 tokens of 2048 to 4 of 64, 8192 ids: 19.2
-// and 16.0).
-constexpr int kSmallPairs = 4096;
 constexpr int kMaxChoices = 64;
 
 static size_t small_lds(int E) { return (size_t)(3 * E + 1) * 4; }
@@ -495,8 +490,6 @@ __global__ __launch_bounds__(256) void moe_copy_int8_kernel(const uint16_t* __re
     if constexpr (kSmall) write_plan(plan, t, true, plan_lds, row, tid);
 }
 
-static bool small_sort(int64_t T, int k) { return T > 0 && T * k <= kSmallPairs; }
-
 static int64_t zero_grid(int64_t M, Held held) { return held == Held::Bf16 ? (M + kZeroRows - 1) / kZeroRows : 0; }
 
 static int64_t copy_grid(int64_t T, int64_t H, Held held) {
@@ -507,9 +500,15 @@ static int64_t copy_grid(int64_t T, int64_t H, Held held) {
     }
 }
 
-dg_status dispatch_limits(int64_t T, int64_t k, int64_t H, int64_t M, Held held) {
-    if (small_sort(T, (int)k))  // of the quantized forms at most 2^12 tokens by 2^12 parts
-        return held != Held::Bf16 || grid_fits(T * ((H / 8 + 255) / 256) + zero_grid(M, held), 256) ? DG_OK : DG_ERR_SHAPE;
+static bool small_sort(int64_t T, int64_t k, int64_t E, int64_t H, int64_t M, Held held) {
+    return sorts_for_itself(T * k, E,
+                            held == Held::Bf16   ? small_grid_bf16(T, H, M)
+                            : held == Held::Int8 ? T
+                                                 : small_grid_fp8(T, H));
+}
+
+dg_status dispatch_limits(int64_t T, int64_t k, int64_t E, int64_t H, int64_t M, Held held) {
+    if (small_sort(T, k, E, H, M, held)) return DG_OK;  // at most kSmallSteps / 4 workgroups
     return grid_fits(copy_grid(T, H, held) + zero_grid(M, held), 256) ? DG_OK : DG_ERR_SHAPE;
 }
 
@@ -549,8 +548,9 @@ static dg_status launch_copies(const DispatchArgs& a, Held held, hipStream_t str
 }
 
 dg_status launch_dispatch(const DispatchArgs& a, Held held, hipStream_t stream) {
-    if (small_sort(a.sort.T, a.sort.k)) return launch_copies<true>(a, held, stream);
-    const dg_status st = launch_sort(a.sort, stream);
+    const SortArgs& p = a.sort;
+    if (small_sort(p.T, p.k, p.E, a.H, p.M, held)) return launch_copies<true>(a, held, stream);
+    const dg_status st = launch_sort(p, stream);
     return st != DG_OK ? st : launch_copies<false>(a, held, stream);
 }
 

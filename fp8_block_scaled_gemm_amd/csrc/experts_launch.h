@@ -31,7 +31,7 @@ struct DispatchArgs {
     int64_t H;
 };
 // DG_ERR_SHAPE where a launch of these sizes is past what a grid holds.
-dg_status dispatch_limits(int64_t T, int64_t k, int64_t H, int64_t M, Held held);
+dg_status dispatch_limits(int64_t T, int64_t k, int64_t E, int64_t H, int64_t M, Held held);
 dg_status launch_dispatch(const DispatchArgs& a, Held held, hipStream_t stream);
 
 struct UnpermuteArgs {
