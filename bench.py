@@ -89,7 +89,7 @@ def algorithmic(case):
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "fp8_block_scaled_gemm_amd", "csrc")
-    for f in ("gemm.hip", "tiles.h", "device_common.h", "launch.h"):
+    for f in ("gemm.hip", "tiles.h", "tile_order.h", "device_common.h", "launch.h"):
         h.update(open(os.path.join(csrc, f), "rb").read())
     return h.hexdigest()[:16]
 

@@ -30,10 +30,11 @@
 //     (scattered 8-byte fragment stores reach half the write bandwidth).
 //   - Workgroups are dispatched round-robin over the 8 XCDs; the tile order
 //     gives each XCD a contiguous range of tiles, grouped a few m-blocks at a
-//     time (the contiguous form: every eighth column tile), so that concurrent
-//     tiles on one XCD share A and B slabs in its L2.
+//     time (the contiguous form: of the part of the buffer in use), so that
+//     concurrent tiles on one XCD share A and B slabs in its L2.
 #include "device_common.h"
 #include "launch.h"
+#include "tile_order.h"
 #include "tiles.h"
 #include "wave_ops.h"
 
@@ -97,6 +98,33 @@ __device__ __forceinline__ bool masked_slot(int b, int m_blocks, int n_blocks, i
     return false;
 }
 
+// Contiguous form: the tile of workgroup b, in the order of tile_order.h, and its
+// block's first group.
+template <class T>
+__device__ __forceinline__ bool contiguous_tile(int b, int m_blocks, int n_blocks, int64_t G,
+                                                const int32_t* __restrict__ layout, int lane, TileInfo& ti) {
+    if (b >= m_blocks * n_blocks) return false;
+    // the ids in plain order are loaded beside the ones looked at
+    Place at = plain_place(b, n_blocks);
+    int id0 = layout[(int64_t)at.m * T::BM + lane], id1 = layout[(int64_t)at.m * T::BM + 64 + lane];
+    if (!wide_buffer(m_blocks, n_blocks)) {
+        const int look = lane < kLooks ? look_at(lane, m_blocks) : -1;
+        const int seen = look >= 0 ? layout[(int64_t)look * T::BM] : -1;
+        const uint64_t used = __ballot(seen >= 0 && seen < G);
+        const int run = used == 0 ? 0 : run_blocks(64 - __builtin_clzll(used), m_blocks);
+        if (b < run * n_blocks) {
+            at = run_place(b, run, n_blocks, T::kGroupM);
+            id0 = layout[(int64_t)at.m * T::BM + lane];
+            id1 = layout[(int64_t)at.m * T::BM + 64 + lane];
+        }
+    }
+    ti.m0 = at.m * T::BM;
+    ti.n0 = at.n * T::BN;
+    ti.valid = T::BM;
+    ti.arow0 = ti.m0;
+    return largest_group(id0, id1, G, (int)G, ti);
+}
+
 // Decode workgroup `b`'s tile; false when it is a padding slot or the tile
 // has no routed row (masked rows past masked_m, contiguous blocks of
 // padding).  Contiguous: the block's first group is the largest id in
@@ -119,19 +147,8 @@ __device__ __forceinline__ bool decode_tile(int b, int m_blocks, int n_blocks, i
         return true;
     }
     if constexpr (kForm == Form::Contiguous) {
-        // Tiles in plain order, the columns of a block first: each XCD takes every
-        // eighth column tile of all blocks.  A buffer of the most rows that any
-        // choice of experts needs holds them at its beginning, and with a run of
-        // blocks for each XCD one of the eight did all of the work (4128 rows in a
-        // buffer of 33664, 8 groups of 4096 x 7168: 884 us, 185 in this order;
-        // full buffers 1036 -> 1008 at 4096 x 7168, 545 -> 551 at 7168 x 2048).
         static_assert(T::BM == 128, "one group per 128-row block");
-        if (b >= m_blocks * n_blocks) return false;
-        ti.m0 = b / n_blocks * T::BM;
-        ti.n0 = b % n_blocks * T::BN;
-        ti.valid = T::BM;
-        ti.arow0 = ti.m0;
-        return block_group(aux, G, (int)G, lane, ti);
+        return contiguous_tile<T>(b, m_blocks, n_blocks, G, aux, lane, ti);
     }
     int tile = xcd_tile(b, m_blocks * n_blocks);
     if (tile < 0) return false;

@@ -5,10 +5,10 @@
 #include <atomic>
 
 #include "device_common.h"
+#include "tile_order.h"
+#include "wave_ops.h"
 
 namespace dg {
-
-constexpr int kNumXcds = 8;
 
 template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int GROUP_M_>
 struct TileConfig {
@@ -58,22 +58,24 @@ struct TileInfo {
     uint64_t ok0, ok1;  // contiguous form: routed-row masks, tile rows 0-63 / 64-127
 };
 
-// Contiguous form: the largest valid group id below `below` among the rows
-// of the 128-row block at ti.m0 and the masks of the rows carrying it; false
-// when there is none.  Every wave computes this from the layout itself.
-__device__ __forceinline__ bool block_group(const int32_t* __restrict__ layout, int64_t G, int below,
-                                            int lane, TileInfo& ti) {
-    const int id0 = layout[ti.m0 + lane], id1 = layout[ti.m0 + 64 + lane];
+// Contiguous form: the largest valid group id below `below` among the ids of a
+// 128-row block (lane l has those of rows l and 64 + l) and the masks of the rows
+// carrying it; false when there is none.
+__device__ __forceinline__ bool largest_group(int id0, int id1, int64_t G, int below, TileInfo& ti) {
     auto usable = [&](int id) { return id >= 0 && id < G && id < below; };
-    int gid = max(usable(id0) ? id0 : -1, usable(id1) ? id1 : -1);
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) gid = max(gid, __shfl_xor(gid, d, 64));
-    gid = __builtin_amdgcn_readfirstlane(gid);
+    const int largest = max(usable(id0) ? id0 : -1, usable(id1) ? id1 : -1);
+    const int gid = (int)wave_max((uint32_t)(largest + 1)) - 1;
     if (gid < 0) return false;
     ti.g = gid;
     ti.ok0 = __ballot(id0 == gid);
     ti.ok1 = __ballot(id1 == gid);
     return true;
+}
+
+// The same of the block at ti.m0.  Every wave computes this from the layout itself.
+__device__ __forceinline__ bool block_group(const int32_t* __restrict__ layout, int64_t G, int below,
+                                            int lane, TileInfo& ti) {
+    return largest_group(layout[ti.m0 + lane], layout[ti.m0 + 64 + lane], G, below, ti);
 }
 
 // An output tile passes through LDS in bf16 and is written back
