@@ -681,12 +681,14 @@ dg_status launch_unpermute_backward(const UnpermuteBackwardArgs& a, hipStream_t 
 
 // ------------------------------------------------------------------ the gate
 
-// sigmoid(g) for a bf16 g, off by at most 5 * 2^-24 of itself: exp(-g) is
-// 2^n 2^f with n the integer nearest to -g log2(e), and f, at most 1/2, from two
-// fused steps (g has 8 bits and the upper part of log2(e) 16, so that -g hi - n
-// is exact); then the hardware's 2^f and reciprocal (an ulp each).  With the
-// library's exponential and a full division the arithmetic, not memory, bounded
-// the gate (32768 rows of 2048 in 95 us, 57 at a copy's rate).
+// sigmoid(g) for a bf16 g, off by at most 5 * 2^-24 of itself where it is 2^-126
+// or more (g above -87.3), by less than 2^-126 below that, where it may come as 0:
+// the reciprocal has no subnormal results, and 1 + exp(-g) is infinite from 2^128 on.
+// exp(-g) is 2^n 2^f with n the integer nearest to -g log2(e), and f, at most
+// 1/2, from two fused steps (g has 8 bits and the upper part of log2(e) 16, so
+// that -g hi - n is exact); then the hardware's 2^f and reciprocal (an ulp
+// each).  With the library's exponential and a full division the arithmetic, not
+// memory, bounded the gate (32768 rows of 2048 in 95 us, 57 at a copy's rate).
 __device__ __forceinline__ float sigmoid_bf16(float g) {
     constexpr float kHi = 1.44268798828125f;          // log2(e), 16 bits
     constexpr float kLo = (float)(1.4426950408889634 - 1.44268798828125);

@@ -115,7 +115,8 @@ dg_status dg_moe_unpermute_backward(const uint16_t* grad, const uint16_t* y, con
                                     void* stream);
 
 /* The gate between an expert's two products: h = silu(gate) * up, in fp32,
- * (gate, up) = the halves of a row.
+ * (gate, up) = the halves of a row.  A sigmoid below 2^-126 (gates below -87.3)
+ * may come as 0, here and in the gradient.
  *   z       [M][2I] bf16 bits: the first product's rows
  *   layout  [M] int32, or NULL for every row: rows whose entry is negative are
  *           not computed
