@@ -34,8 +34,9 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 // 256 x 256 in 8 waves: 1.38 us a K block where the products alone (no loads, no
 // reads) take 1.05, and 11 us for a tile's beginning, its end and the launch, of
 // which the stores of one round of tiles, 34 MB, are 5.  4096 x 7168 x 2048:
-// 55 us, 2190 TOPS; 8192^3: 374 us, 2940 (the library's int8 product: 73 and 530
-// us on this card).  Tried: the FP8 kernel's two barriers a block (59.7 us);
+// 57 us, 2110 TOPS; 8192^3: 418 us, 2630 (the library's int8 product side by
+// side: 69 and 452; on a card with a higher clock 55 and 374 us here, 2940
+// TOPS).  Tried, beside 55: the FP8 kernel's two barriers a block (59.7 us);
 // four waves of 128 x 128 with 512 registers each, whose sums the compiler moves
 // about (78); 32 x 32 x 32 products (64); the loads at the second phase's
 // beginning instead of spread over it (59-60); a barrier in the middle of the
@@ -384,10 +385,11 @@ static dg_status launch_tiled(const Int8Args& a, int64_t split, hipStream_t stre
 // each, straight from memory into fragments (a lane's two operands of a block
 // are 32 bytes of its row, so that a wave reads whole lines), without a barrier
 // before the shares of the sums, which are exact in any order, are added in LDS.
-// 1 x 7168 x 2048: 5.1 us, of which a launch alone takes 2.5 and 15 MB at a
-// copy's rate 3 (17 rows in tiles: 5.5); 1 x 2112 x 7168 6.3, 8 x 4096 x 7168
-// 7.6 (20 and 32 rows in tiles: 7.8 and 8.5).  With two or four row tiles its
-// loads, 16 bytes of a row a lane, bound it (64 x 2112 x 7168: 15 and 22 us).
+// A call from a graph, in tiles in brackets: 1 x 7168 x 2048 5.2 us (5.8), of
+// which the kernel is 4.6, a launch alone 2.5 and 15 MB at a copy's rate 3;
+// 1 x 2112 x 7168 6.6 (10.0), 8 x 4096 x 7168 8.2 (10.7); 17 rows take tiles, 6.0.
+// With two or four row tiles its loads, 16 bytes of a row a lane, bound it
+// (64 x 2112 x 7168: 15 and 22 us).
 template <int CN>
 __global__ __launch_bounds__(512) void int8_few_rows_kernel(const uint8_t* __restrict__ A, const float* __restrict__ sa,
                                                             const uint8_t* __restrict__ B, const float* __restrict__ sb,
@@ -486,8 +488,8 @@ static dg_status launch_grouped(const Int8Args& a, hipStream_t stream) {
 dg_status launch_int8_gemm(const Int8Args& a, hipStream_t stream) {
     if (a.layout != nullptr) return launch_grouped(a, stream);
     const int64_t cus = device_cus();
-    // 32 columns a workgroup where they are enough for the CUs (1 x 7168 x 2048:
-    // 5.7 us, 6.3 with 16), else 16 (8 x 4096 x 7168: 7.8, 10.7 with 32)
+    // 32 columns a workgroup where they are enough for the CUs (16 x 7168 x 2048:
+    // 5.7 us, 6.6 with 16), else 16 (8 x 4096 x 7168: 8.2, 11.0 with 32)
     if (a.rows <= 16) return a.N / 32 * 8 >= cus * 7 ? launch_few_rows<2>(a, stream) : launch_few_rows<1>(a, stream);
     // The tile shape with the least estimated time: rounds of one tile a CU
     // times what a K block of the shape takes, in ns, from whole launches of
