@@ -25,9 +25,9 @@ namespace dg {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-// Pairs that one workgroup sorts by itself: one tile (256 experts: 1024 pairs
-// 8.3 us; 2048 pairs 9.5 in one workgroup, 9.0 in two and two launches, 8192
-// pairs 17.0 and 8.5).
+// Pairs that one workgroup sorts by itself: one tile.  256 experts: 1024 pairs 8.4
+// us; 2048 pairs 9.8 in one workgroup, 9.7 in two and two launches, 8192 pairs
+// 17.5 and 9.3.  16 experts: 2048 pairs 6.0 and 7.3, 8192 11.8 and 7.6.
 constexpr int kSortOnePairs = 1024;
 constexpr int kSortMaxRuns = 256;
 
@@ -463,7 +463,7 @@ __global__ __launch_bounds__(256) void moe_copy_fp8_kernel(const uint16_t* __res
 }
 
 // int8 rows: one workgroup per token, as the scale needs all of it.  4096 tokens
-// of 7168 into 8 rows each: 71 us with the sort, 4.1 TB/s.
+// of 7168 into 8 rows each: 55 us, 5.4 TB/s; 66 with the sort of 256 experts.
 template <int C, bool kSmall>
 __global__ __launch_bounds__(256) void moe_copy_int8_kernel(const uint16_t* __restrict__ x,
                                                             const int32_t* __restrict__ rows, uint8_t* __restrict__ q,

@@ -35,12 +35,12 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 // reads) take 1.05, and 11 us for a tile's beginning, its end and the launch, of
 // which the stores of one round of tiles, 34 MB, are 5.  4096 x 7168 x 2048:
 // 57 us, 2110 TOPS; 8192^3: 418 us, 2630 (the library's int8 product side by
-// side: 69 and 452; on a card with a higher clock 55 and 374 us here, 2940
-// TOPS).  Tried, beside 55: the FP8 kernel's two barriers a block (59.7 us);
-// four waves of 128 x 128 with 512 registers each, whose sums the compiler moves
-// about (78); 32 x 32 x 32 products (64); the loads at the second phase's
-// beginning instead of spread over it (59-60); a barrier in the middle of the
-// first phase for earlier loads (62).
+// side: 69 and 452; on another card 55 and 374 us here, 2940 TOPS).  Tried,
+// beside 55: the FP8 kernel's two barriers a block (59.7 us); four waves of 128 x
+// 128 with 512 registers each, whose sums the compiler moves about (78); 32 x 32
+// x 32 products (64); the loads at the second phase's beginning instead of spread
+// over it (59-60); a barrier in the middle of the first phase for earlier loads
+// (62).
 //
 // Where few tiles leave CUs without one, a K block's latency bounds a tile, and
 // PARTS groups of waves with stages of their own take every PARTS-th block each;
