@@ -13,7 +13,8 @@ Tensor conventions: e4m3 codes are ``torch.uint8`` (or
 ``torch.float8_e4m3fn``, viewed as bytes), scales ``torch.float32``, int8 codes
 ``torch.int8``, group arrays ``torch.int32``, and D is ``torch.bfloat16`` (or ``torch.uint16`` /
 ``torch.int16`` holding bf16 bit patterns).  All tensors live on the GPU,
-are contiguous and 16-byte aligned.
+are contiguous and 16-byte aligned.  A buffer that a call writes counts as
+modified in place: a recorded graph that saved it before refuses to go back.
 """
 from __future__ import annotations
 
@@ -163,12 +164,14 @@ def _device_of(*tensors) -> torch.device:
     return dev
 
 
-def _call(dev: torch.device, name: str, *args):
+def _call(dev: torch.device, written, name: str, *args):
     # the library launches on the current device, with the stream passed in
     with torch.cuda.device(dev):
         status = getattr(load_library(), name)(*args)
     if status != DG_OK:
         raise DGError(name, status)
+    # a recorded graph that saved one of these before refuses to go back with other values
+    torch.autograd.graph.increment_version(written)
 
 
 def dg_fp8_gemm_nt(A, sa, B, sb, D):
@@ -180,7 +183,7 @@ def dg_fp8_gemm_nt(A, sa, B, sb, D):
     _check(A, "A"); _check(B, "B", shape=(N, K))
     _check(sa, "sa", torch.float32, (M, KB)); _check(sb, "sb", torch.float32, (NB, KB))
     _check(D, "D", _D_TYPES, (M, N))
-    _call(_device_of(A, sa, B, sb, D), "dg_fp8_gemm_nt",
+    _call(_device_of(A, sa, B, sb, D), D, "dg_fp8_gemm_nt",
           A.data_ptr(), sa.data_ptr(), B.data_ptr(), sb.data_ptr(),
           D.data_ptr(), M, N, K, _stream_ptr(D))
     return D
@@ -196,7 +199,7 @@ def dg_fp8_gemm_nt_acc(A, sa, B, sb, C, D):
     _check(sa, "sa", torch.float32, (M, KB)); _check(sb, "sb", torch.float32, (NB, KB))
     _check(C, "C", torch.float32, (M, N))
     _check(D, "D", _D_TYPES, (M, N))
-    _call(_device_of(A, sa, B, sb, C, D), "dg_fp8_gemm_nt_acc",
+    _call(_device_of(A, sa, B, sb, C, D), D, "dg_fp8_gemm_nt_acc",
           A.data_ptr(), sa.data_ptr(), B.data_ptr(), sb.data_ptr(),
           C.data_ptr(), D.data_ptr(), M, N, K, _stream_ptr(D))
     return D
@@ -213,7 +216,7 @@ def dg_fp8_gemm_grouped_contiguous(A, sa, B, sb, D, grouped_layout):
     _check(sa, "sa", torch.float32, (M_sum, KB)); _check(sb, "sb", torch.float32, (G, NB, KB))
     _check(D, "D", _D_TYPES, (M_sum, N))
     _check(grouped_layout, "grouped_layout", torch.int32, (M_sum,))
-    _call(_device_of(A, sa, B, sb, D, grouped_layout), "dg_fp8_gemm_grouped_contiguous",
+    _call(_device_of(A, sa, B, sb, D, grouped_layout), D, "dg_fp8_gemm_grouped_contiguous",
           A.data_ptr(), sa.data_ptr(), B.data_ptr(),
           sb.data_ptr(), D.data_ptr(), grouped_layout.data_ptr(), M_sum, N, K, G, _stream_ptr(D))
     return D
@@ -230,7 +233,7 @@ def dg_fp8_gemm_grouped_masked(A, sa, B, sb, D, masked_m):
     _check(sa, "sa", torch.float32, (G, M_max, KB)); _check(sb, "sb", torch.float32, (G, NB, KB))
     _check(D, "D", _D_TYPES, (G, M_max, N))
     _check(masked_m, "masked_m", torch.int32, (G,))
-    _call(_device_of(A, sa, B, sb, D, masked_m), "dg_fp8_gemm_grouped_masked",
+    _call(_device_of(A, sa, B, sb, D, masked_m), D, "dg_fp8_gemm_grouped_masked",
           A.data_ptr(), sa.data_ptr(), B.data_ptr(),
           sb.data_ptr(), D.data_ptr(), masked_m.data_ptr(), G, M_max, N, K, _stream_ptr(D))
     return D
@@ -246,7 +249,7 @@ def dg_quantize_fp8_per_token(x, q=None, s=None):
         s = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
     q = _bytes(q, "q")
     _check(q, "q", shape=(M, K)); _check(s, "s", torch.float32, (M, K // 128))
-    _call(_device_of(x, q, s), "dg_quantize_fp8_per_token",
+    _call(_device_of(x, q, s), (q, s), "dg_quantize_fp8_per_token",
           x.data_ptr(), M, K, q.data_ptr(), s.data_ptr(),
           _stream_ptr(x))
     return q, s
@@ -262,7 +265,7 @@ def dg_quantize_fp8_per_token_bf16(x, q=None, s=None):
         s = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
     q = _bytes(q, "q")
     _check(q, "q", shape=(M, K)); _check(s, "s", torch.float32, (M, K // 128))
-    _call(_device_of(x, q, s), "dg_quantize_fp8_per_token_bf16",
+    _call(_device_of(x, q, s), (q, s), "dg_quantize_fp8_per_token_bf16",
           x.data_ptr(), M, K, q.data_ptr(), s.data_ptr(),
           _stream_ptr(x))
     return q, s
@@ -279,7 +282,7 @@ def dg_quantize_fp8_per_block(x, q=None, s=None):
         s = torch.empty((NB, K // 128), dtype=torch.float32, device=x.device)
     q = _bytes(q, "q")
     _check(q, "q", shape=(N, K)); _check(s, "s", torch.float32, (NB, K // 128))
-    _call(_device_of(x, q, s), "dg_quantize_fp8_per_block",
+    _call(_device_of(x, q, s), (q, s), "dg_quantize_fp8_per_block",
           x.data_ptr(), N, K, q.data_ptr(), s.data_ptr(),
           _stream_ptr(x))
     return q, s
@@ -301,7 +304,7 @@ def dg_fp8_gemm_nt_e8m0(A, sa, B, sb, D):
     _check(A, "A"); _check(B, "B", shape=(N, K))
     _check(sa, "sa", torch.uint8, (M, SP)); _check(sb, "sb", torch.uint8, (NB, SP))
     _check(D, "D", _D_TYPES, (M, N))
-    _call(_device_of(A, sa, B, sb, D), "dg_fp8_gemm_nt_e8m0",
+    _call(_device_of(A, sa, B, sb, D), D, "dg_fp8_gemm_nt_e8m0",
           A.data_ptr(), sa.data_ptr(), B.data_ptr(), sb.data_ptr(),
           D.data_ptr(), M, N, K, _stream_ptr(D))
     return D
@@ -317,7 +320,7 @@ def dg_fp8_gemm_grouped_contiguous_e8m0(A, sa, B, sb, D, grouped_layout):
     _check(sa, "sa", torch.uint8, (M_sum, SP)); _check(sb, "sb", torch.uint8, (G, NB, SP))
     _check(D, "D", _D_TYPES, (M_sum, N))
     _check(grouped_layout, "grouped_layout", torch.int32, (M_sum,))
-    _call(_device_of(A, sa, B, sb, D, grouped_layout), "dg_fp8_gemm_grouped_contiguous_e8m0",
+    _call(_device_of(A, sa, B, sb, D, grouped_layout), D, "dg_fp8_gemm_grouped_contiguous_e8m0",
           A.data_ptr(), sa.data_ptr(), B.data_ptr(),
           sb.data_ptr(), D.data_ptr(), grouped_layout.data_ptr(), M_sum, N, K, G, _stream_ptr(D))
     return D
@@ -333,7 +336,7 @@ def dg_fp8_gemm_grouped_masked_e8m0(A, sa, B, sb, D, masked_m):
     _check(sa, "sa", torch.uint8, (G, M_max, SP)); _check(sb, "sb", torch.uint8, (G, NB, SP))
     _check(D, "D", _D_TYPES, (G, M_max, N))
     _check(masked_m, "masked_m", torch.int32, (G,))
-    _call(_device_of(A, sa, B, sb, D, masked_m), "dg_fp8_gemm_grouped_masked_e8m0",
+    _call(_device_of(A, sa, B, sb, D, masked_m), D, "dg_fp8_gemm_grouped_masked_e8m0",
           A.data_ptr(), sa.data_ptr(), B.data_ptr(),
           sb.data_ptr(), D.data_ptr(), masked_m.data_ptr(), G, M_max, N, K, _stream_ptr(D))
     return D
@@ -351,7 +354,7 @@ def dg_quantize_fp8_per_token_e8m0(x, q=None, s=None):
         s = torch.zeros((M, SP), dtype=torch.uint8, device=x.device)
     q = _bytes(q, "q")
     _check(q, "q", shape=(M, K)); _check(s, "s", torch.uint8, (M, SP))
-    _call(_device_of(x, q, s), "dg_quantize_fp8_per_token_e8m0",
+    _call(_device_of(x, q, s), (q, s), "dg_quantize_fp8_per_token_e8m0",
           x.data_ptr(), M, K, q.data_ptr(), s.data_ptr(),
           _stream_ptr(x))
     return q, s
@@ -368,7 +371,7 @@ def dg_quantize_fp8_per_block_e8m0(x, q=None, s=None):
         s = torch.zeros((NB, SP), dtype=torch.uint8, device=x.device)
     q = _bytes(q, "q")
     _check(q, "q", shape=(N, K)); _check(s, "s", torch.uint8, (NB, SP))
-    _call(_device_of(x, q, s), "dg_quantize_fp8_per_block_e8m0",
+    _call(_device_of(x, q, s), (q, s), "dg_quantize_fp8_per_block_e8m0",
           x.data_ptr(), N, K, q.data_ptr(), s.data_ptr(),
           _stream_ptr(x))
     return q, s

@@ -162,6 +162,28 @@ PyObject* guarded(PyObject* const* a, Py_ssize_t n, F body) {
     return nullptr;
 }
 
+// A tensor that the caller gave and the call wrote.  Its version goes up, so that
+// a recorded graph that saved it before refuses to go back with other values.
+PyObject* written(PyObject* given) {
+    const at::Tensor& t = THPVariable_Unpack(given);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    return Py_NewRef(given);
+}
+
+// The tensor that a caller gave, or the new one.
+PyObject* returned(PyObject* given, const at::Tensor& t) {
+    return given == Py_None ? THPVariable_Wrap(t) : written(given);
+}
+
+// A tuple of the calls' outputs; `given` are the arguments they came as.
+PyObject* returned(std::initializer_list<std::pair<PyObject*, const at::Tensor*>> outs) {
+    PyObject* const tuple = PyTuple_New((Py_ssize_t)outs.size());
+    if (tuple == nullptr) return nullptr;
+    Py_ssize_t i = 0;
+    for (const auto& o : outs) PyTuple_SET_ITEM(tuple, i++, returned(o.first, *o.second));
+    return tuple;
+}
+
 // logits, k, ids, weights, bias, n_group, topk_group, scoring, renormalize, scale, stream
 PyObject* moe_topk(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded<11>(args, n, [](PyObject* const* a) -> PyObject* {
@@ -187,11 +209,7 @@ PyObject* moe_topk(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                       renormalize, scale, stream);
         });
         if (s != DG_OK) return PyLong_FromLong(s);
-        PyObject* const out = PyTuple_New(2);
-        if (out == nullptr) return nullptr;
-        PyTuple_SET_ITEM(out, 0, a[2] == Py_None ? THPVariable_Wrap(ids) : Py_NewRef(a[2]));
-        PyTuple_SET_ITEM(out, 1, a[3] == Py_None ? THPVariable_Wrap(weights) : Py_NewRef(a[3]));
-        return out;
+        return returned({{a[2], &ids}, {a[3], &weights}});
     });
 }
 
@@ -218,7 +236,7 @@ PyObject* moe_topk_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                                stream);
         });
         if (s != DG_OK) return PyLong_FromLong(s);
-        return a[3] == Py_None ? THPVariable_Wrap(out) : Py_NewRef(a[3]);
+        return returned(a[3], out);
     });
 }
 
@@ -259,7 +277,7 @@ PyObject* moe_mlp(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                        T, k, E, H, I, pws, ws.numel(), stream);
         });
         if (s != DG_OK) return PyLong_FromLong(s);
-        return a[9] == Py_None ? THPVariable_Wrap(y) : Py_NewRef(a[9]);
+        return returned(a[9], y);
     });
 }
 
@@ -298,22 +316,8 @@ PyObject* gemm_lora(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                             L, R, pws, ws.numel(), stream);
         });
         if (s != DG_OK) return PyLong_FromLong(s);
-        return Py_NewRef(a[5]);
+        return written(a[5]);
     });
-}
-
-// The tensor that a caller gave, or the new one.
-PyObject* returned(PyObject* given, const at::Tensor& t) {
-    return given == Py_None ? THPVariable_Wrap(t) : Py_NewRef(given);
-}
-
-// A tuple of the calls' outputs; `given` are the arguments they came as.
-PyObject* returned(std::initializer_list<std::pair<PyObject*, const at::Tensor*>> outs) {
-    PyObject* const tuple = PyTuple_New((Py_ssize_t)outs.size());
-    if (tuple == nullptr) return nullptr;
-    Py_ssize_t i = 0;
-    for (const auto& o : outs) PyTuple_SET_ITEM(tuple, i++, returned(o.first, *o.second));
-    return tuple;
 }
 
 // A pointer that may be left out: None.
@@ -581,7 +585,7 @@ PyObject* int8_gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
                            : dg_int8_gemm_nt(pA, psa, pB, psb, pD, M, N, K, stream);
         });
         if (s != DG_OK) return PyLong_FromLong(s);
-        return Py_NewRef(a[4]);
+        return written(a[4]);
     });
 }
 
